@@ -40,6 +40,19 @@ EXPORTS = (
     "gdn_chunk_fwd_noalloc",
     "gdn_recurrent_fwd",
     "gdn_selftest_wait_timeout",
+    "gdn_conv_bwd_workspace_size",
+    "gdn_conv_fwd",
+    "gdn_conv_bwd",
+    "gdn_conv_update",
+    "gdn_scan_fwd_workspace_size",
+    "gdn_scan_bwd_workspace_size",
+    "gdn_scan_saved_size",
+    "gdn_scan_fwd",
+    "gdn_scan_bwd",
+    "gdn_scan_step",
+    "gdn_norm_bwd_workspace_size",
+    "gdn_norm_fwd",
+    "gdn_norm_bwd",
 )
 
 # Size of the static scratch array behind gdn_chunk_fwd_noalloc.
@@ -52,6 +65,32 @@ class gdn_problem(ctypes.Structure):
         ("K", ctypes.c_int), ("V", ctypes.c_int), ("num_seqs", ctypes.c_int),
         ("cu_seqlens", ctypes.c_void_p), ("cu_seqlens_host", ctypes.c_void_p),
         ("dtype", ctypes.c_int), ("scale", ctypes.c_float),
+    ]
+
+
+class gdn_conv_problem(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int), ("T", ctypes.c_int), ("C", ctypes.c_int), ("W", ctypes.c_int),
+        ("num_seqs", ctypes.c_int), ("cu_seqlens", ctypes.c_void_p), ("dtype", ctypes.c_int),
+        ("silu", ctypes.c_int), ("x_stride", ctypes.c_longlong),
+    ]
+
+
+class gdn_scan_problem(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int), ("T", ctypes.c_int), ("Hq", ctypes.c_int), ("Hv", ctypes.c_int),
+        ("K", ctypes.c_int), ("V", ctypes.c_int), ("num_seqs", ctypes.c_int),
+        ("cu_seqlens", ctypes.c_void_p), ("dtype", ctypes.c_int), ("dt_dtype", ctypes.c_int),
+        ("dt_softplus", ctypes.c_int), ("x_stride", ctypes.c_longlong), ("b_stride", ctypes.c_longlong),
+        ("c_stride", ctypes.c_longlong), ("dt_stride", ctypes.c_longlong),
+    ]
+
+
+class gdn_norm_problem(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_longlong), ("D", ctypes.c_int), ("dtype", ctypes.c_int),
+        ("weight_dtype", ctypes.c_int), ("center", ctypes.c_int), ("gate_first", ctypes.c_int),
+        ("eps", ctypes.c_float),
     ]
 
 
@@ -99,6 +138,22 @@ def lib() -> ctypes.CDLL:
             L.gdn_timing_report.restype = i
             L.gdn_selftest_wait_timeout.argtypes = [ctypes.c_ulonglong, vp, vp]
             L.gdn_selftest_wait_timeout.restype = i
+            # problem, tensors, [workspace, its size], stream
+            for fn, prob, tensors, ws in (
+                    ("gdn_conv_fwd", gdn_conv_problem, 6, False), ("gdn_conv_bwd", gdn_conv_problem, 10, True),
+                    ("gdn_conv_update", gdn_conv_problem, 5, False), ("gdn_scan_fwd", gdn_scan_problem, 11, True),
+                    ("gdn_scan_bwd", gdn_scan_problem, 19, True), ("gdn_scan_step", gdn_scan_problem, 10, False),
+                    ("gdn_norm_fwd", gdn_norm_problem, 6, False), ("gdn_norm_bwd", gdn_norm_problem, 10, True)):
+                f = getattr(L, fn)
+                f.argtypes = [ctypes.POINTER(prob), *[vp] * tensors, *([vp, sz] if ws else []), vp]
+                f.restype = i
+            for fn, prob in (("gdn_conv_bwd_workspace_size", gdn_conv_problem),
+                             ("gdn_scan_fwd_workspace_size", gdn_scan_problem),
+                             ("gdn_scan_bwd_workspace_size", gdn_scan_problem),
+                             ("gdn_scan_saved_size", gdn_scan_problem),
+                             ("gdn_norm_bwd_workspace_size", gdn_norm_problem)):
+                getattr(L, fn).argtypes = [ctypes.POINTER(prob)]
+                getattr(L, fn).restype = sz
             L.gdn_version.argtypes = []
             L.gdn_version.restype = ctypes.c_char_p
             _lib = L

@@ -14,6 +14,7 @@
 #include <string>
 #include <vector>
 
+#include "gdn_host.cuh"
 #include "gdn_internal.cuh"
 
 namespace gdn {
@@ -26,18 +27,6 @@ namespace {
 constexpr int kMaxDevices = 64;
 std::mutex g_status_mutex;
 unsigned *g_status_ptr[kMaxDevices] = {};
-
-unsigned *status_ptr() {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
-    std::lock_guard<std::mutex> lock(g_status_mutex);
-    if (!g_status_ptr[dev]) {
-        void *p = nullptr;
-        if (cudaGetSymbolAddress(&p, g_status_word) != cudaSuccess) return nullptr;
-        g_status_ptr[dev] = (unsigned *)p;
-    }
-    return g_status_ptr[dev];
-}
 
 // ------------------------------------------------------------ kernel timing
 // While enabled, each launch is bracketed by two events on its stream.
@@ -61,29 +50,37 @@ cudaEvent_t take_event() {  // caller holds g_tmu
     return e;
 }
 
-struct TimedLaunch {
-    const char *name;
-    cudaStream_t st;
-    cudaEvent_t a = nullptr;
-    TimedLaunch(const char *n, cudaStream_t s) : name(n), st(s) {
-        std::lock_guard<std::mutex> lock(g_tmu);
-        if (!g_timing) return;
-        a = take_event();
-        if (a) cudaEventRecord(a, st);
-    }
-    ~TimedLaunch() {
-        if (!a) return;
-        std::lock_guard<std::mutex> lock(g_tmu);
-        cudaEvent_t b = take_event();
-        if (!b) return;
-        cudaEventRecord(b, st);
-        g_recs.push_back({name, a, b});
-    }
-};
+}  // namespace
 
-size_t align_up(size_t x, size_t a = 256) { return (x + a - 1) / a * a; }
+unsigned *status_ptr() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+    std::lock_guard<std::mutex> lock(g_status_mutex);
+    if (!g_status_ptr[dev]) {
+        void *p = nullptr;
+        if (cudaGetSymbolAddress(&p, g_status_word) != cudaSuccess) return nullptr;
+        g_status_ptr[dev] = (unsigned *)p;
+    }
+    return g_status_ptr[dev];
+}
 
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+TimedLaunch::TimedLaunch(const char *n, cudaStream_t s) : name(n), st(s) {
+    std::lock_guard<std::mutex> lock(g_tmu);
+    if (!g_timing) return;
+    a = take_event();
+    if (a) cudaEventRecord(a, st);
+}
+
+TimedLaunch::~TimedLaunch() {
+    if (!a) return;
+    std::lock_guard<std::mutex> lock(g_tmu);
+    cudaEvent_t b = take_event();
+    if (!b) return;
+    cudaEventRecord(b, st);
+    g_recs.push_back({name, a, b});
+}
+
+namespace {
 
 // Validated problem summary computed on the host.
 struct Plan {

@@ -1,0 +1,176 @@
+// gdn_layer.cuh -- declarations shared by the operators around the gated delta
+// rule: the short causal convolution, the selective state space scan and the
+// gated layer norm.
+#pragma once
+
+#include "gdn_internal.cuh"
+
+namespace gdn {
+
+// Sequences on the flattened token axis: B rows of T tokens, or N packed ones whose
+// offsets stand in cu (device, [N + 1]). A kernel clamps what it reads from cu to
+// [0, total], so an inconsistent copy never leads out of the tensors; one block of
+// each call's first kernel checks it and records GDN_ERR_DEVICE_ARG.
+struct SeqMap {
+    const int *cu;  // nullptr: no packing
+    int N, T, total;
+
+    __device__ __forceinline__ int begin(int n) const {
+        if (!cu) return n * T;
+        return min(max(cu[n], 0), total);
+    }
+    __device__ __forceinline__ int end(int n) const {
+        if (!cu) return (n + 1) * T;
+        return max(begin(n), min(max(cu[n + 1], 0), total));
+    }
+    // Sequence that token t belongs to: the last n with begin(n) <= t.
+    __device__ __forceinline__ int owner(int t) const {
+        if (!cu) return t / T;
+        int lo = 0, hi = N - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (cu[mid] <= t) lo = mid; else hi = mid - 1;
+        }
+        return lo;
+    }
+    // Slots of q tokens each, every sequence's slots one after another: sequence n's
+    // begin at begin(n) / q + n. Since ceil(len / q) <= floor(end / q) - floor(begin / q) + 1
+    // the ranges do not overlap, and total / q + N slots hold them all; the last slot of a
+    // range may be unused. No table has to be built and the host needs no copy of cu.
+    __device__ __forceinline__ int slot0(int n, int q) const {
+        if (!cu) return n * ((T + q - 1) / q);
+        return begin(n) / q + n;
+    }
+    // Sequence and slot within it of slot i; false if i is unused.
+    __device__ __forceinline__ bool slot(int i, int q, int *n, int *local) const {
+        if (!cu) {
+            const int per = (T + q - 1) / q;
+            *n = i / per;
+            *local = i - *n * per;
+            return *n < N;
+        }
+        int lo = 0, hi = N - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (slot0(mid, q) <= i) lo = mid; else hi = mid - 1;
+        }
+        *n = lo;
+        *local = i - slot0(lo, q);
+        return *local >= 0 && *local < (end(lo) - begin(lo) + q - 1) / q;
+    }
+    int slots(int q) const { return cu ? total / q + N : N * ((T + q - 1) / q); }  // upper bound (host)
+};
+
+// By one block: checks the packed offsets.
+__device__ __forceinline__ void check_cu(const SeqMap &m, unsigned *status, int tid, int threads) {
+    if (!m.cu) return;
+    bool bad = false;
+    for (int n = tid; n < m.N; n += threads) bad |= m.cu[n] < 0 || m.cu[n + 1] < m.cu[n] || m.cu[n + 1] > m.total;
+    if (tid == 0) bad |= m.cu[0] != 0 || m.cu[m.N] != m.total;
+    if (bad) set_status(status, GDN_ERR_DEVICE_ARG);
+}
+
+// kFast: single-instruction exponentials (relative error below 2^-18 for |x| < 16), enough
+// where the results are rounded to bf16; the library's expf otherwise.
+template <bool kFast>
+__device__ __forceinline__ float sigmoid(float x) {
+    return kFast ? __fdividef(1.f, 1.f + __expf(-x)) : 1.f / (1.f + expf(-x));
+}
+
+// VEC consecutive elements as fp32, by one 16-byte access (or one element).
+template <typename T, int VEC>
+__device__ __forceinline__ void load_vec(const T *p, float (&v)[VEC]) {
+    if constexpr (VEC == 1) {
+        v[0] = to_f32(*p);
+    } else if constexpr (sizeof(T) == 4) {
+        const float4 f = *reinterpret_cast<const float4 *>(p);
+        v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+    } else {
+        const uint4 u = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_vec(T *p, const float (&v)[VEC]) {
+    if constexpr (VEC == 1) {
+        *p = from_f32<T>(v[0]);
+    } else if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// --------------------------------------------------------------- convolution
+struct ConvArgs {
+    SeqMap seq;
+    int C, W, dtype;
+    bool silu;
+    long long x_stride;  // elements between tokens of x
+    const void *x, *weight, *bias, *state;  // weight [C, W]; bias [C], state [N, W-1, C] nullable
+    void *y, *final_state;                  // final nullable
+    // backward
+    const void *dy, *dfinal;                // dfinal nullable
+    void *dx, *dweight, *dbias, *dstate;    // dbias, dstate nullable
+    float *part;                            // [token blocks, W + 1, C]
+    unsigned *status;
+    cudaStream_t stream;
+};
+size_t conv_part_bytes(int total, int C, int W);
+cudaError_t launch_conv_fwd(const ConvArgs &a);
+cudaError_t launch_conv_bwd(const ConvArgs &a);
+cudaError_t launch_conv_update(const ConvArgs &a);  // state in place, seq without packing
+
+// ----------------------------------------------------------------- layer norm
+struct NormArgs {
+    long long R;
+    int D, dtype, wdtype;
+    float eps;
+    bool center, gate_first;
+    const void *x, *weight, *bias, *gate;  // bias, gate nullable
+    void *y;
+    float *stats;                          // [R, 2]: mean, 1 / standard deviation
+    const void *dy;
+    void *dx, *dgate, *dweight, *dbias;
+    float *part;                           // [blocks, 2, D]
+    cudaStream_t stream;
+};
+size_t norm_part_bytes(const NormArgs &a);
+cudaError_t launch_norm_fwd(const NormArgs &a);
+cudaError_t launch_norm_bwd(const NormArgs &a);
+
+// ----------------------------------------------------------------------- scan
+struct ScanArgs {
+    SeqMap seq;
+    int G, H, K, P, dtype, dt_dtype;
+    bool softplus;
+    long long xs, bs, cs, dts;  // elements between tokens of x, B, C, dt
+    const void *x, *dt, *B, *C;
+    const float *A, *D, *dt_bias, *h0;  // D, dt_bias, h0 nullable
+    void *y;
+    float *final_state;                 // nullable
+    // backward
+    const void *dy;
+    const float *dht;
+    void *dx, *ddt, *dB, *dC;
+    float *dA, *dD, *ddt_bias, *dh0;
+    void *saved, *ws;
+    unsigned *status;
+    cudaStream_t stream;
+};
+cudaError_t launch_scan_step(const ScanArgs &a);
+size_t scan_simt_bwd_bytes(const ScanArgs &a);
+cudaError_t launch_scan_simt_bwd(const ScanArgs &a);
+
+}  // namespace gdn

@@ -1,0 +1,245 @@
+// gdn_layer_api.cu -- C entry points of the operators around the gated delta rule:
+// the short causal convolution, the selective state space scan and the gated layer norm
+// (see include/gdn.h). Validates on the host, then launches on the caller's stream.
+#include <math.h>
+#include <stdlib.h>
+#include <string.h>
+
+#include <initializer_list>
+
+#include "gdn_host.cuh"
+#include "gdn_layer.cuh"
+
+using namespace gdn;
+
+namespace {
+
+bool known_dtype(int d) { return d == GDN_DTYPE_F32 || d == GDN_DTYPE_BF16; }
+
+size_t elem(int dtype) { return dtype == GDN_DTYPE_F32 ? 4 : 2; }
+
+bool all_aligned16(std::initializer_list<const void *> ps) {
+    for (const void *p : ps)
+        if (p && !aligned16(p)) return false;
+    return true;
+}
+
+// The sequences of a problem; GDN_OK or why they are refused.
+int make_seq(int B, int T, int num_seqs, const int32_t *cu, SeqMap *m) {
+    if (B < 1 || T < 0 || num_seqs < 0) return GDN_ERR_INVALID_ARG;
+    const long long total = (long long)B * T;
+    if (total > (1ll << 30)) return GDN_ERR_INVALID_ARG;  // token indices stay in int
+    if (num_seqs > 0 && (B != 1 || !cu)) return GDN_ERR_INVALID_ARG;
+    m->cu = num_seqs > 0 ? cu : nullptr;
+    m->N = num_seqs > 0 ? num_seqs : B;
+    m->T = T;
+    m->total = (int)total;
+    return GDN_OK;
+}
+
+int conv_args(const gdn_conv_problem *p, ConvArgs *a) {
+    if (!p) return GDN_ERR_INVALID_ARG;
+    memset(a, 0, sizeof(*a));
+    if (!known_dtype(p->dtype)) return GDN_ERR_UNSUPPORTED;
+    if (p->C < 1 || p->W < 1) return GDN_ERR_INVALID_ARG;
+    if (p->W < 2 || p->W > 4 || p->C > (1 << 20)) return GDN_ERR_UNSUPPORTED;
+    const int rc = make_seq(p->B, p->T, p->num_seqs, p->cu_seqlens, &a->seq);
+    if (rc != GDN_OK) return rc;
+    if (p->x_stride < p->C) return GDN_ERR_INVALID_ARG;
+    a->C = p->C, a->W = p->W, a->dtype = p->dtype, a->silu = p->silu != 0, a->x_stride = p->x_stride;
+    return GDN_OK;
+}
+
+int scan_args(const gdn_scan_problem *p, ScanArgs *a) {
+    if (!p) return GDN_ERR_INVALID_ARG;
+    memset(a, 0, sizeof(*a));
+    if (!known_dtype(p->dtype) || !known_dtype(p->dt_dtype)) return GDN_ERR_UNSUPPORTED;
+    if (p->dt_dtype != GDN_DTYPE_F32 && p->dt_dtype != p->dtype) return GDN_ERR_UNSUPPORTED;
+    if (p->Hq < 1 || p->Hv < 1 || p->K < 1 || p->V < 1) return GDN_ERR_INVALID_ARG;
+    if (p->Hv % p->Hq) return GDN_ERR_INVALID_ARG;
+    if ((p->K != 64 && p->K != 128) || (p->V != 64 && p->V != 128) || p->Hv > 1024) return GDN_ERR_UNSUPPORTED;
+    const int rc = make_seq(p->B, p->T, p->num_seqs, p->cu_seqlens, &a->seq);
+    if (rc != GDN_OK) return rc;
+    const int el = 16 / (int)elem(p->dtype);
+    if (p->x_stride < (long long)p->Hv * p->V || p->b_stride < (long long)p->Hq * p->K ||
+        p->c_stride < (long long)p->Hq * p->K || p->dt_stride < p->Hv || p->x_stride % el || p->b_stride % el || p->c_stride % el)
+        return GDN_ERR_INVALID_ARG;
+    a->G = p->Hq, a->H = p->Hv, a->K = p->K, a->P = p->V;
+    a->dtype = p->dtype, a->dt_dtype = p->dt_dtype, a->softplus = p->dt_softplus != 0;
+    a->xs = p->x_stride, a->bs = p->b_stride, a->cs = p->c_stride, a->dts = p->dt_stride;
+    return GDN_OK;
+}
+
+int norm_args(const gdn_norm_problem *p, NormArgs *a) {
+    if (!p) return GDN_ERR_INVALID_ARG;
+    memset(a, 0, sizeof(*a));
+    if (!known_dtype(p->dtype) || !known_dtype(p->weight_dtype)) return GDN_ERR_UNSUPPORTED;
+    if (p->weight_dtype != GDN_DTYPE_F32 && p->weight_dtype != p->dtype) return GDN_ERR_UNSUPPORTED;
+    if (p->rows < 0 || p->D < 1 || !(p->eps >= 0.f) || isinf(p->eps)) return GDN_ERR_INVALID_ARG;
+    if (p->D > (1 << 20)) return GDN_ERR_UNSUPPORTED;
+    a->R = p->rows, a->D = p->D, a->dtype = p->dtype, a->wdtype = p->weight_dtype, a->eps = p->eps;
+    a->center = p->center != 0, a->gate_first = p->gate_first != 0;
+    return GDN_OK;
+}
+
+int finish(cudaError_t e) { return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA; }
+
+bool good_ws(const void *ws, size_t have, size_t need) {
+    return have >= need && (ws || !need) && !((uintptr_t)ws & 255u);
+}
+
+}  // namespace
+
+extern "C" {
+
+// ----------------------------------------------------------------- convolution
+size_t gdn_conv_bwd_workspace_size(const gdn_conv_problem *p) {
+    ConvArgs a;
+    return conv_args(p, &a) == GDN_OK ? align_up(conv_part_bytes(a.seq.total, a.C, a.W)) : 0;
+}
+
+int gdn_conv_fwd(const gdn_conv_problem *p, const void *x, const void *weight, const void *bias, const void *initial_state,
+                 void *y, void *final_state, void *stream) {
+    ConvArgs a;
+    const int rc = conv_args(p, &a);
+    if (rc != GDN_OK) return rc;
+    if (!weight || (a.seq.total && (!x || !y))) return GDN_ERR_INVALID_ARG;
+    if (final_state && final_state == initial_state) return GDN_ERR_INVALID_ARG;
+    if (!all_aligned16({x, weight, bias, initial_state, y, final_state})) return GDN_ERR_INVALID_ARG;
+    a.x = x, a.weight = weight, a.bias = bias, a.state = initial_state, a.y = y, a.final_state = final_state;
+    a.stream = (cudaStream_t)stream;
+    if (!(a.status = status_ptr())) return GDN_ERR_CUDA;
+    TimedLaunch t("conv_fwd", a.stream);
+    return finish(launch_conv_fwd(a));
+}
+
+int gdn_conv_bwd(const gdn_conv_problem *p, const void *x, const void *weight, const void *bias, const void *initial_state,
+                 const void *dy, const void *dfinal, void *dx, void *dweight, void *dbias, void *dinitial_state, void *workspace,
+                 size_t workspace_bytes, void *stream) {
+    ConvArgs a;
+    const int rc = conv_args(p, &a);
+    if (rc != GDN_OK) return rc;
+    if (!weight || !dweight || (a.seq.total && (!x || !dy || !dx))) return GDN_ERR_INVALID_ARG;
+    if (!all_aligned16({x, weight, bias, initial_state, dy, dfinal, dx, dweight, dbias, dinitial_state})) return GDN_ERR_INVALID_ARG;
+    if (!good_ws(workspace, workspace_bytes, conv_part_bytes(a.seq.total, a.C, a.W))) return GDN_ERR_WORKSPACE;
+    a.x = x, a.weight = weight, a.bias = bias, a.state = initial_state, a.dy = dy, a.dfinal = dfinal;
+    a.dx = dx, a.dweight = dweight, a.dbias = dbias, a.dstate = dinitial_state, a.part = (float *)workspace;
+    a.stream = (cudaStream_t)stream;
+    if (!(a.status = status_ptr())) return GDN_ERR_CUDA;
+    TimedLaunch t("conv_bwd", a.stream);
+    return finish(launch_conv_bwd(a));
+}
+
+int gdn_conv_update(const gdn_conv_problem *p, const void *x, const void *weight, const void *bias, void *state, void *y,
+                    void *stream) {
+    ConvArgs a;
+    const int rc = conv_args(p, &a);
+    if (rc != GDN_OK) return rc;
+    if (p->num_seqs || !weight || !state || (a.seq.total && (!x || !y))) return GDN_ERR_INVALID_ARG;
+    if (!all_aligned16({x, weight, bias, state, y})) return GDN_ERR_INVALID_ARG;
+    a.x = x, a.weight = weight, a.bias = bias, a.state = state, a.y = y;
+    a.stream = (cudaStream_t)stream;
+    TimedLaunch t("conv_update", a.stream);
+    return finish(launch_conv_update(a));
+}
+
+// ------------------------------------------------------------------------ scan
+size_t gdn_scan_saved_size(const gdn_scan_problem *) { return 0; }
+
+size_t gdn_scan_fwd_workspace_size(const gdn_scan_problem *) { return 0; }
+
+size_t gdn_scan_bwd_workspace_size(const gdn_scan_problem *p) {
+    ScanArgs a;
+    return scan_args(p, &a) == GDN_OK ? align_up(scan_simt_bwd_bytes(a)) : 0;
+}
+
+static int scan_inputs(const gdn_scan_problem *p, ScanArgs *a, const void *x, const void *dt, const float *A, const void *B,
+                       const void *C, const float *D, const float *dt_bias, const float *h0, void *stream) {
+    const int rc = scan_args(p, a);
+    if (rc != GDN_OK) return rc;
+    if (!A || (a->seq.total && (!x || !dt || !B || !C))) return GDN_ERR_INVALID_ARG;
+    if (!all_aligned16({x, A, B, C, D, dt_bias, h0}) || ((uintptr_t)dt & (elem(a->dt_dtype) - 1))) return GDN_ERR_INVALID_ARG;
+    a->x = x, a->dt = dt, a->A = A, a->B = B, a->C = C, a->D = D, a->dt_bias = dt_bias, a->h0 = h0;
+    a->stream = (cudaStream_t)stream;
+    return GDN_OK;
+}
+
+int gdn_scan_fwd(const gdn_scan_problem *p, const void *x, const void *dt, const float *A, const void *B, const void *C,
+                 const float *D, const float *dt_bias, const float *h0, void *y, float *final_state, void *saved, void *workspace,
+                 size_t workspace_bytes, void *stream) {
+    ScanArgs a;
+    const int rc = scan_inputs(p, &a, x, dt, A, B, C, D, dt_bias, h0, stream);
+    if (rc != GDN_OK) return rc;
+    if (a.seq.total && !y) return GDN_ERR_INVALID_ARG;
+    if (!all_aligned16({y, final_state}) || ((uintptr_t)saved & 255u)) return GDN_ERR_INVALID_ARG;
+    if (!good_ws(workspace, workspace_bytes, gdn_scan_fwd_workspace_size(p))) return GDN_ERR_WORKSPACE;
+    a.y = y, a.final_state = final_state, a.saved = saved, a.ws = workspace;
+    if (!(a.status = status_ptr())) return GDN_ERR_CUDA;
+    TimedLaunch t("scan_fwd", a.stream);
+    return finish(launch_scan_step(a));
+}
+
+int gdn_scan_step(const gdn_scan_problem *p, const void *x, const void *dt, const float *A, const void *B, const void *C,
+                  const float *D, const float *dt_bias, const float *h0, void *y, float *final_state, void *stream) {
+    ScanArgs a;
+    const int rc = scan_inputs(p, &a, x, dt, A, B, C, D, dt_bias, h0, stream);
+    if (rc != GDN_OK) return rc;
+    if (a.seq.total && !y) return GDN_ERR_INVALID_ARG;
+    if (!all_aligned16({y, final_state})) return GDN_ERR_INVALID_ARG;
+    a.y = y, a.final_state = final_state;
+    if (!(a.status = status_ptr())) return GDN_ERR_CUDA;
+    TimedLaunch t("scan_step", a.stream);
+    return finish(launch_scan_step(a));
+}
+
+int gdn_scan_bwd(const gdn_scan_problem *p, const void *x, const void *dt, const float *A, const void *B, const void *C,
+                 const float *D, const float *dt_bias, const float *h0, const void *saved, const void *dy, const float *dht, void *dx,
+                 void *ddt, float *dA, void *dB, void *dC, float *dD, float *ddt_bias, float *dh0, void *workspace,
+                 size_t workspace_bytes, void *stream) {
+    ScanArgs a;
+    const int rc = scan_inputs(p, &a, x, dt, A, B, C, D, dt_bias, h0, stream);
+    if (rc != GDN_OK) return rc;
+    if (!dA || (a.seq.total && (!dy || !dx || !ddt || !dB || !dC))) return GDN_ERR_INVALID_ARG;
+    if (!all_aligned16({dy, dht, dx, ddt, dA, dB, dC, dD, ddt_bias, dh0}) || ((uintptr_t)saved & 255u)) return GDN_ERR_INVALID_ARG;
+    if (!good_ws(workspace, workspace_bytes, gdn_scan_bwd_workspace_size(p))) return GDN_ERR_WORKSPACE;
+    a.saved = const_cast<void *>(saved), a.dy = dy, a.dht = dht, a.dx = dx, a.ddt = ddt, a.dA = dA, a.dB = dB, a.dC = dC, a.dD = dD;
+    a.ddt_bias = ddt_bias, a.dh0 = dh0, a.ws = workspace;
+    if (!(a.status = status_ptr())) return GDN_ERR_CUDA;
+    TimedLaunch t("scan_bwd", a.stream);
+    return finish(launch_scan_simt_bwd(a));
+}
+
+// ------------------------------------------------------------------------ norm
+size_t gdn_norm_bwd_workspace_size(const gdn_norm_problem *p) {
+    NormArgs a;
+    return norm_args(p, &a) == GDN_OK ? align_up(norm_part_bytes(a)) : 0;
+}
+
+int gdn_norm_fwd(const gdn_norm_problem *p, const void *x, const void *weight, const void *bias, const void *gate, void *y,
+                 float *stats, void *stream) {
+    NormArgs a;
+    const int rc = norm_args(p, &a);
+    if (rc != GDN_OK) return rc;
+    if (!weight || (a.R && (!x || !y))) return GDN_ERR_INVALID_ARG;
+    if (!all_aligned16({x, weight, bias, gate, y, stats})) return GDN_ERR_INVALID_ARG;
+    a.x = x, a.weight = weight, a.bias = bias, a.gate = gate, a.y = y, a.stats = stats, a.stream = (cudaStream_t)stream;
+    TimedLaunch t("norm_fwd", a.stream);
+    return finish(launch_norm_fwd(a));
+}
+
+int gdn_norm_bwd(const gdn_norm_problem *p, const void *x, const void *weight, const void *bias, const void *gate, const void *dy,
+                 const float *stats, void *dx, void *dweight, void *dbias, void *dgate, void *workspace, size_t workspace_bytes,
+                 void *stream) {
+    NormArgs a;
+    const int rc = norm_args(p, &a);
+    if (rc != GDN_OK) return rc;
+    if (!weight || !dweight || (a.R && (!x || !dy || !stats || !dx || (gate && !dgate)))) return GDN_ERR_INVALID_ARG;
+    if (!all_aligned16({x, weight, bias, gate, dy, stats, dx, dweight, dbias, dgate})) return GDN_ERR_INVALID_ARG;
+    if (!good_ws(workspace, workspace_bytes, norm_part_bytes(a))) return GDN_ERR_WORKSPACE;
+    a.x = x, a.weight = weight, a.bias = bias, a.gate = gate, a.dy = dy, a.stats = const_cast<float *>(stats);
+    a.dx = dx, a.dweight = dweight, a.dbias = dbias, a.dgate = dgate, a.part = (float *)workspace, a.stream = (cudaStream_t)stream;
+    TimedLaunch t("norm_bwd", a.stream);
+    return finish(launch_norm_bwd(a));
+}
+
+}  // extern "C"

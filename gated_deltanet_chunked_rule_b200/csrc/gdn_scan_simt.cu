@@ -1,0 +1,431 @@
+// gdn_scan_simt.cu -- selective state space scan on the CUDA cores, token by
+// token in fp32: the decode step, and every prompt that the tensor-core kernels do not
+// take (fp32 inputs, K = 64).
+//
+// Per sequence, head (group = head / (H / G)) and token, with the state h [K, P]:
+//
+//   delta = softplus(dt + dt_bias) (or dt + dt_bias),   a = exp(delta A)
+//   h <- a h + (delta B) x^T,    y = C^T h + D x
+//
+// The gradients run the same recurrence forward once more and the adjoint one back (i_t:
+// what comes in from later tokens):
+//
+//   dC_t = h_t dy_t,   i_t = a_{t+1} g_{t+1},   g_t = C_t dy_t^T + i_t,   u_t = B_t^T g_t
+//   dx_t = delta u_t + D dy_t,   dB_t = g_t (delta x_t),   w_t = u_t.x_t
+//   d(delta A)_t = a_t <h_{t-1}, g_t> = r_t - delta_t v_t + <h_t, i_t>,   <h_t, i_t> = d(delta A)_{t+1}
+//   with r_t = C_t^T (a_t h_{t-1}) dy_t and v_t = B_t^T i_t x_t;   ddelta_t = A d(delta A)_t + w_t
+//
+// The sum over r - delta v runs to the end of the token's 16-token tile only, where <h, i> is
+// taken anew from a kept state, and neither holds the token's own product (which would cancel):
+// with it and 64 tokens the sums' rounding reached 1e-4 of dA where the decay is fast.
+//
+// One CTA per (sequence, head, 32 columns of P): warp w holds state rows 32w .. 32w+31, lane
+// l column l, in registers across the call's tokens. Tokens come in tiles of 16, the next
+// tile's loads in flight while one is worked on. The decode step is memory-bound by its
+// state, in and out once; the prompts are bound by the FMAs and shared-memory reads of the
+// 32-row columns.
+#include "gdn_layer.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kCols = 32, kTile = 16, kKeep = kTile;
+
+struct ScanP {
+    SeqMap m;
+    int G, H, P;
+    bool softplus;
+    long long xs, bs, cs, dts;
+    const float *A, *D, *dt_bias;
+};
+
+// log1p(exp(v)), or v itself above 20 (where they agree to fp32 precision).
+__device__ __forceinline__ float delta_of(float raw, bool softplus) {
+    return softplus ? (raw > 20.f ? raw : log1pf(expf(raw))) : raw;
+}
+
+// Sum over the warp's lanes of v[i], delivered to lane i.
+__device__ __forceinline__ float lane_sums(float (&v)[32], int lane) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+    }
+    return v[0];
+}
+
+// A tile of tokens in registers on its way to shared memory.
+template <typename Tin, typename Tdt, int K>
+struct Tile {
+    static constexpr int kX = kTile * kCols / K;
+    float b[kTile], c[kTile], x[kX], dy[kX], dt;
+
+    // tokens t0 + i (step dir) for i < n; Bm, Cm at this group, x at this head and slice
+    template <bool GRAD>
+    __device__ __forceinline__ void load(const ScanP &p, const Tin *x_, const Tdt *dt_, const Tin *B, const Tin *C, const Tin *dy_,
+                                         int h, int g, int c0, int t0, int dir, int n, int tid) {
+#pragma unroll
+        for (int i = 0; i < kTile; ++i) {
+            const size_t t = (size_t)(t0 + dir * i);
+            b[i] = i < n ? to_f32(B[t * p.bs + (size_t)g * K + tid]) : 0.f;
+            c[i] = i < n ? to_f32(C[t * p.cs + (size_t)g * K + tid]) : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < kX; ++j) {
+            const int i = j * (K / kCols) + tid / kCols, col = c0 + tid % kCols;
+            const size_t t = (size_t)(t0 + dir * i);
+            x[j] = i < n ? to_f32(x_[t * p.xs + (size_t)h * p.P + col]) : 0.f;
+            if (GRAD) dy[j] = i < n ? to_f32(dy_[(t * p.H + h) * p.P + col]) : 0.f;
+        }
+        dt = 0.f;
+        if (tid < n) dt = to_f32(dt_[(size_t)(t0 + dir * tid) * p.dts + h]);
+    }
+};
+
+template <int K>
+struct TileSmem {
+    float b[kTile][K], c[kTile][K], x[kTile][kCols], dy[kTile][kCols], a[kTile], d[kTile];
+    float red[kTile][K / 32][kCols], red2[kTile][K / 32][kCols];
+};
+
+// Per token, head and slice of P: r, v, w as above and x.dy.
+enum Dot { kR, kV, kWt, kXd, kDots };
+struct Dots {
+    float *at;  // [kDots][total, H, P/32]
+    size_t n;
+    __device__ __forceinline__ float *operator()(Dot d, size_t i) const { return at + d * n + i; }
+};
+
+// Sum over a row's columns of a per-warp partial; every lane of the calling warp gets it.
+template <int K>
+__device__ __forceinline__ float dot_row(const float (&red)[K / 32][kCols], float other, int lane) {
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < K / 32; ++k) v += red[k][lane];
+    v *= other;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+template <typename Tin, typename Tdt, int K, bool GRAD>
+__device__ __forceinline__ void put_tile(TileSmem<K> &s, const Tile<Tin, Tdt, K> &r, const ScanP &p, float A, float bias, int n, int tid) {
+#pragma unroll
+    for (int i = 0; i < kTile; ++i) s.b[i][tid] = r.b[i], s.c[i][tid] = r.c[i];
+#pragma unroll
+    for (int j = 0; j < Tile<Tin, Tdt, K>::kX; ++j) {
+        const int i = j * (K / kCols) + tid / kCols;
+        s.x[i][tid % kCols] = r.x[j];
+        if (GRAD) s.dy[i][tid % kCols] = r.dy[j];
+    }
+    if (tid < n) {
+        const float d = delta_of(r.dt + bias, p.softplus);
+        s.d[tid] = d;
+        s.a[tid] = expf(d * A);
+    }
+}
+
+// Forward; with GRAD instead the gradient's forward half: dC parts [total, H, P/32, K], r and
+// x.dy, kept states [slots of 16, H, K, P] at each tile's end.
+template <typename Tin, typename Tdt, int K, bool GRAD>
+__global__ void __launch_bounds__(K)
+scan_forward_kernel(ScanP p, const Tin *__restrict__ x, const Tdt *__restrict__ dt, const Tin *__restrict__ B, const Tin *__restrict__ C,
+                    const Tin *__restrict__ dy, const float *h0, Tin *__restrict__ y, float *final_state, float *__restrict__ dc_part,
+                    float *__restrict__ keep, Dots dots, unsigned *status) {
+    __shared__ TileSmem<K> s;
+    const int n = blockIdx.x, h = blockIdx.y, c0 = blockIdx.z * kCols, g = h / (p.H / p.G);
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    if (n == 0 && h == 0 && blockIdx.z == 0) check_cu(p.m, status, tid, K);
+    const int t0 = p.m.begin(n), len = p.m.end(n) - t0;
+    const size_t at = ((size_t)n * p.H + h) * K * p.P + c0 + lane;
+    float hr[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) hr[i] = h0 ? h0[at + (size_t)(32 * w + i) * p.P] : 0.f;
+    const float A = p.A[h], D = p.D ? p.D[h] : 0.f, bias = p.dt_bias ? p.dt_bias[h] : 0.f;
+    Tile<Tin, Tdt, K> r;
+    if (len) r.template load<GRAD>(p, x, dt, B, C, dy, h, g, c0, t0, 1, min(kTile, len), tid);
+    for (int q = 0; q < len; q += kTile) {
+        const int cnt = min(kTile, len - q);
+        put_tile<Tin, Tdt, K, GRAD>(s, r, p, A, bias, cnt, tid);
+        __syncthreads();
+        if (q + kTile < len) r.template load<GRAD>(p, x, dt, B, C, dy, h, g, c0, t0 + q + kTile, 1, min(kTile, len - q - kTile), tid);
+        for (int i = 0; i < cnt; ++i) {
+            const float a = s.a[i], dx = s.d[i] * s.x[i][lane];
+            float yv = 0.f;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+                const float ah = a * hr[k];
+                if (GRAD) yv = fmaf(s.c[i][32 * w + k], ah, yv);
+                hr[k] = fmaf(s.b[i][32 * w + k], dx, ah);
+                if (!GRAD) yv = fmaf(s.c[i][32 * w + k], hr[k], yv);
+            }
+            s.red[i][w][lane] = yv;
+            if (GRAD) {
+                float v[32];
+                const float d = s.dy[i][lane];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) v[k] = hr[k] * d;
+                const float sum = lane_sums(v, lane);
+                dc_part[(((size_t)(t0 + q + i) * p.H + h) * gridDim.z + blockIdx.z) * K + 32 * w + lane] = sum;
+            }
+        }
+        __syncthreads();
+        if (GRAD) {
+            for (int i = w; i < cnt; i += K / 32) {
+                const float d = s.dy[i][lane];
+                const float rv = dot_row<K>(s.red[i], d, lane);
+                float xd = s.x[i][lane] * d;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) xd += __shfl_xor_sync(0xffffffffu, xd, o);
+                const size_t e = ((size_t)(t0 + q + i) * p.H + h) * gridDim.z + blockIdx.z;
+                if (lane == 0) *dots(kR, e) = rv, *dots(kXd, e) = xd;
+            }
+            float *dst = keep + ((size_t)(p.m.slot0(n, kKeep) + q / kKeep) * p.H + h) * K * p.P + c0 + lane;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) dst[(size_t)(32 * w + k) * p.P] = hr[k];
+        } else {
+            for (int e = tid; e < cnt * kCols; e += K) {
+                const int i = e / kCols, col = e % kCols;
+                float v = 0.f;
+#pragma unroll
+                for (int k = 0; k < K / 32; ++k) v += s.red[i][k][col];
+                y[((size_t)(t0 + q + i) * p.H + h) * p.P + c0 + col] = from_f32<Tin>(fmaf(D, s.x[i][col], v));
+            }
+        }
+        __syncthreads();
+    }
+    if (final_state)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) final_state[at + (size_t)(32 * w + i) * p.P] = hr[i];
+}
+
+// The gradient's reverse half: dx, dB parts (without delta), v and w, <h, i> at the end of every
+// tile [slots, H, P/32], dh0.
+template <typename Tin, typename Tdt, int K>
+__global__ void __launch_bounds__(K)
+scan_reverse_kernel(ScanP p, const Tin *__restrict__ x, const Tdt *__restrict__ dt, const Tin *__restrict__ B, const Tin *__restrict__ C,
+                    const Tin *__restrict__ dy, const float *__restrict__ dht, const float *__restrict__ keep, Tin *__restrict__ dx,
+                    float *__restrict__ db_part, float *__restrict__ chunk_q, float *__restrict__ dh0, Dots dots) {
+    __shared__ TileSmem<K> s;
+    __shared__ float qs[K / 32];
+    const int n = blockIdx.x, h = blockIdx.y, c0 = blockIdx.z * kCols, g = h / (p.H / p.G);
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const int t0 = p.m.begin(n), len = p.m.end(n) - t0;
+    const size_t at = ((size_t)n * p.H + h) * K * p.P + c0 + lane;
+    float gr[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) gr[i] = dht ? dht[at + (size_t)(32 * w + i) * p.P] : 0.f;
+    const float A = p.A[h], D = p.D ? p.D[h] : 0.f, bias = p.dt_bias ? p.dt_bias[h] : 0.f;
+    // tiles in reverse: token i of a tile is t0 + q - i; the ragged tile comes first, so that the
+    // tiles are the forward half's
+    const int first = len ? (len - 1) % kTile + 1 : 0;
+    Tile<Tin, Tdt, K> r;
+    if (len) r.template load<true>(p, x, dt, B, C, dy, h, g, c0, t0 + len - 1, -1, first, tid);
+    int cnt = first;
+    for (int q = len - 1; q >= 0; q -= cnt, cnt = kTile) {
+        put_tile<Tin, Tdt, K, true>(s, r, p, A, bias, cnt, tid);
+        {
+            const size_t slot = p.m.slot0(n, kKeep) + q / kKeep;
+            const float *src = keep + (slot * p.H + h) * K * p.P + c0 + lane;
+            float v = 0.f;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v = fmaf(src[(size_t)(32 * w + k) * p.P], gr[k], v);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            if (lane == 0) qs[w] = v;
+            __syncthreads();
+            if (tid == 0) {
+                v = 0.f;
+#pragma unroll
+                for (int k = 0; k < K / 32; ++k) v += qs[k];
+                chunk_q[(slot * p.H + h) * gridDim.z + blockIdx.z] = v;
+            }
+        }
+        __syncthreads();
+        if (q - cnt >= 0) r.template load<true>(p, x, dt, B, C, dy, h, g, c0, t0 + q - cnt, -1, kTile, tid);
+        for (int i = 0; i < cnt; ++i) {
+            const float d = s.dy[i][lane], xv = s.x[i][lane], a = s.a[i];
+            float u = 0.f, ui = 0.f, v[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+                ui = fmaf(s.b[i][32 * w + k], gr[k], ui);
+                gr[k] = fmaf(s.c[i][32 * w + k], d, gr[k]);
+                u = fmaf(s.b[i][32 * w + k], gr[k], u);
+                v[k] = gr[k] * xv;
+                gr[k] *= a;
+            }
+            s.red[i][w][lane] = u;
+            s.red2[i][w][lane] = ui;
+            const float sum = lane_sums(v, lane);
+            db_part[(((size_t)(t0 + q - i) * p.H + h) * gridDim.z + blockIdx.z) * K + 32 * w + lane] = sum;
+        }
+        __syncthreads();
+        for (int e = tid; e < cnt * kCols; e += K) {
+            const int i = e / kCols, col = e % kCols;
+            float u = 0.f;
+#pragma unroll
+            for (int k = 0; k < K / 32; ++k) u += s.red[i][k][col];
+            dx[((size_t)(t0 + q - i) * p.H + h) * p.P + c0 + col] = from_f32<Tin>(fmaf(s.d[i], u, D * s.dy[i][col]));
+        }
+        for (int i = w; i < cnt; i += K / 32) {
+            const float xv = s.x[i][lane], wv = dot_row<K>(s.red[i], xv, lane), vv = dot_row<K>(s.red2[i], xv, lane);
+            const size_t e = ((size_t)(t0 + q - i) * p.H + h) * gridDim.z + blockIdx.z;
+            if (lane == 0) *dots(kWt, e) = wv, *dots(kV, e) = vv;
+        }
+        __syncthreads();
+    }
+    if (dh0)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) dh0[at + (size_t)(32 * w + i) * p.P] = gr[i];
+}
+
+// Per token: dC, dB summed over a group's heads.
+template <typename Tin, typename Tdt, int K>
+__global__ void __launch_bounds__(K)
+scan_gather_kernel(ScanP p, const Tdt *__restrict__ dt, const float *__restrict__ dc_part, const float *__restrict__ db_part,
+                   Tin *__restrict__ dB, Tin *__restrict__ dC) {
+    const int tid = threadIdx.x, S = p.P / kCols, r = p.H / p.G;
+    const size_t t = blockIdx.x;
+    for (int g = 0; g < p.G; ++g) {
+        float sb = 0.f, sc = 0.f;
+        for (int h = g * r; h < (g + 1) * r; ++h) {
+            float pb = 0.f;
+            for (int k = 0; k < S; ++k) {
+                pb += db_part[((t * p.H + h) * S + k) * K + tid];
+                sc += dc_part[((t * p.H + h) * S + k) * K + tid];
+            }
+            sb = fmaf(delta_of(to_f32(dt[t * p.dts + h]) + (p.dt_bias ? p.dt_bias[h] : 0.f), p.softplus), pb, sb);
+        }
+        dB[(t * p.G + g) * K + tid] = from_f32<Tin>(sb);
+        dC[(t * p.G + g) * K + tid] = from_f32<Tin>(sc);
+    }
+}
+
+// Per tile of 16 tokens and head (a thread per head): the gradients of the log decay and
+// dt, and this tile's parts [slots, 3, H] of dA, ddt_bias and dD.
+template <typename Tdt>
+__global__ void __launch_bounds__(128)
+scan_gates_kernel(ScanP p, const Tdt *__restrict__ dt, Dots dots, const float *__restrict__ chunk_q, int S,
+                  Tdt *__restrict__ ddt, float *__restrict__ part) {
+    const int h = blockIdx.y * blockDim.x + threadIdx.x, slot = blockIdx.x;
+    if (h >= p.H) return;
+    int n, local;
+    float dA = 0.f, dbias = 0.f, dD = 0.f;
+    if (p.m.slot(slot, kKeep, &n, &local)) {
+        const int t0 = p.m.begin(n) + local * kKeep, len = min(kKeep, p.m.end(n) - t0);
+        const float A = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.f;
+        float carry = 0.f;
+        for (int k = 0; k < S; ++k) carry += chunk_q[((size_t)slot * p.H + h) * S + k];
+        for (int t = t0 + len - 1; t >= t0; --t) {
+            const size_t at = (size_t)t * p.H + h;
+            const float raw = to_f32(dt[t * p.dts + h]) + bias, d = delta_of(raw, p.softplus);
+            float rv = 0.f, vv = 0.f, wv = 0.f;
+            for (int k = 0; k < S; ++k) {
+                rv += *dots(kR, at * S + k), vv += *dots(kV, at * S + k), wv += *dots(kWt, at * S + k);
+                dD += *dots(kXd, at * S + k);
+            }
+            carry += rv - d * vv;
+            dA = fmaf(d, carry, dA);
+            float g = fmaf(A, carry, wv);
+            if (p.softplus) g /= 1.f + expf(-raw);
+            ddt[at] = from_f32<Tdt>(g);
+            dbias += g;
+        }
+    }
+    part[((size_t)slot * 3 + 0) * p.H + h] = dA;
+    part[((size_t)slot * 3 + 1) * p.H + h] = dbias;
+    part[((size_t)slot * 3 + 2) * p.H + h] = dD;
+}
+
+// dA, ddt_bias, dD [H] from the slots' parts, in a fixed order.
+__global__ void __launch_bounds__(256) scan_sum_kernel(const float *__restrict__ part, int slots, int H, float *dA, float *ddt_bias, float *dD) {
+    __shared__ float red[256];
+    const int h = blockIdx.x, j = blockIdx.y;
+    float v = 0.f;
+    for (int k = threadIdx.x; k < slots; k += 256) v += part[((size_t)k * 3 + j) * H + h];
+    red[threadIdx.x] = v;
+    __syncthreads();
+    for (int o = 128; o > 0; o >>= 1) {
+        if (threadIdx.x < o) red[threadIdx.x] += red[threadIdx.x + o];
+        __syncthreads();
+    }
+    float *out = j == 0 ? dA : j == 1 ? ddt_bias : dD;
+    if (threadIdx.x == 0 && out) out[h] = red[0];
+}
+
+struct SimtWs {
+    size_t keep, dc, db, q, rw, part, total;
+};
+
+SimtWs simt_ws(const ScanArgs &a) {
+    auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+    const size_t tok = a.seq.total, S = a.P / kCols, slots = a.seq.slots(kKeep);
+    SimtWs w;
+    w.keep = 0;
+    w.dc = w.keep + up(slots * a.H * a.K * a.P * 4);
+    w.db = w.dc + up(tok * a.H * S * a.K * 4);
+    w.q = w.db + up(tok * a.H * S * a.K * 4);
+    w.rw = w.q + up(slots * a.H * S * 4);
+    w.part = w.rw + up(kDots * tok * a.H * S * 4);
+    w.total = w.part + up(slots * 3 * a.H * 4);
+    return w;
+}
+
+ScanP params(const ScanArgs &a) {
+    return ScanP{a.seq, a.G, a.H, a.P, a.softplus, a.xs, a.bs, a.cs, a.dts, a.A, a.D, a.dt_bias};
+}
+
+template <typename Tin, typename Tdt, int K>
+cudaError_t forward(const ScanArgs &a) {
+    const dim3 grid(a.seq.N, a.H, a.P / kCols);
+    scan_forward_kernel<Tin, Tdt, K, false><<<grid, K, 0, a.stream>>>(params(a), (const Tin *)a.x, (const Tdt *)a.dt, (const Tin *)a.B,
+                                                                     (const Tin *)a.C, nullptr, a.h0, (Tin *)a.y, a.final_state, nullptr,
+                                                                     nullptr, Dots{}, a.status);
+    return cudaGetLastError();
+}
+
+template <typename Tin, typename Tdt, int K>
+cudaError_t backward(const ScanArgs &a) {
+    const ScanP p = params(a);
+    const SimtWs w = simt_ws(a);
+    char *ws = (char *)a.ws;
+    float *keep = (float *)(ws + w.keep), *dc = (float *)(ws + w.dc), *db = (float *)(ws + w.db), *q = (float *)(ws + w.q);
+    float *part = (float *)(ws + w.part);
+    const Dots dots{(float *)(ws + w.rw), (size_t)a.seq.total * a.H * (a.P / kCols)};
+    const Tin *x = (const Tin *)a.x, *B = (const Tin *)a.B, *C = (const Tin *)a.C, *dy = (const Tin *)a.dy;
+    const Tdt *dt = (const Tdt *)a.dt;
+    const dim3 grid(a.seq.N, a.H, a.P / kCols);
+    const int slots = a.seq.slots(kKeep);
+    scan_forward_kernel<Tin, Tdt, K, true><<<grid, K, 0, a.stream>>>(p, x, dt, B, C, dy, a.h0, nullptr, nullptr, dc, keep, dots, a.status);
+    scan_reverse_kernel<Tin, Tdt, K><<<grid, K, 0, a.stream>>>(p, x, dt, B, C, dy, a.dht, keep, (Tin *)a.dx, db, q, a.dh0, dots);
+    if (a.seq.total)
+        scan_gather_kernel<Tin, Tdt, K><<<a.seq.total, K, 0, a.stream>>>(p, dt, dc, db, (Tin *)a.dB, (Tin *)a.dC);
+    if (slots)
+        scan_gates_kernel<Tdt><<<dim3(slots, (a.H + 127) / 128), 128, 0, a.stream>>>(p, dt, dots, q, a.P / kCols, (Tdt *)a.ddt, part);
+    scan_sum_kernel<<<dim3(a.H, 3), 256, 0, a.stream>>>(part, slots, a.H, a.dA, a.ddt_bias, a.dD);
+    return cudaGetLastError();
+}
+
+template <typename Tin, typename Tdt>
+cudaError_t by_k(const ScanArgs &a, bool bwd) {
+    if (a.K == 128) return bwd ? backward<Tin, Tdt, 128>(a) : forward<Tin, Tdt, 128>(a);
+    return bwd ? backward<Tin, Tdt, 64>(a) : forward<Tin, Tdt, 64>(a);
+}
+
+cudaError_t dispatch(const ScanArgs &a, bool bwd) {
+    if (a.seq.N == 0) return cudaSuccess;
+    if (a.dtype == GDN_DTYPE_F32) return by_k<float, float>(a, bwd);
+    return a.dt_dtype == GDN_DTYPE_F32 ? by_k<__nv_bfloat16, float>(a, bwd) : by_k<__nv_bfloat16, __nv_bfloat16>(a, bwd);
+}
+
+}  // namespace
+
+cudaError_t launch_scan_step(const ScanArgs &a) { return dispatch(a, false); }
+size_t scan_simt_bwd_bytes(const ScanArgs &a) { return simt_ws(a).total; }
+cudaError_t launch_scan_simt_bwd(const ScanArgs &a) { return dispatch(a, true); }
+
+}  // namespace gdn

@@ -181,6 +181,118 @@ int gdn_recurrent_fwd(const gdn_problem *p, const void *q, const void *k, const 
                       const float *g, const float *beta, const float *h0, void *o,
                       float *final_state, void *stream /* cudaStream_t */);
 
+/* ---------------------------------------------------------------------------
+ * Operators around the gated delta rule: the short causal convolution in front
+ * of a recurrence, the selective state space scan (the sibling recurrence with
+ * the same state, without the delta correction) and the gated layer norm behind
+ * it. Conventions as above: caller-owned device pointers on the current device,
+ * 16-byte aligned; nothing allocated or synchronised; a rejected call enqueues
+ * nothing; bf16 or fp32. Token strides (in elements) let an input be a slice of
+ * a wider tensor: token t of batch row b starts at (b*T + t) * stride. Every
+ * other tensor is contiguous. cu_seqlens is read on the device only: an
+ * inconsistent one never leads out of the tensors and is recorded as
+ * GDN_ERR_DEVICE_ARG in the status word; the results are then unspecified.
+ * Packed sequences are independent, also for non-finite values. Results do not
+ * change from run to run. The FlashQLA pages have no counterpart to these.
+ * ------------------------------------------------------------------------- */
+
+/* Short causal convolution, depthwise: per channel and sequence
+ *   pre_t = bias + sum_j weight[c][j] x_{t-W+1+j},  y_t = pre_t, or pre_t sigmoid(pre_t)
+ * with the W-1 inputs before the first token in the sequence's state row. */
+typedef struct {
+    int B, T, C, W;             /* W in {2, 3, 4}                                   */
+    int num_seqs;               /* 0: N = B; else B == 1 and cu_seqlens given       */
+    const int32_t *cu_seqlens;  /* device, [num_seqs + 1]                           */
+    int dtype;                  /* of every tensor                                  */
+    int silu;                   /* 0: none                                          */
+    long long x_stride;         /* elements between tokens of x, at least C         */
+} gdn_conv_problem;
+
+size_t gdn_conv_bwd_workspace_size(const gdn_conv_problem *p);
+
+/* x [B*T, C] (strided), weight [C, W], bias [C] or NULL, initial_state [N, W-1, C]
+ * (oldest first) or NULL (zeros), y [B*T, C], final_state [N, W-1, C] or NULL: the last
+ * W-1 inputs, initial_state's among them for a shorter sequence. The two states must
+ * not be the same buffer. */
+int gdn_conv_fwd(const gdn_conv_problem *p, const void *x, const void *weight, const void *bias,
+                 const void *initial_state, void *y, void *final_state, void *stream);
+
+/* dy, dx [B*T, C]; dfinal or NULL; dweight [C, W]; dbias, dinitial_state may be NULL. */
+int gdn_conv_bwd(const gdn_conv_problem *p, const void *x, const void *weight, const void *bias,
+                 const void *initial_state, const void *dy, const void *dfinal, void *dx, void *dweight,
+                 void *dbias, void *dinitial_state, void *workspace, size_t workspace_bytes, void *stream);
+
+/* The next T (a few) tokens of B sequences; state [B, W-1, C] is updated in place.
+ * num_seqs must be 0. */
+int gdn_conv_update(const gdn_conv_problem *p, const void *x, const void *weight, const void *bias,
+                    void *state, void *y, void *stream);
+
+/* Selective state space scan: per sequence n and head h (group h / (Hv/Hq) of B, C)
+ *   delta_t = dt_t + dt_bias (softplus of it with dt_softplus)
+ *   h_t = exp(delta_t A) h_{t-1} + delta_t B_t x_t^T,   y_t = h_t^T C_t + D x_t
+ * with a state h of [K, V] as above. x, y [B*T, Hv, V]; B, C [B*T, Hq, K]; dt [B*T, Hv];
+ * A, D, dt_bias [Hv] fp32 (D, dt_bias may be NULL: zero); states [N, Hv, K, V] fp32.
+ * delta_t A is <= 0 in practice; its running sums must stay below 80. */
+typedef struct {
+    int B, T, Hq, Hv, K, V;     /* K, V in {64, 128}; Hv a multiple of Hq, at most 1024      */
+    int num_seqs;               /* 0: N = B; else B == 1 and cu_seqlens given                */
+    const int32_t *cu_seqlens;  /* device, [num_seqs + 1]                                    */
+    int dtype;                  /* x, B, C, y and their gradients                            */
+    int dt_dtype;               /* dt and its gradient: GDN_DTYPE_F32 or dtype               */
+    int dt_softplus;
+    long long x_stride, b_stride, c_stride, dt_stride; /* elements between tokens; those of
+                                   x, B, C multiples of 16 bytes                             */
+} gdn_scan_problem;
+
+size_t gdn_scan_fwd_workspace_size(const gdn_scan_problem *p);
+size_t gdn_scan_bwd_workspace_size(const gdn_scan_problem *p);
+/* Bytes of what the forward can keep for the backward (0: nothing to keep). */
+size_t gdn_scan_saved_size(const gdn_scan_problem *p);
+
+/* h0 or NULL (zero); final_state or NULL; saved or NULL. */
+int gdn_scan_fwd(const gdn_scan_problem *p, const void *x, const void *dt, const float *A, const void *B,
+                 const void *C, const float *D, const float *dt_bias, const float *h0, void *y,
+                 float *final_state, void *saved, void *workspace, size_t workspace_bytes, void *stream);
+
+/* dy [B*T, Hv, V] and dht [N, Hv, K, V] (or NULL: zero) in; dx, ddt, dA, dB, dC out (contiguous);
+ * dD, ddt_bias, dh0 may be NULL. dB and dC sum the heads of their group. saved: what
+ * gdn_scan_fwd kept for the same problem and inputs, or NULL (recomputed). */
+int gdn_scan_bwd(const gdn_scan_problem *p, const void *x, const void *dt, const float *A, const void *B,
+                 const void *C, const float *D, const float *dt_bias, const float *h0, const void *saved,
+                 const void *dy, const float *dht, void *dx, void *ddt, float *dA, void *dB, void *dC,
+                 float *dD, float *ddt_bias, float *dh0, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Token by token, for a few tokens per sequence (decoding): the state is read and
+ * written once per call; final_state may be h0 (in place). */
+int gdn_scan_step(const gdn_scan_problem *p, const void *x, const void *dt, const float *A, const void *B,
+                  const void *C, const float *D, const float *dt_bias, const float *h0, void *y,
+                  float *final_state, void *stream);
+
+/* Layer norm over the last axis, with an optional silu gate:
+ *   u = x, or x silu(gate) with gate_first;  n = (u - mean) / sqrt(var + eps)
+ *   y = n weight + bias, times silu(gate) with a gate and without gate_first
+ * Without center the mean is taken as 0 (RMS norm). */
+typedef struct {
+    long long rows;
+    int D;
+    int dtype;        /* x, gate, y and their gradients                    */
+    int weight_dtype; /* weight, bias, their gradients: F32 or dtype       */
+    int center, gate_first;
+    float eps;
+} gdn_norm_problem;
+
+size_t gdn_norm_bwd_workspace_size(const gdn_norm_problem *p);
+
+/* x, gate (or NULL), y [rows, D]; weight, bias (or NULL) [D]; stats fp32 [rows, 2] (mean and
+ * 1/sqrt(var + eps), for the backward) or NULL. */
+int gdn_norm_fwd(const gdn_norm_problem *p, const void *x, const void *weight, const void *bias,
+                 const void *gate, void *y, float *stats, void *stream);
+
+/* stats from gdn_norm_fwd. dbias may be NULL; dgate must be given with a gate. */
+int gdn_norm_bwd(const gdn_norm_problem *p, const void *x, const void *weight, const void *bias,
+                 const void *gate, const void *dy, const float *stats, void *dx, void *dweight, void *dbias,
+                 void *dgate, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Synchronises `stream`, then returns and clears the current device's status
  * word (GDN_OK if no kernel recorded a problem since the last call). */
 int gdn_get_device_status(void *stream /* cudaStream_t */);
