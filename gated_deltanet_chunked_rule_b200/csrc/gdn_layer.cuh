@@ -45,9 +45,9 @@ struct SeqMap {
     __device__ __forceinline__ bool slot(int i, int q, int *n, int *local) const {
         if (!cu) {
             const int per = (T + q - 1) / q;
-            *n = i / per;
-            *local = i - *n * per;
-            return *n < N;
+            *n = per ? i / per : i;
+            *local = per ? i - *n * per : 0;
+            return per && *n < N;
         }
         int lo = 0, hi = N - 1;
         while (lo < hi) {

@@ -9,6 +9,7 @@
 
 #include "gdn_host.cuh"
 #include "gdn_layer.cuh"
+#include "gdn_scan_tc.cuh"
 
 using namespace gdn;
 
@@ -82,6 +83,55 @@ int norm_args(const gdn_norm_problem *p, NormArgs *a) {
     return GDN_OK;
 }
 
+// bf16 prompts take the tensor-core kernels; fp32 ones, and all under GDN_IMPL=simt, the CUDA cores.
+bool scan_on_tensor_cores(const ScanArgs &a) {
+    const char *e = getenv("GDN_IMPL");
+    return a.dtype == GDN_DTYPE_BF16 && !(e && strcmp(e, "simt") == 0);
+}
+
+// What the forward keeps: every chunk's entry state, hi then lo.
+size_t scan_saved_bytes(const ScanArgs &a) { return 2 * align_up(scan_tc::tile_bytes(a)); }
+
+// Forward workspace: segment scratch | entry states (hi; for a call that keeps none).
+struct ScanFwdLayout {
+    size_t seg, tiles, total;
+};
+ScanFwdLayout scan_fwd_layout(const ScanArgs &a) {
+    ScanFwdLayout L;
+    L.seg = 0;
+    L.tiles = L.seg + scan_tc::segment_bytes(a);
+    L.total = L.tiles + align_up(scan_tc::tile_bytes(a));
+    return L;
+}
+
+scan_tc::StateArgs state_pass(const ScanArgs &a, bool reverse, char *seg) {
+    scan_tc::StateArgs s{};
+    s.a = &a;
+    s.reverse = reverse;
+    s.chunks_per_seg = scan_tc::chunks_per_segment(a);
+    if (s.chunks_per_seg) {
+        const size_t slots = a.seq.slots(s.chunks_per_seg * scan_tc::kC);
+        s.seg = (float *)seg;
+        s.seg_gam = (float *)(seg + align_up(slots * a.H * a.P * a.K * sizeof(float)));
+    }
+    s.first = reverse ? a.dht : a.h0;
+    s.last = reverse ? a.dh0 : a.final_state;
+    return s;
+}
+
+scan_tc::Tiles tile_pair(char *at, const ScanArgs &a) {
+    return scan_tc::Tiles{(__nv_bfloat16 *)at, (__nv_bfloat16 *)(at + align_up(scan_tc::tile_bytes(a)))};
+}
+
+cudaError_t scan_fwd_tc(const ScanArgs &a) {
+    const ScanFwdLayout L = scan_fwd_layout(a);
+    char *ws = (char *)a.ws;
+    scan_tc::StateArgs s = state_pass(a, false, ws + L.seg);
+    s.tiles = a.saved ? tile_pair((char *)a.saved, a) : scan_tc::Tiles{(__nv_bfloat16 *)(ws + L.tiles), nullptr};
+    const cudaError_t e = scan_tc::launch_states(s);
+    return e != cudaSuccess ? e : scan_tc::launch_out(a, s.tiles.hi);
+}
+
 int finish(cudaError_t e) { return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA; }
 
 bool good_ws(const void *ws, size_t have, size_t need) {
@@ -144,9 +194,15 @@ int gdn_conv_update(const gdn_conv_problem *p, const void *x, const void *weight
 }
 
 // ------------------------------------------------------------------------ scan
-size_t gdn_scan_saved_size(const gdn_scan_problem *) { return 0; }
+size_t gdn_scan_saved_size(const gdn_scan_problem *p) {
+    ScanArgs a;
+    return scan_args(p, &a) == GDN_OK && scan_on_tensor_cores(a) ? scan_saved_bytes(a) : 0;
+}
 
-size_t gdn_scan_fwd_workspace_size(const gdn_scan_problem *) { return 0; }
+size_t gdn_scan_fwd_workspace_size(const gdn_scan_problem *p) {
+    ScanArgs a;
+    return scan_args(p, &a) == GDN_OK && scan_on_tensor_cores(a) ? scan_fwd_layout(a).total : 0;
+}
 
 size_t gdn_scan_bwd_workspace_size(const gdn_scan_problem *p) {
     ScanArgs a;
@@ -175,6 +231,7 @@ int gdn_scan_fwd(const gdn_scan_problem *p, const void *x, const void *dt, const
     if (!good_ws(workspace, workspace_bytes, gdn_scan_fwd_workspace_size(p))) return GDN_ERR_WORKSPACE;
     a.y = y, a.final_state = final_state, a.saved = saved, a.ws = workspace;
     if (!(a.status = status_ptr())) return GDN_ERR_CUDA;
+    if (scan_on_tensor_cores(a)) return finish(scan_fwd_tc(a));
     TimedLaunch t("scan_fwd", a.stream);
     return finish(launch_scan_step(a));
 }
