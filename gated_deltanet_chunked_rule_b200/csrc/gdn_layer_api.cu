@@ -132,6 +132,37 @@ cudaError_t scan_fwd_tc(const ScanArgs &a) {
     return e != cudaSuccess ? e : scan_tc::launch_out(a, s.tiles.hi);
 }
 
+// Backward workspace: segment scratch | exit-state gradients (hi, lo) | entry states (hi, lo; for
+// a call without `saved`) | the gradient kernel's parts.
+struct ScanBwdLayout {
+    size_t seg, g, h, grad, total;
+};
+ScanBwdLayout scan_bwd_layout(const ScanArgs &a) {
+    ScanBwdLayout L;
+    L.seg = 0;
+    L.g = L.seg + scan_tc::segment_bytes(a);
+    L.h = L.g + scan_saved_bytes(a);
+    L.grad = L.h + scan_saved_bytes(a);
+    L.total = L.grad + scan_tc::grad_bytes(a);
+    return L;
+}
+
+cudaError_t scan_bwd_tc(const ScanArgs &a) {
+    const ScanBwdLayout L = scan_bwd_layout(a);
+    char *ws = (char *)a.ws;
+    const scan_tc::Tiles g = tile_pair(ws + L.g, a), h = tile_pair(a.saved ? (char *)a.saved : ws + L.h, a);
+    if (!a.saved) {
+        scan_tc::StateArgs s = state_pass(a, false, ws + L.seg);
+        s.tiles = h;
+        const cudaError_t e = scan_tc::launch_states(s);
+        if (e != cudaSuccess) return e;
+    }
+    scan_tc::StateArgs s = state_pass(a, true, ws + L.seg);
+    s.tiles = g;
+    const cudaError_t e = scan_tc::launch_states(s);
+    return e != cudaSuccess ? e : scan_tc::launch_grad(a, h, g, ws + L.grad);
+}
+
 int finish(cudaError_t e) { return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA; }
 
 bool good_ws(const void *ws, size_t have, size_t need) {
@@ -206,7 +237,8 @@ size_t gdn_scan_fwd_workspace_size(const gdn_scan_problem *p) {
 
 size_t gdn_scan_bwd_workspace_size(const gdn_scan_problem *p) {
     ScanArgs a;
-    return scan_args(p, &a) == GDN_OK ? align_up(scan_simt_bwd_bytes(a)) : 0;
+    if (scan_args(p, &a) != GDN_OK) return 0;
+    return scan_on_tensor_cores(a) ? scan_bwd_layout(a).total : align_up(scan_simt_bwd_bytes(a));
 }
 
 static int scan_inputs(const gdn_scan_problem *p, ScanArgs *a, const void *x, const void *dt, const float *A, const void *B,
@@ -262,6 +294,7 @@ int gdn_scan_bwd(const gdn_scan_problem *p, const void *x, const void *dt, const
     a.saved = const_cast<void *>(saved), a.dy = dy, a.dht = dht, a.dx = dx, a.ddt = ddt, a.dA = dA, a.dB = dB, a.dC = dC, a.dD = dD;
     a.ddt_bias = ddt_bias, a.dh0 = dh0, a.ws = workspace;
     if (!(a.status = status_ptr())) return GDN_ERR_CUDA;
+    if (scan_on_tensor_cores(a)) return finish(scan_bwd_tc(a));
     TimedLaunch t("scan_bwd", a.stream);
     return finish(launch_scan_simt_bwd(a));
 }

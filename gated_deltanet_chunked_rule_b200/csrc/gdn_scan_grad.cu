@@ -1,0 +1,676 @@
+// gdn_scan_grad.cu -- per-chunk gradients of the tensor-core selective scan. Chunks do not
+// depend on each other: the entry states h and the exit-state gradients g' of all chunks are
+// there (bf16 pairs hi + lo from the state passes).
+//
+// Per chunk and head (rows r, s; L_rs = e^{gam_r - gam_s} for s <= r; delta = the step sizes):
+//
+//   S = C B^T,   Q = dY X^T,   W = L o S o Q
+//   dx_s = delta_s [ (L o S)^T dY + e^{gam_C - gam_s} B g' ]_s + D dY_s
+//   dC   = sum over heads  (L o Q o delta_s) B   + (e^{gam} dY) h^T
+//   dB   = sum over heads  (L o Q o delta_s)^T C + (delta e^{gam_C - gam} X) g'^T
+//   w_s  = sum_r W_rs + e^{gam_C - gam_s} x_s.(B g')_s                    (d/d delta_s, direct)
+//   dgam: the gradient of token t's log decay is what crosses t, every pair once:
+//         sum_{r >= t > s} W_rs delta_s + sum_{r >= t} e^{gam_r} dY_r.(C h)_r
+//         + sum_{s < t} delta_s e^{gam_C - gam_s} x_s.(B g')_s + e^{gam_C} <h, g'>
+//   ddelta_t = A dgam_t + w_t
+//
+// Everything that ends in an fp32 result (dA, ddt, its bias) is formed in fp32 from exact
+// products and the two-part states; sums of the crossing pairs run forward or backward
+// without cancellation, except inside one 32 x 32 diagonal block. bf16 results take one
+// rounded operand per term: L o S, the scaled rows, the summed L o Q o delta.
+//
+// A CTA (one per SM) takes one chunk and a run of units (a head's 64 columns; linear in them)
+// of one group. The products with B and C of the masked Q are taken once, after the masked
+// Qs are summed over the units in registers; dC and dB stay in tensor memory meanwhile (S |
+// one 128-column work region | dC | dB = 512 columns). Warps 0-7: a thread per row, two column
+// halves; warp 8 loads (TMA, bulk copies) and issues the products. The work region holds C h,
+// then Q, then (L o S)^T dY and B g'; e^{gam} dY h^T and X g'^T run while the mask is applied.
+#include <algorithm>
+
+#include "gdn_scan_tc.cuh"
+
+namespace gdn {
+namespace scan_tc {
+namespace {
+
+using namespace sm100;
+using namespace gdn::warp;
+
+constexpr int kThreads = 288;
+// B | C | P (L o S, at the end the summed masked Q) | x, then scaled x | dY, then dx | h hi, lo | g' hi, lo | scaled dY
+constexpr int kB = 0, kCt = 32768, kPm = 65536, kX = 98304, kY = 114688, kH = 131072, kG = 163840, kSy = 196608;
+constexpr int kVec = 212992;
+struct Vec {
+    float v[4][kC];     // e^{(start of row block w) - gam_s} for s left of block w
+    float gl[kC];       // gam (log2) relative to the row block's start
+    float delta[kC];
+    float rsum[4][kC];  // row sums of W delta per column block (strictly below the diagonal)
+    float csum[4][kC];  // column sums of W per row block (strictly below the diagonal)
+    float wdiag[kC];    // W_tt
+    float rowi[2][kC];  // e^{gam_r} dY_r.(C h)_r, per column half
+    float bt[2][kC];    // e^{gam_C - gam_s} x_s.(B g')_s, per column half
+    float tot[4][4];    // per row block: sums of rowi, delta bt, R[.][0], R[.][1]
+    float red[3][8];
+    double wsum[2][4];
+};
+constexpr int kBarsAt = kVec + (sizeof(Vec) + 15) / 16 * 16;
+constexpr int kSmem = kBarsAt + 256 + 1024;
+static_assert(kSmem <= 227 * 1024, "shared memory");
+constexpr uint32_t kColS = 0, kColR = 128, kColC = 256, kColB = 384;
+
+struct GradP {
+    Params p;
+    int run, runs;
+    const __nv_bfloat16 *h_hi, *h_lo, *g_hi, *g_lo;
+    const __nv_bfloat16 *dy;
+    __nv_bfloat16 *dx, *dB, *dC;
+    void *ddt;
+    float *part_bc;  // [2][runs][total, G, K] where runs > 1
+    float *part;     // [slots, 3, H]: dA, ddt_bias, dD
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Sum over the warp's lanes of v[i], delivered to lane i.
+__device__ __forceinline__ float lane_sums(float (&v)[32], int lane) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+    }
+    return v[0];
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+template <int K>
+__global__ void __launch_bounds__(kThreads, 1)
+scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_c,
+                 const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_dy,
+                 const __grid_constant__ CUtensorMap tm_dx, const GradP q) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align_smem_1024(smem_raw);
+    const uint32_t sb = smem_u32(smem);
+    const Params &p = q.p;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = blockIdx.y / q.runs, run = blockIdx.y % q.runs, u_first = run * q.run;
+    const int units = min(q.run, p.U - u_first);
+    int n, local;
+    if (!p.m.slot(blockIdx.x, kC, &n, &local)) {  // an unused slot adds nothing
+        for (int i = tid; i < 3 * units; i += kThreads)
+            q.part[((size_t)blockIdx.x * 3 + i / units) * p.H + p.head(g, u_first + i % units)] = 0.f;
+        return;
+    }
+    const int t0 = p.m.begin(n) + local * kC, len = min(kC, p.m.end(n) - t0);
+    const bool full_chunk = len == kC;
+    constexpr int kTile = K * kPT * 2;
+
+    Vec &vec = *reinterpret_cast<Vec *>(smem + kVec);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kBarsAt);
+    uint64_t *cb_full = bars, *h_full = bars + 1, *g_full = bars + 2, *x_full = bars + 3, *y_full = bars + 4;  // loads
+    uint64_t *ch_full = bars + 5, *q_full = bars + 6, *cd_full = bars + 7, *dx_full = bars + 8, *end_full = bars + 9;  // products
+    uint64_t *cb_ready = bars + 10, *r_free = bars + 11, *s_ready = bars + 12, *p_ready = bars + 13, *hg_read = bars + 14,
+             *dx_done = bars + 15, *m_ready = bars + 16;  // the row threads
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 17);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    if (tid == 0) {
+        for (int i = 0; i < 10; ++i) mbar_init(bars + i, 1);
+        for (int i = 10; i < 17; ++i) mbar_init(bars + i, 256);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    auto fail = [&]() {
+        *abort_flag = 1;
+        set_status(p.status, GDN_ERR_TIMEOUT);
+    };
+
+    if (warp == 8) {
+        if (lane == 0) {
+            int hs = 0, gs = 0, xs = 0, ys = 0;  // loads issued
+            auto unit_at = [&](int i) { return ((size_t)blockIdx.x * p.G * p.U + g * p.U + u_first + i) * (K * kPT); };
+            auto load_h = [&](int i) {
+                mbar_arrive_expect_tx(h_full, 2 * kTile);
+                bulk_load(smem + kH, q.h_hi + unit_at(i), kTile, h_full);
+                bulk_load(smem + kH + kTile, q.h_lo + unit_at(i), kTile, h_full);
+                ++hs;
+            };
+            auto load_g = [&](int i) {
+                mbar_arrive_expect_tx(g_full, 2 * kTile);
+                bulk_load(smem + kG, q.g_hi + unit_at(i), kTile, g_full);
+                bulk_load(smem + kG + kTile, q.g_lo + unit_at(i), kTile, g_full);
+                ++gs;
+            };
+            auto load_x = [&](int i) {
+                const int u = u_first + i;
+                mbar_arrive_expect_tx(x_full, 16384);
+                tma_load_3d(smem + kX, &tm_x, x_full, (u % p.S) * kPT, p.head(g, u), t0);
+                ++xs;
+            };
+            auto load_y = [&](int i) {
+                const int u = u_first + i;
+                mbar_arrive_expect_tx(y_full, 16384);
+                tma_load_3d(smem + kY, &tm_dy, y_full, (u % p.S) * kPT, p.head(g, u), t0);
+                ++ys;
+            };
+            mbar_arrive_expect_tx(cb_full, 2 * (K / 64) * 16384);
+            for (int j = 0; j < K / 64; ++j) {
+                tma_load_3d(smem + kCt + j * 16384, &tm_c, cb_full, 64 * j, g, t0);
+                tma_load_3d(smem + kB + j * 16384, &tm_b, cb_full, 64 * j, g, t0);
+            }
+            load_h(0), load_x(0), load_y(0), load_g(0);
+            constexpr uint32_t idQ = idesc_bf16(128, 128, false, false), idH = idesc_bf16(128, 64, false, true),
+                               idO = idesc_bf16(128, K, false, false), idX = idesc_bf16(128, 64, true, true),
+                               idC = idesc_bf16(128, K, false, true), idB = idesc_bf16(128, K, true, true);
+            bool ok = wait_bar(cb_full, 0, abort_flag) && wait_bar(cb_ready, 0, abort_flag);
+            tc_fence_after();
+            if (ok) {
+#pragma unroll
+                for (int k = 0; k < K / 16; ++k) mma_bf16(tmem + kColS, by_cols(sb + kCt, k), by_cols(sb + kB, k), idQ, k > 0);
+            }
+            for (int i = 0; i < units && ok; ++i) {
+                // C h (the work region is free: the row threads arrived on the last dx_done)
+                ok = wait_bar(h_full, i & 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 2 * (K / 16); ++k)
+                    mma_bf16(tmem + kColR, by_cols(sb + kCt, k % (K / 16)), state_by_rows<K>(sb + kH + k / (K / 16) * kTile, k % (K / 16)),
+                             idH, k > 0);
+                mma_commit(ch_full);
+                // Q = dY X^T
+                ok = wait_bar(x_full, i & 1, abort_flag) && wait_bar(y_full, i & 1, abort_flag) && wait_bar(r_free, i & 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mma_bf16(tmem + kColR, by_cols(sb + kY, k), by_cols(sb + kX, k), idQ, k > 0);
+                mma_commit(q_full);
+                // dC += (e^gam dY) h^T, dB += (delta e^{gam_C - gam} X) g'^T
+                ok = wait_bar(g_full, i & 1, abort_flag) && wait_bar(s_ready, i & 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    mma_bf16(tmem + kColC, by_cols(sb + kSy, k & 3), state_by_cols<K>(sb + kH + (k >> 2) * kTile, k & 3), idO, i + k > 0);
+                    mma_bf16(tmem + kColB, by_cols(sb + kX, k & 3), state_by_cols<K>(sb + kG + (k >> 2) * kTile, k & 3), idO, i + k > 0);
+                }
+                mma_commit(cd_full);
+                // (L o S)^T dY and B g'
+                ok = wait_bar(p_ready, i & 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) mma_bf16(tmem + kColR, by_rows(sb + kPm, k), by_rows(sb + kY, k), idX, k > 0);
+#pragma unroll
+                for (int k = 0; k < 2 * (K / 16); ++k)
+                    mma_bf16(tmem + kColR + 64, by_cols(sb + kB, k % (K / 16)),
+                             state_by_rows<K>(sb + kG + k / (K / 16) * kTile, k % (K / 16)), idH, k > 0);
+                mma_commit(dx_full);
+                const bool more = i + 1 < units;
+                ok = wait_bar(cd_full, i & 1, abort_flag);
+                if (ok && more) load_x(i + 1);
+                ok = ok && wait_bar(hg_read, i & 1, abort_flag);
+                if (ok && more) load_h(i + 1);
+                ok = ok && wait_bar(dx_full, i & 1, abort_flag);
+                if (ok && more) load_g(i + 1);
+                ok = ok && wait_bar(dx_done, i & 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                if (full_chunk) {  // dx stands in dY's tile
+                    const int u = u_first + i;
+                    tma_store_3d(&tm_dx, sb + kY, (u % p.S) * kPT, p.head(g, u), t0);
+                    bulk_commit();
+                    bulk_wait_read<0>();
+                }
+                if (more) load_y(i + 1);
+            }
+            if (ok) ok = wait_bar(m_ready, 0, abort_flag);
+            if (ok) {
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    mma_bf16(tmem + kColC, by_cols(sb + kPm, k), by_rows(sb + kB, k), idC, true);
+                    mma_bf16(tmem + kColB, by_rows(sb + kPm, k), by_rows(sb + kCt, k), idB, true);
+                }
+                mma_commit(end_full);
+            }
+            if (!ok) fail();
+            // no copy outlives the CTA
+            bool done = drain(cb_full, 0);
+            done = drain(h_full, (hs - 1) & 1) && done;
+            done = drain(g_full, (gs - 1) & 1) && done;
+            done = drain(x_full, (xs - 1) & 1) && done;
+            done = drain(y_full, (ys - 1) & 1) && done;
+            if (!done) fail();
+            bulk_wait_all();
+        }
+    } else {
+        const int wr = warp & 3, half = warp >> 2, row = wr * 32 + lane;  // row block, column half
+        const bool live = row < len;
+        const uint32_t lanes = (uint32_t)(wr * 32) << 16;
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, uint32_t parity) { ok = __all_sync(0xffffffffu, ok && wait_bar(bar, parity, abort_flag)); };
+        // rows of the next sequence: no product may meet them
+        wait(cb_full, 0);
+        if (ok && !live) {
+#pragma unroll
+            for (int j = 0; j < K / 8; ++j)
+                st_shared_v4(sb + (half ? kCt : kB) + (j >> 3) * 16384 + piece(row, j & 7), 0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async();
+        mbar_arrive(cb_ready);
+
+        float msum[2][32] = {};  // masked Q summed over the units: column blocks half, half + 2
+        float u_r = 0.f, e_r = 0.f, tail = 0.f, decay = 0.f, delta = 0.f, D = 0.f, raw = 0.f, A = 0.f;
+        float dgam = 0.f, wsum = 0.f, dD = 0.f;  // of the head so far (dgam, w: half 0)
+        int cur = -1;
+        for (int i = 0; i < units; ++i) {
+            const int u = u_first + i, h = p.head(g, u);
+            if (h != cur) {  // another head: its gates
+                raw = live ? p.raw_dt(t0 + row, h) : 0.f;
+                A = p.A[h];
+                D = p.D ? p.D[h] : 0.f;
+                delta = live ? p.delta(raw) : 0.f;
+                double x = (double)delta * A;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const double y = __shfl_up_sync(0xffffffffu, x, o);
+                    if (lane >= o) x += y;
+                }
+                if (lane == 31) vec.wsum[half][wr] = x;
+                if (half) named_sync<128>(3);
+                else named_sync<128>(2);
+                double base = 0.0, total = 0.0;
+                for (int k = 0; k < 4; ++k) {
+                    if (k < wr) base += vec.wsum[half][k];
+                    total += vec.wsum[half][k];
+                }
+                u_r = expf((float)x);
+                e_r = expf((float)(base + x));
+                tail = expf((float)(total - (base + x)));
+                decay = expf((float)total);
+                if (half == 0) {
+                    vec.gl[row] = (float)(x * 1.4426950408889634);
+                    vec.delta[row] = delta;
+                    double to = vec.wsum[0][wr] - x;
+                    for (int w = wr + 1; w < 4; ++w) {
+                        vec.v[w][row] = expf((float)to);
+                        to += vec.wsum[0][w];
+                    }
+                }
+                dgam = wsum = dD = 0.f;
+                cur = h;
+            }
+            // ---- rows of x and dY; e^gam dY for dC, dY.(C h)
+            wait(x_full, i & 1);
+            wait(y_full, i & 1);
+            uint4 xr[4];  // x, this half's 32 columns
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t at = piece(row, half * 4 + j);
+                xr[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (!live) {
+                    st_shared_v4(sb + kX + at, 0u, 0u, 0u, 0u);
+                    st_shared_v4(sb + kY + at, 0u, 0u, 0u, 0u);
+                    st_shared_v4(sb + kSy + at, 0u, 0u, 0u, 0u);
+                    continue;
+                }
+                xr[j] = ld_shared_v4(sb + kX + at);
+                const uint4 y = ld_shared_v4(sb + kY + at);
+                const uint32_t w[4] = {y.x, y.y, y.z, y.w}, v[4] = {xr[j].x, xr[j].y, xr[j].z, xr[j].w};
+                uint32_t o[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    dD = fmaf(bf_lo(w[k]), bf_lo(v[k]), fmaf(bf_hi(w[k]), bf_hi(v[k]), dD));
+                    o[k] = pack_bf16(e_r * bf_lo(w[k]), e_r * bf_hi(w[k]));
+                }
+                st_shared_v4(sb + kSy + at, o[0], o[1], o[2], o[3]);
+            }
+            wait(ch_full, i & 1);
+            tc_fence_after();
+            float ri_half = 0.f;
+            if (ok) {
+                float v[32], s = 0.f;
+                tmem_ld32(tmem + lanes + kColR + 32 * half, v);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint4 y = ld_shared_v4(sb + kY + piece(row, half * 4 + j));
+                    const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) s = fmaf(bf_lo(w[k]), v[8 * j + 2 * k], fmaf(bf_hi(w[k]), v[8 * j + 2 * k + 1], s));
+                }
+                ri_half = live ? e_r * s : 0.f;
+            }
+            fence_proxy_async();
+            tc_fence_before();
+            mbar_arrive(r_free);
+            named_sync<256>(1);  // the gate vectors are written, the last unit's sums are read
+            vec.rowi[half][row] = ri_half;
+            // ---- Q is there and x read by it: scaled x in its place
+            wait(q_full, i & 1);
+            tc_fence_after();
+            if (ok && live) {
+                const float sc = delta * tail;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t v[4] = {xr[j].x, xr[j].y, xr[j].z, xr[j].w};
+                    uint32_t o[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) o[k] = pack_bf16(sc * bf_lo(v[k]), sc * bf_hi(v[k]));
+                    st_shared_v4(sb + kX + piece(row, half * 4 + j), o[0], o[1], o[2], o[3]);
+                }
+            }
+            fence_proxy_async();
+            mbar_arrive(s_ready);
+            // ---- the mask: column blocks half and half + 2
+#pragma unroll
+            for (int bb = 0; bb < 2; ++bb) {
+                const int blk = half + 2 * bb;
+                const uint32_t pt = sb + kPm + (blk >> 1) * 16384;
+                if (blk > wr) {  // right of the diagonal
+                    if (i == 0)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) st_shared_v4(pt + piece(row, (blk & 1) * 4 + j), 0u, 0u, 0u, 0u);
+                    continue;
+                }
+                if (!ok) continue;
+                float s[32], v[32];
+                tmem_ld32(tmem + lanes + kColS + 32 * blk, s);
+                tmem_ld32(tmem + lanes + kColR + 32 * blk, v);
+                const float *dl = vec.delta + 32 * blk;
+                float rs = 0.f;
+                if (blk < wr) {
+                    const float *ve = vec.v[wr] + 32 * blk;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const float L = u_r * ve[k], d = dl[k];
+                        msum[bb][k] = fmaf(L * d, v[k], msum[bb][k]);
+                        s[k] *= L;
+                        v[k] *= s[k];
+                        rs = fmaf(v[k], d, rs);
+                    }
+                } else {
+                    const float *gl = vec.gl + 32 * blk, me = gl[lane];
+                    float diag = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const float L = k <= lane ? ex2(me - gl[k]) : 0.f, d = dl[k];
+                        msum[bb][k] = fmaf(L * d, v[k], msum[bb][k]);
+                        s[k] *= L;
+                        v[k] *= s[k];
+                        if (k == lane) diag = v[k], v[k] = 0.f;
+                        rs = fmaf(v[k], d, rs);
+                    }
+                    vec.wdiag[row] = diag;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    st_shared_v4(pt + piece(row, (blk & 1) * 4 + j), pack_bf16(s[8 * j], s[8 * j + 1]), pack_bf16(s[8 * j + 2], s[8 * j + 3]),
+                                 pack_bf16(s[8 * j + 4], s[8 * j + 5]), pack_bf16(s[8 * j + 6], s[8 * j + 7]));
+                vec.rsum[blk][row] = rs;
+                const float cs = lane_sums(v, lane);
+                vec.csum[wr][32 * blk + lane] = cs;
+            }
+            fence_proxy_async();
+            tc_fence_before();
+            mbar_arrive(p_ready);
+            // ---- <h, g'> (this thread's 32 elements)
+            float hg = 0.f;
+            wait(g_full, i & 1);
+            if (ok) {
+#pragma unroll
+                for (int j = 0; j < K * kPT / 8 / 256; ++j) {
+                    const uint32_t at = (j * 256 + tid) * 16;
+                    const uint4 a = ld_shared_v4(sb + kH + at), b = ld_shared_v4(sb + kH + kTile + at);
+                    const uint4 c = ld_shared_v4(sb + kG + at), d = ld_shared_v4(sb + kG + kTile + at);
+                    const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w}, cw[4] = {c.x, c.y, c.z, c.w},
+                                   dw[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        hg = fmaf(bf_lo(aw[k]) + bf_lo(bw[k]), bf_lo(cw[k]) + bf_lo(dw[k]), hg);
+                        hg = fmaf(bf_hi(aw[k]) + bf_hi(bw[k]), bf_hi(cw[k]) + bf_hi(dw[k]), hg);
+                    }
+                }
+            }
+            mbar_arrive(hg_read);
+            hg = warp_sum(hg);
+            if (lane == 0) vec.red[0][warp] = hg;
+            // ---- dx
+            wait(dx_full, i & 1);
+            tc_fence_after();
+            if (ok) {
+                float a[32], b[32], s = 0.f;
+                tmem_ld32(tmem + lanes + kColR + 32 * half, a);
+                tmem_ld32(tmem + lanes + kColR + 64 + 32 * half, b);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t at = sb + kY + piece(row, half * 4 + j);
+                    const uint4 y = ld_shared_v4(at);
+                    const uint32_t w[4] = {y.x, y.y, y.z, y.w}, v[4] = {xr[j].x, xr[j].y, xr[j].z, xr[j].w};
+                    uint32_t o[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int c = 8 * j + 2 * k;
+                        s = fmaf(bf_lo(v[k]), b[c], fmaf(bf_hi(v[k]), b[c + 1], s));
+                        o[k] = pack_bf16(fmaf(delta, fmaf(tail, b[c], a[c]), D * bf_lo(w[k])),
+                                         fmaf(delta, fmaf(tail, b[c + 1], a[c + 1]), D * bf_hi(w[k])));
+                    }
+                    if (full_chunk)
+                        st_shared_v4(at, o[0], o[1], o[2], o[3]);
+                    else if (live)
+                        *reinterpret_cast<uint4 *>(q.dx + ((size_t)(t0 + row) * p.H + h) * p.P + (u % p.S) * kPT + half * 32 + 8 * j) =
+                            make_uint4(o[0], o[1], o[2], o[3]);
+                }
+                vec.bt[half][row] = live ? tail * s : 0.f;
+            }
+            fence_proxy_async();
+            tc_fence_before();
+            mbar_arrive(dx_done);
+            named_sync<256>(1);  // every row's and column's sums are written
+            if (half == 0) {
+                // strictly lower W: sums of this token's row left of its block, of its column below it, and
+                // of both inside it
+                float roff = 0.f, coff = 0.f;
+                for (int k = 0; k < wr; ++k) roff += vec.rsum[k][row];
+                for (int k = wr + 1; k < 4; ++k) coff += vec.csum[k][row];
+                const float rd = vec.rsum[wr][row], cd = vec.csum[wr][row];
+                const float ri = vec.rowi[0][row] + vec.rowi[1][row], bt = vec.bt[0][row] + vec.bt[1][row];
+                float suf = ri + roff + rd - delta * cd, pre = delta * (bt + coff);
+                const float pre_own = pre;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float a = __shfl_down_sync(0xffffffffu, suf, o), b = __shfl_up_sync(0xffffffffu, pre, o);
+                    if (lane + o < 32) suf += a;
+                    if (lane >= o) pre += b;
+                }
+                const float t_ri = warp_sum(ri), t_bt = warp_sum(delta * bt);
+                const float r0 = warp_sum(wr > 0 ? vec.rsum[0][row] : 0.f), r1 = warp_sum(wr > 1 ? vec.rsum[1][row] : 0.f);
+                if (lane == 0) vec.tot[wr][0] = t_ri, vec.tot[wr][1] = t_bt, vec.tot[wr][2] = r0, vec.tot[wr][3] = r1;
+                named_sync<128>(2);
+                float dg = suf + (pre - pre_own);
+                for (int k = 0; k < 4; ++k) {
+                    if (k > wr) dg += vec.tot[k][0];
+                    if (k < wr) dg += vec.tot[k][1];
+                }
+                // pairs of blocks around this one: rows below, columns left
+                if (wr == 1) dg += vec.tot[2][2] + vec.tot[3][2];
+                if (wr == 2) dg += vec.tot[3][2] + vec.tot[3][3];
+                float e = 0.f;
+                for (int k = 0; k < 8; ++k) e += vec.red[0][k];
+                dgam += dg + decay * e;
+                wsum += cd + coff + vec.wdiag[row] + bt;
+            }
+            if (u % p.S == p.S - 1) {  // the head's last slice
+                float ddt = 0.f;
+                if (half == 0 && live) {
+                    ddt = fmaf(A, dgam, wsum);
+                    if (p.softplus) ddt /= 1.f + expf(-raw);
+                    const size_t at = (size_t)(t0 + row) * p.H + h;
+                    if (p.dt_f32) ((float *)q.ddt)[at] = ddt;
+                    else ((__nv_bfloat16 *)q.ddt)[at] = __float2bfloat16_rn(ddt);
+                }
+                const float a = warp_sum(half == 0 && live ? delta * dgam : 0.f), b = warp_sum(ddt), d = warp_sum(dD);
+                named_sync<256>(1);  // red is read
+                if (lane == 0) vec.red[0][warp] = a, vec.red[1][warp] = b, vec.red[2][warp] = d;
+                named_sync<256>(1);
+                if (tid < 3) {
+                    float v = 0.f;
+                    for (int k = 0; k < 8; ++k) v += vec.red[tid][k];
+                    q.part[((size_t)blockIdx.x * 3 + tid) * p.H + h] = v;
+                }
+                named_sync<256>(1);
+            }
+        }
+        // ---- the summed masked Q, in P's place (its last product has completed: dx_full)
+#pragma unroll
+        for (int bb = 0; bb < 2; ++bb) {
+            const int blk = half + 2 * bb;
+            if (blk > wr) continue;  // zeros stand there
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                st_shared_v4(sb + kPm + (blk >> 1) * 16384 + piece(row, (blk & 1) * 4 + j), pack_bf16(msum[bb][8 * j], msum[bb][8 * j + 1]),
+                             pack_bf16(msum[bb][8 * j + 2], msum[bb][8 * j + 3]), pack_bf16(msum[bb][8 * j + 4], msum[bb][8 * j + 5]),
+                             pack_bf16(msum[bb][8 * j + 6], msum[bb][8 * j + 7]));
+        }
+        fence_proxy_async();
+        tc_fence_before();
+        mbar_arrive(m_ready);
+        wait(end_full, 0);
+        tc_fence_after();
+        if (ok) {
+            const size_t at = ((size_t)(t0 + row) * p.G + g) * K + half * (K / 2);
+#pragma unroll
+            for (int which = 0; which < 2; ++which) {
+                __nv_bfloat16 *out = which ? q.dB : q.dC;
+                float *part = q.part_bc + ((size_t)which * q.runs + run) * p.m.total * p.G * K;
+#pragma unroll
+                for (int c = 0; c < K / 2; c += 32) {
+                    float v[32];
+                    tmem_ld32(tmem + lanes + (which ? kColB : kColC) + half * (K / 2) + c, v);
+                    if (!live) continue;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (q.runs == 1) {
+                            *reinterpret_cast<uint4 *>(out + at + c + 8 * j) =
+                                make_uint4(pack_bf16(v[8 * j], v[8 * j + 1]), pack_bf16(v[8 * j + 2], v[8 * j + 3]),
+                                           pack_bf16(v[8 * j + 4], v[8 * j + 5]), pack_bf16(v[8 * j + 6], v[8 * j + 7]));
+                        } else {
+                            *reinterpret_cast<float4 *>(part + at + c + 8 * j) = make_float4(v[8 * j], v[8 * j + 1], v[8 * j + 2], v[8 * j + 3]);
+                            *reinterpret_cast<float4 *>(part + at + c + 8 * j + 4) =
+                                make_float4(v[8 * j + 4], v[8 * j + 5], v[8 * j + 6], v[8 * j + 7]);
+                        }
+                    }
+                }
+            }
+        } else {
+            fail();
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// dC, dB from the runs' fp32 parts, in a fixed order; 4 elements per thread.
+__global__ void __launch_bounds__(256) scan_join_kernel(const float *__restrict__ part, int runs, long long n, __nv_bfloat16 *dC, __nv_bfloat16 *dB) {
+    const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= n) return;
+    const float *src = part + (long long)blockIdx.y * runs * n + i;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < runs; ++k) {
+        const float4 a = *reinterpret_cast<const float4 *>(src + k * n);
+        v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
+    }
+    *reinterpret_cast<uint2 *>((blockIdx.y ? dB : dC) + i) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+}
+
+// Units per CTA (whole heads): a CTA costs about three units' time besides them; the fewest
+// waves times that length.
+int units_per_cta(const ScanArgs &a) {
+    const int S = a.P / kPT, U = a.H / a.G * S, slots = a.seq.slots(kC), sms = sm_count();
+    double best = 1e30;
+    int pick = U;
+    for (int r = S; r <= U; r += S) {
+        const long long ctas = (long long)slots * a.G * ((U + r - 1) / r);
+        const double cost = (double)((ctas + sms - 1) / sms) * (r + 3);
+        if (cost < best) best = cost, pick = r;
+    }
+    return pick;
+}
+
+int runs_of(const ScanArgs &a) {
+    const int U = a.H / a.G * (a.P / kPT), r = units_per_cta(a);
+    return (U + r - 1) / r;
+}
+
+template <int K>
+cudaError_t run(const ScanArgs &a, const Tiles &h, const Tiles &gr, char *ws) {
+    GradP q{};
+    q.p = params(a);
+    q.run = units_per_cta(a), q.runs = runs_of(a);
+    q.h_hi = h.hi, q.h_lo = h.lo, q.g_hi = gr.hi, q.g_lo = gr.lo;
+    q.dx = (__nv_bfloat16 *)a.dx, q.dB = (__nv_bfloat16 *)a.dB, q.dC = (__nv_bfloat16 *)a.dC;
+    q.dy = (const __nv_bfloat16 *)a.dy, q.ddt = a.ddt;
+    const int slots = a.seq.total ? a.seq.slots(kC) : 0;
+    q.part = (float *)ws;
+    q.part_bc = (float *)(ws + align_up((size_t)slots * 3 * a.H * 4));
+    if (slots) {
+        CUtensorMap mb, mc, mx, my, mdx;
+        const long long dense = (long long)a.H * a.P;
+        if (!token_map(&mb, a.B, K, a.G, a.bs, a.seq.total) || !token_map(&mc, a.C, K, a.G, a.cs, a.seq.total) ||
+            !token_map(&mx, a.x, a.P, a.H, a.xs, a.seq.total) || !token_map(&my, a.dy, a.P, a.H, dense, a.seq.total) ||
+            !token_map(&mdx, a.dx, a.P, a.H, dense, a.seq.total))
+            return cudaErrorInvalidValue;
+        auto kernel = scan_grad_kernel<K>;
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        {
+            TimedLaunch t("scan_grad", a.stream);
+            kernel<<<dim3(slots, a.G * q.runs), kThreads, kSmem, a.stream>>>(mb, mc, mx, my, mdx, q);
+        }
+        if (q.runs > 1) {
+            TimedLaunch t("scan_join", a.stream);
+            const long long n = (long long)a.seq.total * a.G * K;
+            scan_join_kernel<<<dim3((unsigned)((n / 4 + 255) / 256), 2), 256, 0, a.stream>>>(q.part_bc, q.runs, n, q.dC, q.dB);
+        }
+    }
+    TimedLaunch t("scan_sum", a.stream);
+    return launch_scan_sum(q.part, slots, a);
+}
+
+}  // namespace
+
+size_t grad_bytes(const ScanArgs &a) {
+    if (!a.seq.total) return 256;
+    const int runs = runs_of(a);
+    return align_up((size_t)a.seq.slots(kC) * 3 * a.H * 4) + (runs > 1 ? align_up(2ull * runs * a.seq.total * a.G * a.K * 4) : 0);
+}
+
+cudaError_t launch_grad(const ScanArgs &a, const Tiles &h, const Tiles &g, char *ws) {
+    return a.K == 128 ? run<128>(a, h, g, ws) : run<64>(a, h, g, ws);
+}
+
+}  // namespace scan_tc
+}  // namespace gdn

@@ -406,8 +406,7 @@ cudaError_t backward(const ScanArgs &a) {
         scan_gather_kernel<Tin, Tdt, K><<<a.seq.total, K, 0, a.stream>>>(p, dt, dc, db, (Tin *)a.dB, (Tin *)a.dC);
     if (slots)
         scan_gates_kernel<Tdt><<<dim3(slots, (a.H + 127) / 128), 128, 0, a.stream>>>(p, dt, dots, q, a.P / kCols, (Tdt *)a.ddt, part);
-    scan_sum_kernel<<<dim3(a.H, 3), 256, 0, a.stream>>>(part, slots, a.H, a.dA, a.ddt_bias, a.dD);
-    return cudaGetLastError();
+    return launch_scan_sum(part, slots, a);
 }
 
 template <typename Tin, typename Tdt>
@@ -423,6 +422,11 @@ cudaError_t dispatch(const ScanArgs &a, bool bwd) {
 }
 
 }  // namespace
+
+cudaError_t launch_scan_sum(const float *part, int slots, const ScanArgs &a) {
+    scan_sum_kernel<<<dim3(a.H, 3), 256, 0, a.stream>>>(part, slots, a.H, a.dA, a.ddt_bias, a.dD);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_scan_step(const ScanArgs &a) { return dispatch(a, false); }
 size_t scan_simt_bwd_bytes(const ScanArgs &a) { return simt_ws(a).total; }

@@ -125,5 +125,9 @@ size_t segment_bytes(const ScanArgs &a);
 
 cudaError_t launch_out(const ScanArgs &a, const __nv_bfloat16 *tiles_hi);
 
+// Gradients from every chunk's entry state h and exit gradient g; scratch of grad_bytes.
+size_t grad_bytes(const ScanArgs &a);
+cudaError_t launch_grad(const ScanArgs &a, const Tiles &h, const Tiles &g, char *ws);
+
 }  // namespace scan_tc
 }  // namespace gdn

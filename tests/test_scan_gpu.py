@@ -141,6 +141,15 @@ def test_batch_of_slices_without_saved(gdn, dtype, slow):
         assert torch.equal(got[k], kept[k]), k
 
 
+@pytest.mark.parametrize("lens,packed", [([1100], False), ([1025, 1, 0, 70, 1300], True), ([640] * 2, False), ([1536], True)])
+@pytest.mark.parametrize("K,P,H", [(128, 64, 1), (64, 128, 2)])
+def test_sequences_cut_into_segments(gdn, lens, packed, K, P, H):
+    # few heads and many chunks: state passes over segments of a sequence, composed; ends on and
+    # off the segments' borders, beside short and empty sequences
+    v = make(lens, H, 1, K, P, torch.bfloat16, seed=21, packed=packed, slow=True)
+    verify(v, lens, True, train(gdn, v))
+
+
 def test_large_and_small_steps(gdn):
     # delta near 0 and above softplus's switch; decays that underflow to 0
     for dtype in (torch.float32, torch.bfloat16):
