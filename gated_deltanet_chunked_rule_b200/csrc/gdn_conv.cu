@@ -9,11 +9,13 @@
 //
 // Memory-bound: forward reads x and writes y, backward reads x and dy and writes dx. A
 // warp owns 32 x 16 bytes of channels and a run of tokens; the last W-1 inputs stay in
-// registers, so that every row is read once per run (plus W-1 rows of overlap), eight
-// rows in flight. The backward recomputes pre, and holds the unfinished dx of the last
-// W-1 tokens in registers the same way. The weight's gradient sums in fp32: over a run in
+// registers, so that every row is read once per run (plus W-1 rows of overlap). Rows come in
+// batches of eight (four in the backward, with dy's) that are loaded together and worked off
+// channel by channel without a branch while they lie in one sequence; a batch that meets a
+// border goes row by row. The backward recomputes pre, and holds dpre of the last W-1 tokens. The weight's gradient sums in fp32: over a run in
 // registers, over a block's runs in shared memory, over blocks by a second kernel in a
 // fixed order.
+#include "gdn_host.cuh"
 #include "gdn_layer.cuh"
 
 namespace gdn {
@@ -21,7 +23,7 @@ namespace {
 
 constexpr int kWarps = 4;   // runs per block
 constexpr int kRunF = 32;   // tokens of a forward run
-constexpr int kRunB = 64;   // tokens of a backward run
+constexpr int kRunB = 32;   // tokens of a backward run
 constexpr int kAhead = 8;   // rows loaded together
 
 struct ConvP {
@@ -31,34 +33,105 @@ struct ConvP {
     long long xs;
 };
 
+// VEC consecutive channels of a row as loaded: four words of one or two elements (or one element).
+template <typename T, int VEC>
+struct Pack {
+    static constexpr int kWords = VEC == 1 ? 1 : 4, kPer = VEC / kWords;
+    uint32_t w[kWords];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) w[k] = 0;
+    }
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (VEC == 1) {
+            w[0] = __float_as_uint(to_f32(*p));
+        } else {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p);
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        }
+    }
+    __device__ __forceinline__ void store(T *p) const {
+        if constexpr (VEC == 1) *p = from_f32<T>(__uint_as_float(w[0]));
+        else *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ float get(int k, int e) const {
+        if constexpr (kPer == 1) return __uint_as_float(w[k]);
+        return __uint_as_float(e ? w[k] & 0xffff0000u : w[k] << 16);
+    }
+    __device__ __forceinline__ void put(int k, const float (&v)[kPer]) {
+        if constexpr (kPer == 1) {
+            w[k] = __float_as_uint(v[0]);
+        } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[0], v[1]);
+            w[k] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+    }
+};
+
+// The taps and bias of VEC channels: contiguous in memory, 16-byte pieces where VEC > 1.
+template <typename T, int VEC, int W>
+struct Taps {
+    using P = Pack<T, VEC>;
+    P w[W], b;
+    __device__ __forceinline__ void load(const T *weight, const T *bias, int c) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) w[j].load(weight + (size_t)c * W + j * VEC);
+        b.zero();
+        if (bias) b.load(bias + c);
+    }
+    // tap j of element e of word k: element (k * kPer + e) * W + j of the piece sequence
+    __device__ __forceinline__ float tap(int k, int e, int j) const {
+        const int i = (k * P::kPer + e) * W + j;
+        return w[i / VEC].get(i % VEC / P::kPer, i % P::kPer);
+    }
+};
+
 // Input row i of sequence n counted from its first state row: the state's rows, then x.
 template <typename T, int VEC, int W>
-__device__ __forceinline__ void seen_row(const ConvP &p, const T *x, const T *state, int n, int s, int i, int c, float (&v)[VEC]) {
-    if (i >= W - 1) {
-        load_vec<T, VEC>(x + (size_t)(s + i - (W - 1)) * p.xs + c, v);
-    } else if (state) {
-        load_vec<T, VEC>(state + ((size_t)n * (W - 1) + i) * p.C + c, v);
-    } else {
+__device__ __forceinline__ void seen_row(const ConvP &p, const T *x, const T *state, int n, int s, int i, int c, Pack<T, VEC> &v) {
+    if (i >= W - 1) v.load(x + (size_t)(s + i - (W - 1)) * p.xs + c);
+    else if (state) v.load(state + ((size_t)n * (W - 1) + i) * p.C + c);
+    else v.zero();
+}
+
+// U outputs in place of U inputs; hist: the W-1 inputs before them, then the last W-1 of them.
+template <typename T, int VEC, int W, int U>
+__device__ __forceinline__ void forward_rows(const Taps<T, VEC, W> &t, bool silu, Pack<T, VEC> (&r)[U], Pack<T, VEC> (&hist)[W - 1]) {
+    using P = Pack<T, VEC>;
+    P next[W - 1];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) v[e] = 0.f;
+    for (int i = 0; i < W - 1; ++i) next[i] = U + i >= W - 1 ? r[U + i - (W - 1) < 0 ? 0 : U + i - (W - 1)] : hist[U + i < W - 1 ? U + i : 0];
+#pragma unroll
+    for (int k = 0; k < P::kWords; ++k) {
+        float out[U][P::kPer];
+#pragma unroll
+        for (int e = 0; e < P::kPer; ++e) {
+            float x[W - 1 + U];
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i) x[i] = hist[i].get(k, e);
+#pragma unroll
+            for (int u = 0; u < U; ++u) x[W - 1 + u] = r[u].get(k, e);
+            const float b = t.b.get(k, e);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float a = b;
+#pragma unroll
+                for (int j = 0; j < W; ++j) a = fmaf(t.tap(k, e, j), x[u + j], a);
+                out[u][e] = silu ? a * sigmoid<sizeof(T) == 2>(a) : a;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) r[u].put(k, out[u]);
     }
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) hist[i] = next[i];
 }
 
 template <typename T, int VEC, int W>
-__device__ __forceinline__ void load_weight(const T *weight, const T *bias, int c, float (&w)[W][VEC], float (&b)[VEC]) {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-#pragma unroll
-        for (int j = 0; j < W; ++j) w[j][e] = to_f32(weight[(size_t)(c + e) * W + j]);
-        b[e] = bias ? to_f32(bias[c + e]) : 0.f;
-    }
-}
-
-template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(32 * kWarps)
+__global__ void __launch_bounds__(32 * kWarps, 4)
 conv_fwd_kernel(ConvP p, const T *__restrict__ x, const T *__restrict__ weight, const T *__restrict__ bias,
                 const T *__restrict__ state, T *__restrict__ y, T *__restrict__ final_state, unsigned *status) {
-    constexpr bool kFast = sizeof(T) == 2;
+    using P = Pack<T, VEC>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (blockIdx.x == 0 && blockIdx.y == 0) check_cu(p.m, status, threadIdx.x, blockDim.x);
     const int c = (blockIdx.y * 32 + lane) * VEC;
@@ -70,157 +143,199 @@ conv_fwd_kernel(ConvP p, const T *__restrict__ x, const T *__restrict__ weight, 
         const int s = p.m.begin(n), len = p.m.end(n) - s;
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) {
-            float v[VEC];
+            P v;
             seen_row<T, VEC, W>(p, x, state, n, s, len + k, c, v);
-            store_vec<T, VEC>(final_state + ((size_t)n * (W - 1) + k) * p.C + c, v);
+            v.store(final_state + ((size_t)n * (W - 1) + k) * p.C + c);
         }
         return;
     }
     const int t0 = run * kRunF, t1 = min(t0 + kRunF, p.m.total);
-    float w[W][VEC], b[VEC];
-    load_weight<T, VEC, W>(weight, bias, c, w, b);
     int n = p.m.owner(t0), s = p.m.begin(n), e = p.m.end(n);
-    float win[W][VEC];  // win[i]: input t - (W-1) + i
+    P hist[W - 1];
 #pragma unroll
-    for (int i = 0; i < W - 1; ++i) seen_row<T, VEC, W>(p, x, state, n, s, max(t0 - s, 0) + i, c, win[i]);
+    for (int i = 0; i < W - 1; ++i) seen_row<T, VEC, W>(p, x, state, n, s, max(t0 - s, 0) + i, c, hist[i]);
+    Taps<T, VEC, W> taps;
+    taps.load(weight, bias, c);
     for (int tb = t0; tb < t1; tb += kAhead) {
-        float in[kAhead][VEC];
+        if (tb + kAhead <= min(e, t1)) {  // rows of one sequence
+            P r[kAhead];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-            if (tb + u < t1) load_vec<T, VEC>(x + (size_t)(tb + u) * p.xs + c, in[u]);
+            for (int u = 0; u < kAhead; ++u) r[u].load(x + (size_t)(tb + u) * p.xs + c);
+            forward_rows<T, VEC, W, kAhead>(taps, p.silu, r, hist);
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int t = tb + u;
-            if (t >= t1) break;
+            for (int u = 0; u < kAhead; ++u) r[u].store(y + (size_t)(tb + u) * p.C + c);
+            continue;
+        }
+        for (int t = tb; t < min(tb + kAhead, t1); ++t) {
             if (t >= e && n + 1 < p.m.N) {  // the next sequence with tokens begins here
                 do ++n, e = p.m.end(n); while (t >= e && n + 1 < p.m.N);
                 s = p.m.begin(n);
 #pragma unroll
-                for (int i = 0; i < W - 1; ++i) seen_row<T, VEC, W>(p, x, state, n, s, i, c, win[i]);
+                for (int i = 0; i < W - 1; ++i) seen_row<T, VEC, W>(p, x, state, n, s, i, c, hist[i]);
             }
-            float out[VEC];
-#pragma unroll
-            for (int q = 0; q < VEC; ++q) {
-                win[W - 1][q] = in[u][q];
-                float a = b[q];
-#pragma unroll
-                for (int j = 0; j < W; ++j) a = fmaf(w[j][q], win[j][q], a);
-                out[q] = p.silu ? a * sigmoid<kFast>(a) : a;
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j) win[j][q] = win[j + 1][q];
-            }
-            store_vec<T, VEC>(y + (size_t)t * p.C + c, out);
+            P r[1];
+            r[0].load(x + (size_t)t * p.xs + c);
+            forward_rows<T, VEC, W, 1>(taps, p.silu, r, hist);
+            r[0].store(y + (size_t)t * p.C + c);
         }
     }
 }
 
+// U tokens: dpre from x and dy, the weight's gradient (ACC), and the finished dx of the
+// tokens W-1 earlier, in x's place (plus `add`: the final state's gradient). hist, dh: x and
+// dpre of the W-1 tokens before.
+template <typename T, int VEC, int W, int U, bool ACC>
+__device__ __forceinline__ void backward_rows(const Taps<T, VEC, W> &t, bool silu, Pack<T, VEC> (&r)[U], const Pack<T, VEC> (&dy)[U],
+                                              const Pack<T, VEC> &add, Pack<T, VEC> (&hist)[W - 1], float (&dh)[W - 1][VEC],
+                                              float (&dw)[W][VEC], float (&db)[VEC]) {
+    using P = Pack<T, VEC>;
+    P next[W - 1];
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) next[i] = U + i >= W - 1 ? r[U + i - (W - 1) < 0 ? 0 : U + i - (W - 1)] : hist[U + i < W - 1 ? U + i : 0];
+#pragma unroll
+    for (int k = 0; k < P::kWords; ++k) {
+        float out[U][P::kPer];
+#pragma unroll
+        for (int e = 0; e < P::kPer; ++e) {
+            const int q = k * P::kPer + e;
+            float x[W - 1 + U], d[W - 1 + U];
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i) x[i] = hist[i].get(k, e), d[i] = dh[i][q];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                x[W - 1 + u] = r[u].get(k, e);
+                float g = dy[u].get(k, e);
+                if (silu) {
+                    float a = t.b.get(k, e);
+#pragma unroll
+                    for (int j = 0; j < W; ++j) a = fmaf(t.tap(k, e, j), x[u + j], a);
+                    const float s = sigmoid<sizeof(T) == 2>(a);
+                    g *= fmaf(a, s - s * s, s);
+                }
+                d[W - 1 + u] = g;
+                if (ACC) {
+                    db[q] += g;
+#pragma unroll
+                    for (int j = 0; j < W; ++j) dw[j][q] = fmaf(g, x[u + j], dw[j][q]);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float a = U == 1 ? add.get(k, e) : 0.f;
+#pragma unroll
+                for (int j = 0; j < W; ++j) a = fmaf(t.tap(k, e, j), d[u + W - 1 - j], a);
+                out[u][e] = a;
+            }
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i) dh[i][q] = d[U + i];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) r[u].put(k, out[u]);
+    }
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) hist[i] = next[i];
+}
+
 template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(32 * kWarps)
+__global__ void __launch_bounds__(32 * kWarps, 3)
 conv_bwd_kernel(ConvP p, const T *__restrict__ x, const T *__restrict__ weight, const T *__restrict__ bias,
                 const T *__restrict__ state, const T *__restrict__ dy, const T *__restrict__ dfinal, T *__restrict__ dx,
                 float *__restrict__ part, unsigned *status) {
-    constexpr bool kFast = sizeof(T) == 2;
+    using P = Pack<T, VEC>;
+    constexpr int U = kAhead / 2;
     __shared__ float red[kWarps][(W + 1) * VEC][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (blockIdx.x == 0 && blockIdx.y == 0) check_cu(p.m, status, threadIdx.x, blockDim.x);
     const int c = (blockIdx.y * 32 + lane) * VEC;
     const int run = blockIdx.x * kWarps + warp;
     const int t0 = run * kRunB, t1 = min(t0 + kRunB, p.m.total);
-    float dw[W][VEC], db[VEC];
+    float dw[W][VEC], db[VEC], dh[W - 1][VEC];
 #pragma unroll
     for (int q = 0; q < VEC; ++q) {
         db[q] = 0.f;
 #pragma unroll
         for (int j = 0; j < W; ++j) dw[j][q] = 0.f;
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) dh[i][q] = 0.f;
     }
     if (c < p.C && t0 < t1) {
-        float w[W][VEC], b[VEC];
-        load_weight<T, VEC, W>(weight, bias, c, w, b);
         int n = p.m.owner(t0), s = p.m.begin(n), e = p.m.end(n);
-        float win[W][VEC], acc[W][VEC];  // acc[i]: dx of token t - (W-1) + i, unfinished
+        P hist[W - 1];
 #pragma unroll
-        for (int i = 0; i < W - 1; ++i) seen_row<T, VEC, W>(p, x, state, n, s, max(t0 - s, 0) + i, c, win[i]);
+        for (int i = 0; i < W - 1; ++i) seen_row<T, VEC, W>(p, x, state, n, s, max(t0 - s, 0) + i, c, hist[i]);
+        Taps<T, VEC, W> taps;
+        taps.load(weight, bias, c);
+        // token t's part of the final state's gradient
+        auto final_part = [&](int t) {
+            P f;
+            f.zero();
+            if (dfinal && t >= max(t0, s) && t < t1 && t >= e - (W - 1))
+                f.load(dfinal + ((size_t)n * (W - 1) + (W - 1 - (e - t))) * p.C + c);
+            return f;
+        };
+        auto emit = [&](int t, const P &v) {  // token t is finished, if it is of this sequence and run
+            if (t >= max(t0, s) && t < t1) v.store(dx + (size_t)t * p.C + c);
+        };
+        // the last W-1 tokens before t: nothing later reaches them
+        auto flush = [&](int t) {
+            P none[1], zero[1];
 #pragma unroll
-        for (int i = 0; i < W; ++i)
-#pragma unroll
-            for (int q = 0; q < VEC; ++q) acc[i][q] = 0.f;
-        auto emit = [&](int t, float (&v)[VEC]) {  // token t is finished, if it is of this sequence and run
-            if (t < t0 || t >= t1 || t < s) return;
-            if (dfinal && t >= e - (W - 1)) {
-                float f[VEC];
-                load_vec<T, VEC>(dfinal + ((size_t)n * (W - 1) + (W - 1 - (e - t))) * p.C + c, f);
-#pragma unroll
-                for (int q = 0; q < VEC; ++q) v[q] += f[q];
+            for (int i = 0; i < W - 1; ++i) {
+                none[0].zero(), zero[0].zero();
+                float keep[W][VEC], kb[VEC];
+                backward_rows<T, VEC, W, 1, false>(taps, false, none, zero, final_part(t - (W - 1) + i), hist, dh, keep, kb);
+                emit(t - (W - 1) + i, none[0]);
             }
-            store_vec<T, VEC>(dx + (size_t)t * p.C + c, v);
         };
         const int tend = min(t1 + W - 1, p.m.total);
+        bool done = false;
         int t = t0;
-        for (int tb = t0; tb < tend; tb += kAhead / 2) {
-            float in[kAhead / 2][VEC], dv[kAhead / 2][VEC];
+        while (t < tend && !done) {
+            if (t + U <= e && (t + U <= t1 || t >= t1)) {  // behind the run (t >= t1) for the last dx only
+                P r[U], d[U];
 #pragma unroll
-            for (int u = 0; u < kAhead / 2; ++u)
-                if (tb + u < tend) {
-                    load_vec<T, VEC>(x + (size_t)(tb + u) * p.xs + c, in[u]);
-                    load_vec<T, VEC>(dy + (size_t)(tb + u) * p.C + c, dv[u]);
+                for (int u = 0; u < U; ++u) {
+                    r[u].load(x + (size_t)(t + u) * p.xs + c);
+                    d[u].load(dy + (size_t)(t + u) * p.C + c);
                 }
-            bool done = false;
-#pragma unroll
-            for (int u = 0; u < kAhead / 2; ++u) {
-                if (tb + u >= tend || done) continue;
-                t = tb + u;
-                if (t >= e && n + 1 < p.m.N) {  // a sequence ends: its last tokens are finished
-#pragma unroll
-                    for (int i = 0; i < W - 1; ++i) {
-                        emit(t - (W - 1) + i, acc[i]);
-#pragma unroll
-                        for (int q = 0; q < VEC; ++q) acc[i][q] = 0.f;
-                    }
-                    if (t >= t1) {
-                        done = true;
-                        continue;
-                    }
-                    do ++n, e = p.m.end(n); while (t >= e && n + 1 < p.m.N);
-                    s = p.m.begin(n);
-#pragma unroll
-                    for (int i = 0; i < W - 1; ++i) seen_row<T, VEC, W>(p, x, state, n, s, i, c, win[i]);
+                if (t < t1) {
+                    backward_rows<T, VEC, W, U, true>(taps, p.silu, r, d, r[0], hist, dh, dw, db);
+                } else {
+                    float keep[W][VEC], kb[VEC];
+                    backward_rows<T, VEC, W, U, false>(taps, p.silu, r, d, r[0], hist, dh, keep, kb);
                 }
-                float first[VEC];
 #pragma unroll
-                for (int q = 0; q < VEC; ++q) {
-                    win[W - 1][q] = in[u][q];
-                    float a = b[q], d = dv[u][q];
-                    if (p.silu) {
-#pragma unroll
-                        for (int j = 0; j < W; ++j) a = fmaf(w[j][q], win[j][q], a);
-                        const float g = sigmoid<kFast>(a);
-                        d *= g * (1.f + a * (1.f - g));
-                    }
-                    acc[W - 1][q] = 0.f;
-#pragma unroll
-                    for (int j = 0; j < W; ++j) {
-                        acc[j][q] = fmaf(w[j][q], d, acc[j][q]);  // token t - (W-1) + j meets tap j in t
-                        if (t < t1) dw[j][q] = fmaf(d, win[j][q], dw[j][q]);
-                    }
-                    if (t < t1) db[q] += d;
-                    first[q] = acc[0][q];
-#pragma unroll
-                    for (int j = 0; j < W - 1; ++j) {
-                        win[j][q] = win[j + 1][q];
-                        acc[j][q] = acc[j + 1][q];
-                    }
+                for (int u = 0; u < U; ++u) {  // W-1 <= U: these all lie before e - (W-1)
+                    const int te = t - (W - 1) + u;
+                    if (te >= t0 && te >= s && te < t1) r[u].store(dx + (size_t)te * p.C + c);
                 }
-                emit(t - (W - 1), first);  // acc[i] is now token t + 1 - (W-1) + i's
+                t += U;
+                continue;
             }
-            if (done) {
-                t = -1;
-                break;
-            }
-        }
-        if (t >= 0) {  // the tokens whose later taps lie behind the last token
+            if (t >= e && n + 1 < p.m.N) {  // a sequence ends
+                flush(t);
+                if (t >= t1) {
+                    done = true;
+                    break;
+                }
+                do ++n, e = p.m.end(n); while (t >= e && n + 1 < p.m.N);
+                s = p.m.begin(n);
 #pragma unroll
-            for (int i = 0; i < W - 1; ++i) emit(t + 1 - (W - 1) + i, acc[i]);
+                for (int i = 0; i < W - 1; ++i) seen_row<T, VEC, W>(p, x, state, n, s, i, c, hist[i]);
+            }
+            P r[1], d[1];
+            r[0].load(x + (size_t)t * p.xs + c);
+            d[0].load(dy + (size_t)t * p.C + c);
+            if (t < t1) {
+                backward_rows<T, VEC, W, 1, true>(taps, p.silu, r, d, final_part(t - (W - 1)), hist, dh, dw, db);
+            } else {
+                float keep[W][VEC], kb[VEC];
+                backward_rows<T, VEC, W, 1, false>(taps, p.silu, r, d, final_part(t - (W - 1)), hist, dh, keep, kb);
+            }
+            emit(t - (W - 1), r[0]);
+            ++t;
         }
+        if (!done) flush(t);
     }
 #pragma unroll
     for (int q = 0; q < VEC; ++q) {
@@ -268,29 +383,30 @@ conv_dstate_kernel(ConvP p, const T *__restrict__ x, const T *__restrict__ weigh
     const int c = blockIdx.y * 128 + threadIdx.x, n = blockIdx.x;
     if (c >= p.C) return;
     const int s = p.m.begin(n), len = p.m.end(n) - s;
-    float w[W][1], b[1], d[W - 1];
-    load_weight<T, 1, W>(weight, bias, c, w, b);
+    float d[W - 1];
+    Taps<T, 1, W> taps;
+    taps.load(weight, bias, c);
 #pragma unroll
     for (int t = 0; t < W - 1; ++t) {
         d[t] = 0.f;
         if (t >= len) continue;
         d[t] = to_f32(dy[(size_t)(s + t) * p.C + c]);
         if (!p.silu) continue;
-        float a = b[0];
+        float a = taps.b.get(0, 0);
 #pragma unroll
         for (int j = 0; j < W; ++j) {
-            float v[1];
+            Pack<T, 1> v;
             seen_row<T, 1, W>(p, x, state, n, s, t + j, c, v);
-            a = fmaf(w[j][0], v[0], a);
+            a = fmaf(taps.tap(0, 0, j), v.get(0, 0), a);
         }
         const float g = sigmoid<sizeof(T) == 2>(a);
-        d[t] *= g * (1.f + a * (1.f - g));
+        d[t] *= fmaf(a, g - g * g, g);
     }
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) {
         float v = 0.f;
 #pragma unroll
-        for (int j = 0; j <= i; ++j) v = fmaf(w[j][0], d[i - j], v);
+        for (int j = 0; j <= i; ++j) v = fmaf(taps.tap(0, 0, j), d[i - j], v);
         if (dfinal && i >= len) v += to_f32(dfinal[((size_t)n * (W - 1) + i - len) * p.C + c]);
         dstate[((size_t)n * (W - 1) + i) * p.C + c] = from_f32<T>(v);
     }
@@ -303,29 +419,22 @@ conv_update_kernel(ConvP p, const T *__restrict__ x, const T *__restrict__ weigh
                    T *__restrict__ y) {
     const int c = (blockIdx.y * 128 + threadIdx.x) * VEC, n = blockIdx.x;
     if (c >= p.C) return;
-    float win[W][VEC];
+    using P = Pack<T, VEC>;
+    P hist[W - 1];
     T *st = state + (size_t)n * (W - 1) * p.C + c;
 #pragma unroll
-    for (int i = 0; i < W - 1; ++i) load_vec<T, VEC>(st + (size_t)i * p.C, win[i]);
-    float w[W][VEC], b[VEC];
-    load_weight<T, VEC, W>(weight, bias, c, w, b);
+    for (int i = 0; i < W - 1; ++i) hist[i].load(st + (size_t)i * p.C);
+    Taps<T, VEC, W> taps;
+    taps.load(weight, bias, c);
     for (int t = 0; t < p.m.T; ++t) {
         const size_t tok = (size_t)n * p.m.T + t;
-        load_vec<T, VEC>(x + tok * p.xs + c, win[W - 1]);
-        float out[VEC];
-#pragma unroll
-        for (int q = 0; q < VEC; ++q) {
-            float a = b[q];
-#pragma unroll
-            for (int j = 0; j < W; ++j) a = fmaf(w[j][q], win[j][q], a);
-            out[q] = p.silu ? a * sigmoid<sizeof(T) == 2>(a) : a;
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j) win[j][q] = win[j + 1][q];
-        }
-        store_vec<T, VEC>(y + tok * p.C + c, out);
+        P r[1];
+        r[0].load(x + tok * p.xs + c);
+        forward_rows<T, VEC, W, 1>(taps, p.silu, r, hist);
+        r[0].store(y + tok * p.C + c);
     }
 #pragma unroll
-    for (int i = 0; i < W - 1; ++i) store_vec<T, VEC>(st + (size_t)i * p.C, win[i]);
+    for (int i = 0; i < W - 1; ++i) hist[i].store(st + (size_t)i * p.C);
 }
 
 enum Pass { kFwd, kBwd, kUpdate };
@@ -344,9 +453,12 @@ cudaError_t run_pass(const ConvArgs &a, Pass pass) {
     } else if (pass == kBwd) {
         const T *dy = (const T *)a.dy, *df = (const T *)a.dfinal;
         const int blocks = (a.seq.total + kRunB * kWarps - 1) / (kRunB * kWarps);
-        if (blocks)
+        if (blocks) {
+            TimedLaunch tl("conv_bwd", a.stream);
             conv_bwd_kernel<T, VEC, W><<<dim3(blocks, cb), 32 * kWarps, 0, a.stream>>>(p, x, w, b, st, dy, df, (T *)a.dx, a.part,
                                                                                       a.status);
+        }
+        TimedLaunch tl("conv_bwd_sums", a.stream);
         conv_dw_kernel<T><<<dim3((a.C + 31) / 32, W + 1), 256, 0, a.stream>>>(a.part, blocks, a.C, W, (T *)a.dweight, (T *)a.dbias);
         if (a.dstate)
             conv_dstate_kernel<T, W><<<dim3(a.seq.N, (a.C + 127) / 128), 128, 0, a.stream>>>(p, x, w, b, st, dy, df, (T *)a.dstate);

@@ -89,24 +89,26 @@ bool scan_on_tensor_cores(const ScanArgs &a) {
     return a.dtype == GDN_DTYPE_BF16 && !(e && strcmp(e, "simt") == 0);
 }
 
-// What the forward keeps: every chunk's entry state, hi then lo.
-size_t scan_saved_bytes(const ScanArgs &a) { return 2 * align_up(scan_tc::tile_bytes(a)); }
+// What the forward keeps: the gates, and every chunk's entry state, hi then lo.
+size_t scan_saved_bytes(const ScanArgs &a) { return scan_tc::gates_bytes(a) + 2 * align_up(scan_tc::tile_bytes(a)); }
 
-// Forward workspace: segment scratch | entry states (hi; for a call that keeps none).
+// Forward workspace: segment scratch | gates | entry states (hi; both for a call that keeps none).
 struct ScanFwdLayout {
-    size_t seg, tiles, total;
+    size_t seg, gates, tiles, total;
 };
 ScanFwdLayout scan_fwd_layout(const ScanArgs &a) {
     ScanFwdLayout L;
     L.seg = 0;
-    L.tiles = L.seg + scan_tc::segment_bytes(a);
+    L.gates = L.seg + scan_tc::segment_bytes(a);
+    L.tiles = L.gates + scan_tc::gates_bytes(a);
     L.total = L.tiles + align_up(scan_tc::tile_bytes(a));
     return L;
 }
 
-scan_tc::StateArgs state_pass(const ScanArgs &a, bool reverse, char *seg) {
+scan_tc::StateArgs state_pass(const ScanArgs &a, const scan_tc::Gates &gates, bool reverse, char *seg) {
     scan_tc::StateArgs s{};
     s.a = &a;
+    s.gates = gates;
     s.reverse = reverse;
     s.chunks_per_seg = scan_tc::chunks_per_segment(a);
     if (s.chunks_per_seg) {
@@ -125,42 +127,48 @@ scan_tc::Tiles tile_pair(char *at, const ScanArgs &a) {
 
 cudaError_t scan_fwd_tc(const ScanArgs &a) {
     const ScanFwdLayout L = scan_fwd_layout(a);
-    char *ws = (char *)a.ws;
-    scan_tc::StateArgs s = state_pass(a, false, ws + L.seg);
-    s.tiles = a.saved ? tile_pair((char *)a.saved, a) : scan_tc::Tiles{(__nv_bfloat16 *)(ws + L.tiles), nullptr};
-    const cudaError_t e = scan_tc::launch_states(s);
-    return e != cudaSuccess ? e : scan_tc::launch_out(a, s.tiles.hi);
+    char *ws = (char *)a.ws, *saved = (char *)a.saved;
+    const scan_tc::Gates gates = scan_tc::gates_at(saved ? saved : ws + L.gates, a);
+    cudaError_t e = scan_tc::launch_gates(a, gates);
+    if (e != cudaSuccess) return e;
+    scan_tc::StateArgs s = state_pass(a, gates, false, ws + L.seg);
+    s.tiles = saved ? tile_pair(saved + scan_tc::gates_bytes(a), a) : scan_tc::Tiles{(__nv_bfloat16 *)(ws + L.tiles), nullptr};
+    if ((e = scan_tc::launch_states(s)) != cudaSuccess) return e;
+    return scan_tc::launch_out(a, gates, s.tiles.hi);
 }
 
-// Backward workspace: segment scratch | exit-state gradients (hi, lo) | entry states (hi, lo; for
-// a call without `saved`) | the gradient kernel's parts.
+// Backward workspace: segment scratch | exit-state gradients (hi, lo) | the gradient kernel's
+// parts | gates and entry states (hi, lo), as the forward keeps them, for a call without `saved`.
 struct ScanBwdLayout {
-    size_t seg, g, h, grad, total;
+    size_t seg, g, grad, saved, total;
 };
 ScanBwdLayout scan_bwd_layout(const ScanArgs &a) {
     ScanBwdLayout L;
     L.seg = 0;
     L.g = L.seg + scan_tc::segment_bytes(a);
-    L.h = L.g + scan_saved_bytes(a);
-    L.grad = L.h + scan_saved_bytes(a);
-    L.total = L.grad + scan_tc::grad_bytes(a);
+    L.grad = L.g + 2 * align_up(scan_tc::tile_bytes(a));
+    L.saved = L.grad + scan_tc::grad_bytes(a);
+    L.total = L.saved + scan_saved_bytes(a);
     return L;
 }
 
 cudaError_t scan_bwd_tc(const ScanArgs &a) {
     const ScanBwdLayout L = scan_bwd_layout(a);
-    char *ws = (char *)a.ws;
-    const scan_tc::Tiles g = tile_pair(ws + L.g, a), h = tile_pair(a.saved ? (char *)a.saved : ws + L.h, a);
+    char *ws = (char *)a.ws, *saved = a.saved ? (char *)a.saved : ws + L.saved;
+    const scan_tc::Gates gates = scan_tc::gates_at(saved, a);
+    const scan_tc::Tiles g = tile_pair(ws + L.g, a), h = tile_pair(saved + scan_tc::gates_bytes(a), a);
+    cudaError_t e;
     if (!a.saved) {
-        scan_tc::StateArgs s = state_pass(a, false, ws + L.seg);
+        if ((e = scan_tc::launch_gates(a, gates)) != cudaSuccess) return e;
+        scan_tc::StateArgs s = state_pass(a, gates, false, ws + L.seg);
+        s.last = nullptr;
         s.tiles = h;
-        const cudaError_t e = scan_tc::launch_states(s);
-        if (e != cudaSuccess) return e;
+        if ((e = scan_tc::launch_states(s)) != cudaSuccess) return e;
     }
-    scan_tc::StateArgs s = state_pass(a, true, ws + L.seg);
+    scan_tc::StateArgs s = state_pass(a, gates, true, ws + L.seg);
     s.tiles = g;
-    const cudaError_t e = scan_tc::launch_states(s);
-    return e != cudaSuccess ? e : scan_tc::launch_grad(a, h, g, ws + L.grad);
+    if ((e = scan_tc::launch_states(s)) != cudaSuccess) return e;
+    return scan_tc::launch_grad(a, gates, h, g, ws + L.grad);
 }
 
 int finish(cudaError_t e) { return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA; }
@@ -207,7 +215,6 @@ int gdn_conv_bwd(const gdn_conv_problem *p, const void *x, const void *weight, c
     a.dx = dx, a.dweight = dweight, a.dbias = dbias, a.dstate = dinitial_state, a.part = (float *)workspace;
     a.stream = (cudaStream_t)stream;
     if (!(a.status = status_ptr())) return GDN_ERR_CUDA;
-    TimedLaunch t("conv_bwd", a.stream);
     return finish(launch_conv_bwd(a));
 }
 

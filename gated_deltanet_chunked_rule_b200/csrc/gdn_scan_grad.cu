@@ -22,9 +22,13 @@
 // A CTA (one per SM) takes one chunk and a run of units (a head's 64 columns; linear in them)
 // of one group. The products with B and C of the masked Q are taken once, after the masked
 // Qs are summed over the units in registers; dC and dB stay in tensor memory meanwhile (S |
-// one 128-column work region | dC | dB = 512 columns). Warps 0-7: a thread per row, two column
-// halves; warp 8 loads (TMA, bulk copies) and issues the products. The work region holds C h,
-// then Q, then (L o S)^T dY and B g'; e^{gam} dY h^T and X g'^T run while the mask is applied.
+// one 128-column work region | dC | dB = 512 columns). The work region holds C h, then Q, then
+// (L o S)^T dY and B g'; e^{gam} dY h^T and X g'^T run while the mask is applied. Warps 0-7: a
+// thread per row and column half; warp 8 issues the products on the work region, warp 9 those of
+// dC and dB, warp 10 loads (TMA, bulk copies) and stores: a tile's next load is issued as soon as
+// its last reader is done, dx leaves through the scaled dY's tile so that dY's can be refilled at
+// once. The row warps need the registers of the copying and issuing ones: beside 220 KB of shared
+// memory the L1 holds no spills, and with 60 spilled words the mask alone took 12000 cycles.
 #include <algorithm>
 
 #include "gdn_scan_tc.cuh"
@@ -36,13 +40,16 @@ namespace {
 using namespace sm100;
 using namespace gdn::warp;
 
-constexpr int kThreads = 288;
-// B | C | P (L o S, at the end the summed masked Q) | x, then scaled x | dY, then dx | h hi, lo | g' hi, lo | scaled dY
+constexpr int kRowThreads = 256;
+constexpr int kThreads = kRowThreads + 128;
+constexpr int kRowRegs = 208, kAuxRegs = 88;  // 384 threads are launched with 168 each
+static_assert(kRowThreads * kRowRegs + 128 * kAuxRegs <= kThreads * 168, "register split");
+// B | C | P (L o S, at the end the summed masked Q) | x, then scaled x | dY | h hi, lo | g' hi, lo | scaled dY, then dx
 constexpr int kB = 0, kCt = 32768, kPm = 65536, kX = 98304, kY = 114688, kH = 131072, kG = 163840, kSy = 196608;
 constexpr int kVec = 212992;
 struct Vec {
     float v[4][kC];     // e^{(start of row block w) - gam_s} for s left of block w
-    float gl[kC];       // gam (log2) relative to the row block's start
+    float gl[kC];       // log2 decay from the row block's start
     float delta[kC];
     float rsum[4][kC];  // row sums of W delta per column block (strictly below the diagonal)
     float csum[4][kC];  // column sums of W per row block (strictly below the diagonal)
@@ -51,7 +58,6 @@ struct Vec {
     float bt[2][kC];    // e^{gam_C - gam_s} x_s.(B g')_s, per column half
     float tot[4][4];    // per row block: sums of rowi, delta bt, R[.][0], R[.][1]
     float red[3][8];
-    double wsum[2][4];
 };
 constexpr int kBarsAt = kVec + (sizeof(Vec) + 15) / 16 * 16;
 constexpr int kSmem = kBarsAt + 256 + 1024;
@@ -62,18 +68,11 @@ struct GradP {
     Params p;
     int run, runs;
     const __nv_bfloat16 *h_hi, *h_lo, *g_hi, *g_lo;
-    const __nv_bfloat16 *dy;
     __nv_bfloat16 *dx, *dB, *dC;
     void *ddt;
     float *part_bc;  // [2][runs][total, G, K] where runs > 1
     float *part;     // [slots, 3, H]: dA, ddt_bias, dD
 };
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // Sum over the warp's lanes of v[i], delivered to lane i.
 __device__ __forceinline__ float lane_sums(float (&v)[32], int lane) {
@@ -121,13 +120,14 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kBarsAt);
     uint64_t *cb_full = bars, *h_full = bars + 1, *g_full = bars + 2, *x_full = bars + 3, *y_full = bars + 4;  // loads
     uint64_t *ch_full = bars + 5, *q_full = bars + 6, *cd_full = bars + 7, *dx_full = bars + 8, *end_full = bars + 9;  // products
-    uint64_t *cb_ready = bars + 10, *r_free = bars + 11, *s_ready = bars + 12, *p_ready = bars + 13, *hg_read = bars + 14,
-             *dx_done = bars + 15, *m_ready = bars + 16;  // the row threads
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 17);
+    uint64_t *sy_free = bars + 10;                                                                               // dx is stored
+    uint64_t *cb_ready = bars + 11, *r_free = bars + 12, *s_ready = bars + 13, *p_ready = bars + 14, *hg_read = bars + 15,
+             *dx_done = bars + 16, *m_ready = bars + 17;  // the row threads
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 18);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     if (tid == 0) {
-        for (int i = 0; i < 10; ++i) mbar_init(bars + i, 1);
-        for (int i = 10; i < 17; ++i) mbar_init(bars + i, 256);
+        for (int i = 0; i < 11; ++i) mbar_init(bars + i, 1);
+        for (int i = 11; i < 18; ++i) mbar_init(bars + i, kRowThreads);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -143,115 +143,131 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
         *abort_flag = 1;
         set_status(p.status, GDN_ERR_TIMEOUT);
     };
+    constexpr uint32_t idQ = idesc_bf16(128, 128, false, false), idH = idesc_bf16(128, 64, false, true),
+                       idO = idesc_bf16(128, K, false, false), idX = idesc_bf16(128, 64, true, true),
+                       idC = idesc_bf16(128, K, false, true), idB = idesc_bf16(128, K, true, true);
 
-    if (warp == 8) {
+    if (warp >= 8) {
+    reg_dec<kAuxRegs>();
+    if (warp == 8) {  // products on the work region
         if (lane == 0) {
-            int hs = 0, gs = 0, xs = 0, ys = 0;  // loads issued
-            auto unit_at = [&](int i) { return ((size_t)blockIdx.x * p.G * p.U + g * p.U + u_first + i) * (K * kPT); };
-            auto load_h = [&](int i) {
-                mbar_arrive_expect_tx(h_full, 2 * kTile);
-                bulk_load(smem + kH, q.h_hi + unit_at(i), kTile, h_full);
-                bulk_load(smem + kH + kTile, q.h_lo + unit_at(i), kTile, h_full);
-                ++hs;
-            };
-            auto load_g = [&](int i) {
-                mbar_arrive_expect_tx(g_full, 2 * kTile);
-                bulk_load(smem + kG, q.g_hi + unit_at(i), kTile, g_full);
-                bulk_load(smem + kG + kTile, q.g_lo + unit_at(i), kTile, g_full);
-                ++gs;
-            };
-            auto load_x = [&](int i) {
-                const int u = u_first + i;
-                mbar_arrive_expect_tx(x_full, 16384);
-                tma_load_3d(smem + kX, &tm_x, x_full, (u % p.S) * kPT, p.head(g, u), t0);
-                ++xs;
-            };
-            auto load_y = [&](int i) {
-                const int u = u_first + i;
-                mbar_arrive_expect_tx(y_full, 16384);
-                tma_load_3d(smem + kY, &tm_dy, y_full, (u % p.S) * kPT, p.head(g, u), t0);
-                ++ys;
-            };
-            mbar_arrive_expect_tx(cb_full, 2 * (K / 64) * 16384);
-            for (int j = 0; j < K / 64; ++j) {
-                tma_load_3d(smem + kCt + j * 16384, &tm_c, cb_full, 64 * j, g, t0);
-                tma_load_3d(smem + kB + j * 16384, &tm_b, cb_full, 64 * j, g, t0);
-            }
-            load_h(0), load_x(0), load_y(0), load_g(0);
-            constexpr uint32_t idQ = idesc_bf16(128, 128, false, false), idH = idesc_bf16(128, 64, false, true),
-                               idO = idesc_bf16(128, K, false, false), idX = idesc_bf16(128, 64, true, true),
-                               idC = idesc_bf16(128, K, false, true), idB = idesc_bf16(128, K, true, true);
+            const uint32_t b = cols(sb + kB), c = cols(sb + kCt), y = cols(sb + kY), x = cols(sb + kX), yr = rows(sb + kY),
+                           pm = rows(sb + kPm), h0 = state_rows(sb + kH), h1 = state_rows(sb + kH + kTile),
+                           g0 = state_rows(sb + kG), g1 = state_rows(sb + kG + kTile);
             bool ok = wait_bar(cb_full, 0, abort_flag) && wait_bar(cb_ready, 0, abort_flag);
             tc_fence_after();
             if (ok) {
 #pragma unroll
-                for (int k = 0; k < K / 16; ++k) mma_bf16(tmem + kColS, by_cols(sb + kCt, k), by_cols(sb + kB, k), idQ, k > 0);
+                for (int k = 0; k < K / 16; ++k) mma<kTokenHi, kTokenHi>(tmem + kColS, c + cstep(k), b + cstep(k), idQ, k > 0);
             }
             for (int i = 0; i < units && ok; ++i) {
-                // C h (the work region is free: the row threads arrived on the last dx_done)
-                ok = wait_bar(h_full, i & 1, abort_flag);
+                // C h
+                if (i > 0) ok = wait_bar(dx_done, (i - 1) & 1, abort_flag);  // the work region is read
+                ok = ok && wait_bar(h_full, i & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < 2 * (K / 16); ++k)
-                    mma_bf16(tmem + kColR, by_cols(sb + kCt, k % (K / 16)), state_by_rows<K>(sb + kH + k / (K / 16) * kTile, k % (K / 16)),
-                             idH, k > 0);
+                for (int k = 0; k < K / 16; ++k) {
+                    mma<kTokenHi, kStateRowsHi<K>>(tmem + kColR, c + cstep(k), h0 + srstep(k), idH, k > 0);
+                    mma<kTokenHi, kStateRowsHi<K>>(tmem + kColR, c + cstep(k), h1 + srstep(k), idH, true);
+                }
                 mma_commit(ch_full);
                 // Q = dY X^T
                 ok = wait_bar(x_full, i & 1, abort_flag) && wait_bar(y_full, i & 1, abort_flag) && wait_bar(r_free, i & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < 4; ++k) mma_bf16(tmem + kColR, by_cols(sb + kY, k), by_cols(sb + kX, k), idQ, k > 0);
+                for (int k = 0; k < 4; ++k) mma<kTokenHi, kTokenHi>(tmem + kColR, y + cstep(k), x + cstep(k), idQ, k > 0);
                 mma_commit(q_full);
-                // dC += (e^gam dY) h^T, dB += (delta e^{gam_C - gam} X) g'^T
-                ok = wait_bar(g_full, i & 1, abort_flag) && wait_bar(s_ready, i & 1, abort_flag);
+                // (L o S)^T dY and B g'
+                ok = wait_bar(g_full, i & 1, abort_flag) && wait_bar(p_ready, i & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    mma_bf16(tmem + kColC, by_cols(sb + kSy, k & 3), state_by_cols<K>(sb + kH + (k >> 2) * kTile, k & 3), idO, i + k > 0);
-                    mma_bf16(tmem + kColB, by_cols(sb + kX, k & 3), state_by_cols<K>(sb + kG + (k >> 2) * kTile, k & 3), idO, i + k > 0);
+                for (int k = 0; k < 8; ++k) mma<kTokenHi, kTokenHi>(tmem + kColR, pm + rstep(k), yr + rstep(k), idX, k > 0);
+#pragma unroll
+                for (int k = 0; k < K / 16; ++k) {
+                    mma<kTokenHi, kStateRowsHi<K>>(tmem + kColR + 64, b + cstep(k), g0 + srstep(k), idH, k > 0);
+                    mma<kTokenHi, kStateRowsHi<K>>(tmem + kColR + 64, b + cstep(k), g1 + srstep(k), idH, true);
+                }
+                mma_commit(dx_full);
+            }
+            if (!ok) fail();
+        }
+    } else if (warp == 9) {  // dC and dB
+        if (lane == 0) {
+            const uint32_t sy = cols(sb + kSy), x = cols(sb + kX), h0 = state_cols<K>(sb + kH), h1 = state_cols<K>(sb + kH + kTile),
+                           g0 = state_cols<K>(sb + kG), g1 = state_cols<K>(sb + kG + kTile);
+            bool ok = true;
+            for (int i = 0; i < units && ok; ++i) {
+                // dC += (e^gam dY) h^T, dB += (delta e^{gam_C - gam} X) g'^T
+                ok = wait_bar(h_full, i & 1, abort_flag) && wait_bar(g_full, i & 1, abort_flag) && wait_bar(s_ready, i & 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    mma<kTokenHi, kStateColsHi>(tmem + kColC, sy + cstep(k), h0 + scstep<K>(k), idO, i + k > 0);
+                    mma<kTokenHi, kStateColsHi>(tmem + kColB, x + cstep(k), g0 + scstep<K>(k), idO, i + k > 0);
+                    mma<kTokenHi, kStateColsHi>(tmem + kColC, sy + cstep(k), h1 + scstep<K>(k), idO, true);
+                    mma<kTokenHi, kStateColsHi>(tmem + kColB, x + cstep(k), g1 + scstep<K>(k), idO, true);
                 }
                 mma_commit(cd_full);
-                // (L o S)^T dY and B g'
-                ok = wait_bar(p_ready, i & 1, abort_flag);
-                if (!ok) break;
+            }
+            ok = ok && wait_bar(m_ready, 0, abort_flag);
+            if (ok) {
                 tc_fence_after();
+                const uint32_t mc = cols(sb + kPm), mr = rows(sb + kPm), b = rows(sb + kB), c = rows(sb + kCt);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) mma_bf16(tmem + kColR, by_rows(sb + kPm, k), by_rows(sb + kY, k), idX, k > 0);
-#pragma unroll
-                for (int k = 0; k < 2 * (K / 16); ++k)
-                    mma_bf16(tmem + kColR + 64, by_cols(sb + kB, k % (K / 16)),
-                             state_by_rows<K>(sb + kG + k / (K / 16) * kTile, k % (K / 16)), idH, k > 0);
-                mma_commit(dx_full);
+                for (int k = 0; k < 8; ++k) {
+                    mma<kTokenHi, kTokenHi>(tmem + kColC, mc + cstep(k), b + rstep(k), idC, true);
+                    mma<kTokenHi, kTokenHi>(tmem + kColB, mr + rstep(k), c + rstep(k), idB, true);
+                }
+                mma_commit(end_full);
+            }
+            if (!ok) fail();
+        }
+    } else if (warp == 10) {  // copies
+        if (lane == 0) {
+            auto tile_at = [&](int i) { return (((size_t)blockIdx.x * p.G + g) * p.U + u_first + i) * (K * kPT); };
+            auto load_pair = [&](int at, uint64_t *bar, const __nv_bfloat16 *hi, const __nv_bfloat16 *lo, int i) {
+                mbar_arrive_expect_tx(bar, 2 * kTile);
+                bulk_load(smem + at, hi + tile_at(i), kTile, bar);
+                bulk_load(smem + at + kTile, lo + tile_at(i), kTile, bar);
+            };
+            auto load_rows = [&](int at, uint64_t *bar, const CUtensorMap *map, int i) {
+                const int u = u_first + i;
+                mbar_arrive_expect_tx(bar, 16384);
+                tma_load_3d(smem + at, map, bar, (u % p.S) * kPT, p.head(g, u), t0);
+            };
+            mbar_arrive_expect_tx(cb_full, 2 * (K / 64) * 16384);
+            for (int j = 0; j < K / 64; ++j) {
+                tma_load_3d(smem + kCt + j * 16384, &tm_c, cb_full, 64 * j, g, t0);
+                tma_load_3d(smem + kB + j * 16384, &tm_b, cb_full, 64 * j, g, t0);
+            }
+            int hs = 1, gs = 1, xs = 1, ys = 1;  // loads issued
+            load_pair(kH, h_full, q.h_hi, q.h_lo, 0);
+            load_rows(kX, x_full, &tm_x, 0);
+            load_rows(kY, y_full, &tm_dy, 0);
+            load_pair(kG, g_full, q.g_hi, q.g_lo, 0);
+            bool ok = true;
+            for (int i = 0; i < units && ok; ++i) {
                 const bool more = i + 1 < units;
                 ok = wait_bar(cd_full, i & 1, abort_flag);
-                if (ok && more) load_x(i + 1);
+                if (ok && more) load_rows(kX, x_full, &tm_x, i + 1), ++xs;
                 ok = ok && wait_bar(hg_read, i & 1, abort_flag);
-                if (ok && more) load_h(i + 1);
+                if (ok && more) load_pair(kH, h_full, q.h_hi, q.h_lo, i + 1), ++hs;
                 ok = ok && wait_bar(dx_full, i & 1, abort_flag);
-                if (ok && more) load_g(i + 1);
+                if (ok && more) load_pair(kG, g_full, q.g_hi, q.g_lo, i + 1), ++gs;
                 ok = ok && wait_bar(dx_done, i & 1, abort_flag);
                 if (!ok) break;
-                tc_fence_after();
-                if (full_chunk) {  // dx stands in dY's tile
+                if (more) load_rows(kY, y_full, &tm_dy, i + 1), ++ys;
+                if (full_chunk) {  // dx stands in the scaled dY's tile
                     const int u = u_first + i;
-                    tma_store_3d(&tm_dx, sb + kY, (u % p.S) * kPT, p.head(g, u), t0);
+                    tma_store_3d(&tm_dx, sb + kSy, (u % p.S) * kPT, p.head(g, u), t0);
                     bulk_commit();
                     bulk_wait_read<0>();
                 }
-                if (more) load_y(i + 1);
-            }
-            if (ok) ok = wait_bar(m_ready, 0, abort_flag);
-            if (ok) {
-                tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    mma_bf16(tmem + kColC, by_cols(sb + kPm, k), by_rows(sb + kB, k), idC, true);
-                    mma_bf16(tmem + kColB, by_rows(sb + kPm, k), by_rows(sb + kCt, k), idB, true);
-                }
-                mma_commit(end_full);
+                mbar_arrive(sy_free);
             }
             if (!ok) fail();
             // no copy outlives the CTA
@@ -263,7 +279,9 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
             if (!done) fail();
             bulk_wait_all();
         }
+    }
     } else {
+        reg_inc<kRowRegs>();
         const int wr = warp & 3, half = warp >> 2, row = wr * 32 + lane;  // row block, column half
         const bool live = row < len;
         const uint32_t lanes = (uint32_t)(wr * 32) << 16;
@@ -280,95 +298,86 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
         mbar_arrive(cb_ready);
 
         float msum[2][32] = {};  // masked Q summed over the units: column blocks half, half + 2
-        float u_r = 0.f, e_r = 0.f, tail = 0.f, decay = 0.f, delta = 0.f, D = 0.f, raw = 0.f, A = 0.f;
-        float dgam = 0.f, wsum = 0.f, dD = 0.f;  // of the head so far (dgam, w: half 0)
-        int cur = -1;
+        float u_r = 0.f, e_r = 0.f, tail = 0.f, decay = 0.f, delta = 0.f, D = 0.f;
+        float dgam = 0.f, wsum = 0.f, dD = 0.f;  // of the head so far (dgam, wsum: half 0)
         for (int i = 0; i < units; ++i) {
             const int u = u_first + i, h = p.head(g, u);
-            if (h != cur) {  // another head: its gates
-                raw = live ? p.raw_dt(t0 + row, h) : 0.f;
-                A = p.A[h];
+            if (i % p.S == 0) {  // another head: its gates
+                const float *gt = p.gates.at(blockIdx.x, p.H, h) + row;
+                const float g_f = gt[kC], g_r = gt[2 * kC];
+                const float4 tot = p.gates.totals(blockIdx.x, p.H, h);
+                delta = gt[0];
                 D = p.D ? p.D[h] : 0.f;
-                delta = live ? p.delta(raw) : 0.f;
-                double x = (double)delta * A;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const double y = __shfl_up_sync(0xffffffffu, x, o);
-                    if (lane >= o) x += y;
-                }
-                if (lane == 31) vec.wsum[half][wr] = x;
-                if (half) named_sync<128>(3);
-                else named_sync<128>(2);
-                double base = 0.0, total = 0.0;
-                for (int k = 0; k < 4; ++k) {
-                    if (k < wr) base += vec.wsum[half][k];
-                    total += vec.wsum[half][k];
-                }
-                u_r = expf((float)x);
-                e_r = expf((float)(base + x));
-                tail = expf((float)(total - (base + x)));
-                decay = expf((float)total);
+                float before, after, all;
+                around(tot, wr, &before, &after, &all);
+                u_r = ex2(g_f), e_r = ex2(before + g_f), tail = ex2(after + g_r), decay = ex2(all);
                 if (half == 0) {
-                    vec.gl[row] = (float)(x * 1.4426950408889634);
+                    vec.gl[row] = g_f;
                     vec.delta[row] = delta;
-                    double to = vec.wsum[0][wr] - x;
-                    for (int w = wr + 1; w < 4; ++w) {
-                        vec.v[w][row] = expf((float)to);
-                        to += vec.wsum[0][w];
-                    }
+                    const float t[4] = {tot.x, tot.y, tot.z, tot.w};
+                    float to = g_r;
+#pragma unroll
+                    for (int w = 1; w < 4; ++w)
+                        if (w > wr) {
+                            vec.v[w][row] = ex2(to);
+                            to += t[w];
+                        }
                 }
                 dgam = wsum = dD = 0.f;
-                cur = h;
             }
             // ---- rows of x and dY; e^gam dY for dC, dY.(C h)
             wait(x_full, i & 1);
             wait(y_full, i & 1);
+            if (i > 0) wait(sy_free, (i - 1) & 1);
             uint4 xr[4];  // x, this half's 32 columns
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t at = piece(row, half * 4 + j);
-                xr[j] = make_uint4(0u, 0u, 0u, 0u);
-                if (!live) {
-                    st_shared_v4(sb + kX + at, 0u, 0u, 0u, 0u);
-                    st_shared_v4(sb + kY + at, 0u, 0u, 0u, 0u);
-                    st_shared_v4(sb + kSy + at, 0u, 0u, 0u, 0u);
-                    continue;
-                }
-                xr[j] = ld_shared_v4(sb + kX + at);
-                const uint4 y = ld_shared_v4(sb + kY + at);
-                const uint32_t w[4] = {y.x, y.y, y.z, y.w}, v[4] = {xr[j].x, xr[j].y, xr[j].z, xr[j].w};
-                uint32_t o[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    dD = fmaf(bf_lo(w[k]), bf_lo(v[k]), fmaf(bf_hi(w[k]), bf_hi(v[k]), dD));
-                    o[k] = pack_bf16(e_r * bf_lo(w[k]), e_r * bf_hi(w[k]));
-                }
-                st_shared_v4(sb + kSy + at, o[0], o[1], o[2], o[3]);
-            }
-            wait(ch_full, i & 1);
-            tc_fence_after();
-            float ri_half = 0.f;
+            float ri = 0.f;
             if (ok) {
-                float v[32], s = 0.f;
-                tmem_ld32(tmem + lanes + kColR + 32 * half, v);
+                uint4 yr[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint4 y = ld_shared_v4(sb + kY + piece(row, half * 4 + j));
-                    const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) s = fmaf(bf_lo(w[k]), v[8 * j + 2 * k], fmaf(bf_hi(w[k]), v[8 * j + 2 * k + 1], s));
+                    const uint32_t at = piece(row, half * 4 + j);
+                    xr[j] = live ? ld_shared_v4(sb + kX + at) : make_uint4(0u, 0u, 0u, 0u);
+                    yr[j] = live ? ld_shared_v4(sb + kY + at) : make_uint4(0u, 0u, 0u, 0u);
                 }
-                ri_half = live ? e_r * s : 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t at = piece(row, half * 4 + j);
+                    const uint32_t w[4] = {yr[j].x, yr[j].y, yr[j].z, yr[j].w}, v[4] = {xr[j].x, xr[j].y, xr[j].z, xr[j].w};
+                    uint32_t o[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        dD = fmaf(bf_lo(w[k]), bf_lo(v[k]), fmaf(bf_hi(w[k]), bf_hi(v[k]), dD));
+                        o[k] = pack_bf16(e_r * bf_lo(w[k]), e_r * bf_hi(w[k]));
+                    }
+                    st_shared_v4(sb + kSy + at, o[0], o[1], o[2], o[3]);
+                    if (!live) {
+                        st_shared_v4(sb + kX + at, 0u, 0u, 0u, 0u);
+                        st_shared_v4(sb + kY + at, 0u, 0u, 0u, 0u);
+                    }
+                }
+                wait(ch_full, i & 1);
+                tc_fence_after();
+                float v[32];
+                if (ok) {
+                    tmem_ld32(tmem + lanes + kColR + 32 * half, v);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t w[4] = {yr[j].x, yr[j].y, yr[j].z, yr[j].w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) ri = fmaf(bf_lo(w[k]), v[8 * j + 2 * k], fmaf(bf_hi(w[k]), v[8 * j + 2 * k + 1], ri));
+                    }
+                    ri = live ? e_r * ri : 0.f;
+                }
             }
             fence_proxy_async();
             tc_fence_before();
             mbar_arrive(r_free);
-            named_sync<256>(1);  // the gate vectors are written, the last unit's sums are read
-            vec.rowi[half][row] = ri_half;
+            named_sync<kRowThreads>(1);  // the gate vectors are written, the last unit's sums are read
+            vec.rowi[half][row] = ri;
             // ---- Q is there and x read by it: scaled x in its place
             wait(q_full, i & 1);
             tc_fence_after();
-            if (ok && live) {
+            if (ok) {
                 const float sc = delta * tail;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -385,49 +394,69 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
 #pragma unroll
             for (int bb = 0; bb < 2; ++bb) {
                 const int blk = half + 2 * bb;
-                const uint32_t pt = sb + kPm + (blk >> 1) * 16384;
+                const uint32_t pt = sb + kPm + bb * 16384;
                 if (blk > wr) {  // right of the diagonal
                     if (i == 0)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) st_shared_v4(pt + piece(row, (blk & 1) * 4 + j), 0u, 0u, 0u, 0u);
+                        for (int j = 0; j < 4; ++j) st_shared_v4(pt + piece(row, half * 4 + j), 0u, 0u, 0u, 0u);
                     continue;
                 }
                 if (!ok) continue;
-                float s[32], v[32];
-                tmem_ld32(tmem + lanes + kColS + 32 * blk, s);
-                tmem_ld32(tmem + lanes + kColR + 32 * blk, v);
-                const float *dl = vec.delta + 32 * blk;
-                float rs = 0.f;
+                uint32_t sr[32], vr[32];
+                tmem_ld32_nowait(tmem + lanes + kColS + 32 * blk, sr);
+                tmem_ld32_nowait(tmem + lanes + kColR + 32 * blk, vr);
+                tmem_landed(sr);
+                tmem_landed(vr);
+                const float4 *dl = reinterpret_cast<const float4 *>(vec.delta + 32 * blk);
+                float w[32], rs = 0.f;
                 if (blk < wr) {
-                    const float *ve = vec.v[wr] + 32 * blk;
+                    const float4 *ve = reinterpret_cast<const float4 *>(vec.v[wr] + 32 * blk);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const float L = u_r * ve[k], d = dl[k];
-                        msum[bb][k] = fmaf(L * d, v[k], msum[bb][k]);
-                        s[k] *= L;
-                        v[k] *= s[k];
-                        rs = fmaf(v[k], d, rs);
+                    for (int k4 = 0; k4 < 8; ++k4) {
+                        const float4 d4 = dl[k4], v4 = ve[k4];
+                        const float d[4] = {d4.x, d4.y, d4.z, d4.w}, e[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int k = 4 * k4 + j;
+                            const float qv = __uint_as_float(vr[k]), L = u_r * e[j], s = L * __uint_as_float(sr[k]);
+                            msum[bb][k] = fmaf(L * d[j], qv, msum[bb][k]);
+                            sr[k] = __float_as_uint(s);
+                            w[k] = s * qv;
+                            rs = fmaf(w[k], d[j], rs);
+                        }
                     }
                 } else {
-                    const float *gl = vec.gl + 32 * blk, me = gl[lane];
+                    const float4 *gl = reinterpret_cast<const float4 *>(vec.gl + 32 * blk);
+                    const float me = vec.gl[row];
                     float diag = 0.f;
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const float L = k <= lane ? ex2(me - gl[k]) : 0.f, d = dl[k];
-                        msum[bb][k] = fmaf(L * d, v[k], msum[bb][k]);
-                        s[k] *= L;
-                        v[k] *= s[k];
-                        if (k == lane) diag = v[k], v[k] = 0.f;
-                        rs = fmaf(v[k], d, rs);
+                    for (int k4 = 0; k4 < 8; ++k4) {
+                        const float4 d4 = dl[k4], v4 = gl[k4];
+                        const float d[4] = {d4.x, d4.y, d4.z, d4.w}, e[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int k = 4 * k4 + j;
+                            const float qv = __uint_as_float(vr[k]), L = k <= lane ? ex2(me - e[j]) : 0.f;
+                            const float s = L * __uint_as_float(sr[k]), ww = s * qv;
+                            msum[bb][k] = fmaf(L * d[j], qv, msum[bb][k]);
+                            sr[k] = __float_as_uint(s);
+                            diag = k == lane ? ww : diag;
+                            w[k] = k == lane ? 0.f : ww;
+                            rs = fmaf(w[k], d[j], rs);
+                        }
                     }
                     vec.wdiag[row] = diag;
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    st_shared_v4(pt + piece(row, (blk & 1) * 4 + j), pack_bf16(s[8 * j], s[8 * j + 1]), pack_bf16(s[8 * j + 2], s[8 * j + 3]),
-                                 pack_bf16(s[8 * j + 4], s[8 * j + 5]), pack_bf16(s[8 * j + 6], s[8 * j + 7]));
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        o[k] = pack_bf16(__uint_as_float(sr[8 * j + 2 * k]), __uint_as_float(sr[8 * j + 2 * k + 1]));
+                    st_shared_v4(pt + piece(row, half * 4 + j), o[0], o[1], o[2], o[3]);
+                }
                 vec.rsum[blk][row] = rs;
-                const float cs = lane_sums(v, lane);
+                const float cs = lane_sums(w, lane);
                 vec.csum[wr][32 * blk + lane] = cs;
             }
             fence_proxy_async();
@@ -438,8 +467,8 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
             wait(g_full, i & 1);
             if (ok) {
 #pragma unroll
-                for (int j = 0; j < K * kPT / 8 / 256; ++j) {
-                    const uint32_t at = (j * 256 + tid) * 16;
+                for (int j = 0; j < K * kPT / 8 / kRowThreads; ++j) {
+                    const uint32_t at = (j * kRowThreads + tid) * 16;
                     const uint4 a = ld_shared_v4(sb + kH + at), b = ld_shared_v4(sb + kH + kTile + at);
                     const uint4 c = ld_shared_v4(sb + kG + at), d = ld_shared_v4(sb + kG + kTile + at);
                     const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w}, cw[4] = {c.x, c.y, c.z, c.w},
@@ -454,28 +483,34 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
             mbar_arrive(hg_read);
             hg = warp_sum(hg);
             if (lane == 0) vec.red[0][warp] = hg;
-            // ---- dx
+            // ---- dx, in the scaled dY's place
+            wait(cd_full, i & 1);
             wait(dx_full, i & 1);
             tc_fence_after();
             if (ok) {
-                float a[32], b[32], s = 0.f;
-                tmem_ld32(tmem + lanes + kColR + 32 * half, a);
-                tmem_ld32(tmem + lanes + kColR + 64 + 32 * half, b);
+                uint32_t ar[32], br[32];
+                tmem_ld32_nowait(tmem + lanes + kColR + 32 * half, ar);
+                tmem_ld32_nowait(tmem + lanes + kColR + 64 + 32 * half, br);
+                uint4 yr[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) yr[j] = ld_shared_v4(sb + kY + piece(row, half * 4 + j));
+                tmem_landed(ar);
+                tmem_landed(br);
+                float s = 0.f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint32_t at = sb + kY + piece(row, half * 4 + j);
-                    const uint4 y = ld_shared_v4(at);
-                    const uint32_t w[4] = {y.x, y.y, y.z, y.w}, v[4] = {xr[j].x, xr[j].y, xr[j].z, xr[j].w};
+                    const uint32_t y[4] = {yr[j].x, yr[j].y, yr[j].z, yr[j].w}, v[4] = {xr[j].x, xr[j].y, xr[j].z, xr[j].w};
                     uint32_t o[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int c = 8 * j + 2 * k;
-                        s = fmaf(bf_lo(v[k]), b[c], fmaf(bf_hi(v[k]), b[c + 1], s));
-                        o[k] = pack_bf16(fmaf(delta, fmaf(tail, b[c], a[c]), D * bf_lo(w[k])),
-                                         fmaf(delta, fmaf(tail, b[c + 1], a[c + 1]), D * bf_hi(w[k])));
+                        const float b0 = __uint_as_float(br[c]), b1 = __uint_as_float(br[c + 1]);
+                        s = fmaf(bf_lo(v[k]), b0, fmaf(bf_hi(v[k]), b1, s));
+                        o[k] = pack_bf16(fmaf(delta, fmaf(tail, b0, __uint_as_float(ar[c])), D * bf_lo(y[k])),
+                                         fmaf(delta, fmaf(tail, b1, __uint_as_float(ar[c + 1])), D * bf_hi(y[k])));
                     }
                     if (full_chunk)
-                        st_shared_v4(at, o[0], o[1], o[2], o[3]);
+                        st_shared_v4(sb + kSy + piece(row, half * 4 + j), o[0], o[1], o[2], o[3]);
                     else if (live)
                         *reinterpret_cast<uint4 *>(q.dx + ((size_t)(t0 + row) * p.H + h) * p.P + (u % p.S) * kPT + half * 32 + 8 * j) =
                             make_uint4(o[0], o[1], o[2], o[3]);
@@ -485,7 +520,7 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
             fence_proxy_async();
             tc_fence_before();
             mbar_arrive(dx_done);
-            named_sync<256>(1);  // every row's and column's sums are written
+            named_sync<kRowThreads>(1);  // every row's and column's sums are written
             if (half == 0) {
                 // strictly lower W: sums of this token's row left of its block, of its column below it, and
                 // of both inside it
@@ -493,8 +528,9 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                 for (int k = 0; k < wr; ++k) roff += vec.rsum[k][row];
                 for (int k = wr + 1; k < 4; ++k) coff += vec.csum[k][row];
                 const float rd = vec.rsum[wr][row], cd = vec.csum[wr][row];
-                const float ri = vec.rowi[0][row] + vec.rowi[1][row], bt = vec.bt[0][row] + vec.bt[1][row];
-                float suf = ri + roff + rd - delta * cd, pre = delta * (bt + coff);
+                const float rw = vec.rowi[0][row] + vec.rowi[1][row];
+                const float bt = vec.bt[0][row] + vec.bt[1][row];
+                float suf = rw + roff + rd - delta * cd, pre = delta * (bt + coff);
                 const float pre_own = pre;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -502,7 +538,7 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                     if (lane + o < 32) suf += a;
                     if (lane >= o) pre += b;
                 }
-                const float t_ri = warp_sum(ri), t_bt = warp_sum(delta * bt);
+                const float t_ri = warp_sum(rw), t_bt = warp_sum(delta * bt);
                 const float r0 = warp_sum(wr > 0 ? vec.rsum[0][row] : 0.f), r1 = warp_sum(wr > 1 ? vec.rsum[1][row] : 0.f);
                 if (lane == 0) vec.tot[wr][0] = t_ri, vec.tot[wr][1] = t_bt, vec.tot[wr][2] = r0, vec.tot[wr][3] = r1;
                 named_sync<128>(2);
@@ -519,35 +555,33 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                 dgam += dg + decay * e;
                 wsum += cd + coff + vec.wdiag[row] + bt;
             }
-            if (u % p.S == p.S - 1) {  // the head's last slice
+            if (i % p.S == p.S - 1) {  // the head's last slice
                 float ddt = 0.f;
                 if (half == 0 && live) {
-                    ddt = fmaf(A, dgam, wsum);
-                    if (p.softplus) ddt /= 1.f + expf(-raw);
+                    ddt = fmaf(p.A[h], dgam, wsum);
+                    if (p.softplus) ddt /= 1.f + expf(-p.raw_dt(t0 + row, h));
                     const size_t at = (size_t)(t0 + row) * p.H + h;
                     if (p.dt_f32) ((float *)q.ddt)[at] = ddt;
                     else ((__nv_bfloat16 *)q.ddt)[at] = __float2bfloat16_rn(ddt);
                 }
                 const float a = warp_sum(half == 0 && live ? delta * dgam : 0.f), b = warp_sum(ddt), d = warp_sum(dD);
-                named_sync<256>(1);  // red is read
+                named_sync<kRowThreads>(1);  // red is read
                 if (lane == 0) vec.red[0][warp] = a, vec.red[1][warp] = b, vec.red[2][warp] = d;
-                named_sync<256>(1);
+                named_sync<kRowThreads>(1);
                 if (tid < 3) {
                     float v = 0.f;
                     for (int k = 0; k < 8; ++k) v += vec.red[tid][k];
                     q.part[((size_t)blockIdx.x * 3 + tid) * p.H + h] = v;
                 }
-                named_sync<256>(1);
             }
         }
         // ---- the summed masked Q, in P's place (its last product has completed: dx_full)
 #pragma unroll
         for (int bb = 0; bb < 2; ++bb) {
-            const int blk = half + 2 * bb;
-            if (blk > wr) continue;  // zeros stand there
+            if (half + 2 * bb > wr) continue;  // zeros stand there
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                st_shared_v4(sb + kPm + (blk >> 1) * 16384 + piece(row, (blk & 1) * 4 + j), pack_bf16(msum[bb][8 * j], msum[bb][8 * j + 1]),
+                st_shared_v4(sb + kPm + bb * 16384 + piece(row, half * 4 + j), pack_bf16(msum[bb][8 * j], msum[bb][8 * j + 1]),
                              pack_bf16(msum[bb][8 * j + 2], msum[bb][8 * j + 3]), pack_bf16(msum[bb][8 * j + 4], msum[bb][8 * j + 5]),
                              pack_bf16(msum[bb][8 * j + 6], msum[bb][8 * j + 7]));
         }
@@ -557,7 +591,8 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
         wait(end_full, 0);
         tc_fence_after();
         if (ok) {
-            const size_t at = ((size_t)(t0 + row) * p.G + g) * K + half * (K / 2);
+            const int c0 = half * (K / 2);
+            const size_t at = ((size_t)(t0 + row) * p.G + g) * K + c0;
 #pragma unroll
             for (int which = 0; which < 2; ++which) {
                 __nv_bfloat16 *out = which ? q.dB : q.dC;
@@ -565,7 +600,7 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
 #pragma unroll
                 for (int c = 0; c < K / 2; c += 32) {
                     float v[32];
-                    tmem_ld32(tmem + lanes + (which ? kColB : kColC) + half * (K / 2) + c, v);
+                    tmem_ld32(tmem + lanes + (which ? kColB : kColC) + c0 + c, v);
                     if (!live) continue;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -626,13 +661,13 @@ int runs_of(const ScanArgs &a) {
 }
 
 template <int K>
-cudaError_t run(const ScanArgs &a, const Tiles &h, const Tiles &gr, char *ws) {
+cudaError_t run(const ScanArgs &a, const Gates &gates, const Tiles &h, const Tiles &gr, char *ws) {
     GradP q{};
-    q.p = params(a);
+    q.p = params(a, gates);
     q.run = units_per_cta(a), q.runs = runs_of(a);
     q.h_hi = h.hi, q.h_lo = h.lo, q.g_hi = gr.hi, q.g_lo = gr.lo;
     q.dx = (__nv_bfloat16 *)a.dx, q.dB = (__nv_bfloat16 *)a.dB, q.dC = (__nv_bfloat16 *)a.dC;
-    q.dy = (const __nv_bfloat16 *)a.dy, q.ddt = a.ddt;
+    q.ddt = a.ddt;
     const int slots = a.seq.total ? a.seq.slots(kC) : 0;
     q.part = (float *)ws;
     q.part_bc = (float *)(ws + align_up((size_t)slots * 3 * a.H * 4));
@@ -668,8 +703,8 @@ size_t grad_bytes(const ScanArgs &a) {
     return align_up((size_t)a.seq.slots(kC) * 3 * a.H * 4) + (runs > 1 ? align_up(2ull * runs * a.seq.total * a.G * a.K * 4) : 0);
 }
 
-cudaError_t launch_grad(const ScanArgs &a, const Tiles &h, const Tiles &g, char *ws) {
-    return a.K == 128 ? run<128>(a, h, g, ws) : run<64>(a, h, g, ws);
+cudaError_t launch_grad(const ScanArgs &a, const Gates &gates, const Tiles &h, const Tiles &g, char *ws) {
+    return a.K == 128 ? run<128>(a, gates, h, g, ws) : run<64>(a, gates, h, g, ws);
 }
 
 }  // namespace scan_tc

@@ -6,9 +6,11 @@
 //
 // The product does not depend on the state, so only one multiply-add per element is
 // sequential. A CTA walks the chunks of one segment of a sequence with two units (128
-// accumulator columns) of a group: warps 0-3 hold unit 0's state rows in fp32 registers (a
-// thread per row of K, 64 columns), warps 4-7 unit 1's, warp 8 loads the tiles by TMA (two
-// stages), warp 9 issues the products.
+// accumulator columns) of a group: warps 0-7 hold unit 0's state in fp32 registers (a thread
+// per row of K and 32 columns), warps 8-15 unit 1's, warp 16 loads the tiles by TMA (two
+// stages), warp 17 issues the products. Bound by the sixteen warps' conversions (about 430
+// instructions per chunk each) and the 24 products of 64 cycles; with eight warps of 64
+// columns each the latencies showed and a chunk took 3.6 us instead.
 //
 // The fp32 state keeps fp32 precision although the tensor core takes bf16: B is bf16 as it
 // is, and Xs is cut into three bf16 terms that hold its 24 bits exactly (8 + 8 + 8, by
@@ -30,11 +32,52 @@ namespace {
 using namespace sm100;
 using namespace gdn::warp;
 
-constexpr int kThreads = 320;
+// Gates of every chunk slot: a warp per head.
+__global__ void __launch_bounds__(256) scan_gates_tc_kernel(Params p) {
+    const int lane = threadIdx.x & 31, h = blockIdx.y * 8 + (threadIdx.x >> 5);
+    if (blockIdx.x == 0 && blockIdx.y == 0) check_cu(p.m, p.status, threadIdx.x, blockDim.x);
+    int n, local;
+    if (h >= p.H || !p.m.slot(blockIdx.x, kC, &n, &local)) return;
+    const int t0 = p.m.begin(n) + local * kC, len = min(kC, p.m.end(n) - t0);
+    const float A2 = p.A[h] * 1.44269504f;
+    float raw[4], tot[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) raw[b] = b * 32 + lane < len ? p.raw_dt(t0 + b * 32 + lane, h) : 0.f;
+    float *v = p.gates.v + ((size_t)blockIdx.x * p.H + h) * (3 * kC) + lane;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        // log1p(exp(v)), or v itself above 20 (where they agree to fp32 precision)
+        float d = p.softplus ? (raw[b] > 20.f ? raw[b] : log1pf(expf(raw[b]))) : raw[b];
+        if (b * 32 + lane >= len) d = 0.f;
+        const float g = d * A2;
+        float f = g, r = g;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float x = __shfl_up_sync(0xffffffffu, f, o), y = __shfl_down_sync(0xffffffffu, r, o);
+            if (lane >= o) f += x;
+            if (lane + o < 32) r += y;
+        }
+        const float after = __shfl_down_sync(0xffffffffu, r, 1);
+        tot[b] = __shfl_sync(0xffffffffu, f, 31);
+        v[b * 32] = d;
+        v[kC + b * 32] = f;
+        v[2 * kC + b * 32] = lane < 31 ? after : 0.f;
+    }
+    if (lane == 0)
+        *reinterpret_cast<float4 *>(p.gates.tot + ((size_t)blockIdx.x * p.H + h) * 4) = make_float4(tot[0], tot[1], tot[2], tot[3]);
+}
+
+constexpr int kRowThreads = 512;
+constexpr int kThreads = kRowThreads + 128;
+// Registers: 640 threads are launched with 96 each; the row warps spilled there, and a spill costs
+// an L2 access beside 200 KB of shared memory.
+constexpr int kRowRegs = 104, kAuxRegs = 64;
+static_assert(kRowThreads * kRowRegs + 128 * kAuxRegs <= kThreads * 96, "register split");
+constexpr int kHalf = kPT / 2;          // columns of a thread
 constexpr int kStage = 65536;           // one stage: B (or C) tile 32 KB, x (or dY) tiles 2 x 16 KB
 constexpr int kMid = 2 * kStage;        // second and third terms: 2 x (2 x 16 KB)
-constexpr int kSmall = kMid + 65536;    // scan scratch, barriers
-constexpr int kSmem = kSmall + 512 + 1024;
+constexpr int kSmall = kMid + 65536;    // barriers
+constexpr int kSmem = kSmall + 256 + 1024;
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
 struct StateP {
@@ -55,10 +98,8 @@ scan_state_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constan
     const Params &p = q.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int pairs = (p.U + 1) / 2, g = blockIdx.y / pairs, u0 = (blockIdx.y % pairs) * 2;
-    if (blockIdx.x == 0 && blockIdx.y == 0) check_cu(p.m, p.status, tid, kThreads);
 
-    float *wsum = reinterpret_cast<float *>(smem + kSmall);  // [2 units][2 parities][4 warps]
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kSmall + 128);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kSmall);
     uint64_t *full = bars, *empty = bars + 2, *dfull = bars + 4, *xs_ready = bars + 6, *ml_free = bars + 7;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 8);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -66,15 +107,15 @@ scan_state_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constan
     int n, local;
     const bool used = p.m.slot(blockIdx.x, q.seg_tokens, &n, &local);
     const int s_begin = p.m.begin(n), s_len = p.m.end(n) - s_begin;
-    const int unit_of = warp >> 2;  // (warps 0-7) this thread's unit of the pair
+    // (row warps) this thread's unit of the pair, row and first column
+    const int unit_of = warp >> 3, wr = warp & 3, c0 = ((warp >> 2) & 1) * kHalf, row = wr * 32 + lane;
     const int u = u0 + unit_of;
-    const bool mine = warp < 8 && u < p.U;
-    const int h = mine ? p.head(g, u) : 0, col0 = mine ? (u % p.S) * kPT : 0;
-    const int row = (warp & 3) * 32 + lane;
-    const size_t user = (((size_t)n * p.H + h) * K + row) * p.P + col0;  // this row in the user's states
+    const bool mine = tid < kRowThreads && u < p.U, real = mine && row < K;
+    const int h = mine ? p.head(g, u) : 0;
+    const size_t user = (((size_t)n * p.H + h) * K + row) * p.P + (mine ? (u % p.S) * kPT : 0) + c0;  // in the user's states
     if (!used) {  // an empty sequence keeps its state
-        if (local == 0 && s_len == 0 && !q.ends_only && q.last && mine && row < K)
-            for (int i = 0; i < kPT; ++i) q.last[user + i] = q.first ? q.first[user + i] : 0.f;
+        if (local == 0 && s_len == 0 && !q.ends_only && q.last && real)
+            for (int i = 0; i < kHalf; ++i) q.last[user + i] = q.first ? q.first[user + i] : 0.f;
         return;
     }
     const int seg_begin = s_begin + local * q.seg_tokens, seg_len = min(q.seg_tokens, s_begin + s_len - seg_begin);
@@ -85,12 +126,12 @@ scan_state_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constan
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1), mbar_init(&dfull[i], 1);
-        mbar_init(xs_ready, 256);
+        mbar_init(xs_ready, kRowThreads);
         mbar_init(ml_free, 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == 8) {
+    if (warp == 16) {
         tmem_alloc(tmem_slot, 256);
         tmem_relinquish();
     }
@@ -104,7 +145,9 @@ scan_state_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constan
         set_status(p.status, GDN_ERR_TIMEOUT);
     };
 
-    if (warp == 8) {
+    if (warp >= 16) {  // (the register split stands inside the roles: what follows a join keeps the smaller share)
+    reg_dec<kAuxRegs>();
+    if (warp == 16) {
         if (lane == 0) {
             const int nx = u0 + 1 < p.U ? 2 : 1;
             bool ok = true;
@@ -124,7 +167,7 @@ scan_state_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constan
             for (int k = max(0, i - 2); k < i; ++k)
                 if (!drain(&full[k & 1], (k >> 1) & 1)) fail();
         }
-    } else if (warp == 9) {
+    } else if (warp == 17) {
         if (lane == 0) {
             const uint32_t id = idesc_bf16(128, 128, true, true);
             bool ok = true;
@@ -132,42 +175,51 @@ scan_state_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constan
                 ok = wait_bar(xs_ready, i & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t a = sb + (i & 1) * kStage, d = tmem + (i & 1) * 128;
+                const uint32_t st = sb + (i & 1) * kStage, d = tmem + (i & 1) * 128;
+                const uint32_t a = rows(st), hi = rows(st + 32768), md = rows(sb + kMid), lo = rows(sb + kMid + 32768);
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    mma_bf16(d, by_rows(a, k & 7), by_rows(sb + kMid + (k >> 3) * 32768, k & 7), id, k > 0);
+                for (int k = 0; k < 8; ++k) {
+                    mma<kTokenHi, kTokenHi>(d, a + rstep(k), md + rstep(k), id, k > 0);
+                    mma<kTokenHi, kTokenHi>(d, a + rstep(k), lo + rstep(k), id, true);
+                }
                 mma_commit(ml_free);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) mma_bf16(d, by_rows(a, k), by_rows(a + 32768, k), id, true);
+                for (int k = 0; k < 8; ++k) mma<kTokenHi, kTokenHi>(d, a + rstep(k), hi + rstep(k), id, true);
                 mma_commit(&dfull[i & 1]);
                 mma_commit(&empty[i & 1]);
             }
             if (!ok) fail();
         }
+    }
     } else {
-        float st[kPT];  // the state's row
-        const size_t units = (size_t)p.G * p.U, seg_at = ((size_t)blockIdx.x * units + g * p.U + u) * kPT * K + row;
-        const bool real = mine && row < K;
-        if (real && !q.ends_only && (at_first ? q.first != nullptr : true)) {
+        reg_inc<kRowRegs>();
+        float st[kHalf];  // this thread's part of the state
+        const size_t units = (size_t)p.G * p.U, unit = (size_t)g * p.U + u;
+        float *const seg = q.seg + (((size_t)blockIdx.x * units + unit) * K + row) * kPT + c0;
+        const float *src = q.ends_only ? nullptr : at_first ? (q.first ? q.first + user : nullptr) : seg;
+        if (real && src) {
 #pragma unroll
-            for (int i = 0; i < kPT; ++i) st[i] = at_first ? q.first[user + i] : q.seg[seg_at + (size_t)i * K];
+            for (int i = 0; i < kHalf; i += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(src + i);
+                st[i] = v.x, st[i + 1] = v.y, st[i + 2] = v.z, st[i + 3] = v.w;
+            }
         } else {
 #pragma unroll
-            for (int i = 0; i < kPT; ++i) st[i] = 0.f;
+            for (int i = 0; i < kHalf; ++i) st[i] = 0.f;
         }
-        const float A = mine ? p.A[h] : 0.f;
-        const int chunk_slot0 = p.m.slot0(n, kC) + (seg_begin - s_begin) / kC;
+        const size_t slot0 = (size_t)p.m.slot0(n, kC) + (seg_begin - s_begin) / kC;
+        const bool keeps = q.tiles.hi && real && !q.ends_only;
         auto keep = [&](int i) {  // the state on entry to chunk i of the walk
-            if (!q.tiles.hi || !real || q.ends_only) return;
-            const size_t at = (((size_t)(chunk_slot0 + chunk_at(i)) * units + g * p.U + u) * kPT) * K + (size_t)row * 8;
+            if (!keeps) return;
+            const size_t at = ((slot0 + chunk_at(i)) * units + unit) * (K * kPT) + (size_t)(c0 / 8) * K * 8 + row * 8;
 #pragma unroll
-            for (int b = 0; b < kPT / 8; ++b) {
+            for (int b = 0; b < kHalf / 8; ++b) {
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float x0 = st[8 * b + 2 * j], x1 = st[8 * b + 2 * j + 1];
                     hi[j] = pack_bf16(x0, x1);
-                    lo[j] = pack_bf16(x0 - bf_lo(hi[j]), x1 - bf_hi(hi[j]));
+                    if (q.tiles.lo) lo[j] = pack_bf16(x0 - bf_lo(hi[j]), x1 - bf_hi(hi[j]));
                 }
                 *reinterpret_cast<uint4 *>(q.tiles.hi + at + (size_t)b * K * 8) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 if (q.tiles.lo)
@@ -175,72 +227,68 @@ scan_state_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constan
             }
         };
         keep(0);
-        auto fetch = [&](int i) {  // dt (+ bias) of this thread's token of chunk i
-            const int t = chunk_at(i) * kC + row;
-            return mine && i < chunks && t < seg_len ? p.raw_dt(seg_begin + t, h) : 0.f;
+        // this token's gates of chunk i: what Xs is scaled by, and the chunk's whole decay (log2)
+        float g_delta = 0.f, g_sum = 0.f;
+        float4 g_tot = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto fetch = [&](int i) {
+            if (!mine || i >= chunks) return;
+            const size_t slot = slot0 + chunk_at(i);
+            const float *gt = p.gates.at(slot, p.H, h) + row;
+            if (!REVERSE) g_delta = gt[0];
+            g_sum = REVERSE ? gt[kC] : gt[2 * kC];
+            g_tot = p.gates.totals(slot, p.H, h);
         };
-        float raw = fetch(0), gam_sum = 0.f, decay_prev = 0.f;
+        fetch(0);
+        float gam_sum = 0.f, decay_prev = 0.f;
         bool ok = true;
         for (int i = 0; i <= chunks; ++i) {
             float decay = 0.f;
             if (i < chunks) {
                 const int len = min(kC, seg_len - chunk_at(i) * kC);
-                const bool live = row < len;
-                const float delta = live ? p.delta(raw) : 0.f;
-                raw = fetch(i + 1);
-                // running sums of the log decay: to the right of the token (forward), up to and
-                // including it (reverse); summed from the end that matters, for their precision
-                const float lg = mine ? delta * A : 0.f;
-                float x = lg;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const float y = REVERSE ? __shfl_up_sync(0xffffffffu, x, o) : __shfl_down_sync(0xffffffffu, x, o);
-                    if (REVERSE ? lane >= o : lane + o < 32) x += y;
-                }
-                float *ws = wsum + (unit_of * 2 + (i & 1)) * 4;
-                if (lane == (REVERSE ? 31 : 0)) ws[warp & 3] = x;
-                if (unit_of) named_sync<128>(2);
-                else named_sync<128>(1);
-                float total = 0.f, off = 0.f;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    total += ws[k];
-                    if (REVERSE ? k < (warp & 3) : k > (warp & 3)) off += ws[k];
-                }
-                const float e = REVERSE ? x + off : (x - lg) + off;
-                const float scale = live ? (REVERSE ? expf(e) : delta * expf(e)) : 0.f;
-                decay = expf(total);
-                gam_sum += total;
+                const bool live = mine && row < len;
+                float before, after, all;
+                around(g_tot, wr, &before, &after, &all);
+                const float scale = REVERSE ? ex2(before + g_sum) : g_delta * ex2(after + g_sum);
+                decay = ex2(all);
+                gam_sum += all;
+                fetch(i + 1);
                 // a wait that expired: no more work and no more waits, but every barrier of the
                 // loop is still met, so that it ends
                 ok = ok && wait_bar(&full[i & 1], (i >> 1) & 1, abort_flag);
-                if (i > 0) ok = ok && wait_bar(ml_free, (i - 1) & 1, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 const uint32_t stage = sb + (i & 1) * kStage;
-                if (ok && !live && unit_of == 0) {  // rows of the next sequence: no product may meet them
-#pragma unroll
-                    for (int j = 0; j < K / 8; ++j) st_shared_v4(stage + (j >> 3) * 16384 + piece(row, j & 7), 0u, 0u, 0u, 0u);
-                }
                 const uint32_t xt = stage + 32768 + unit_of * 16384, mid = sb + kMid + unit_of * 16384;
+                uint4 v[4];
 #pragma unroll
-                for (int j = 0; ok && j < 8; ++j) {
-                    uint32_t hi[4] = {}, md[4] = {}, lo[4] = {};
-                    if (live && mine) {
-                        const uint4 v = ld_shared_v4(xt + piece(row, j));
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                for (int j = 0; j < 4; ++j) v[j] = ok && live ? ld_shared_v4(xt + piece(row, c0 / 8 + j)) : make_uint4(0u, 0u, 0u, 0u);
+                if (i > 0) ok = __all_sync(0xffffffffu, ok && wait_bar(ml_free, (i - 1) & 1, abort_flag));
+                if (ok) {
+                    if (row >= len && unit_of == 0) {  // rows of the next sequence: no product may meet them
+#pragma unroll
+                        for (int j = 0; j < K / 16; ++j) {
+                            const int k = (c0 ? K / 16 : 0) + j;
+                            st_shared_v4(stage + (k >> 3) * 16384 + piece(row, k & 7), 0u, 0u, 0u, 0u);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+                        uint32_t hi[4], md[4], lo[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
+                            // a dead row's value is +0, its scale finite: all terms 0
                             const float a0 = bf_lo(w[k]) * scale, a1 = bf_hi(w[k]) * scale;
                             hi[k] = __byte_perm(__float_as_uint(a0), __float_as_uint(a1), 0x7632);
                             const float b0 = a0 - bf_hi(__float_as_uint(a0)), b1 = a1 - bf_hi(__float_as_uint(a1));
                             md[k] = __byte_perm(__float_as_uint(b0), __float_as_uint(b1), 0x7632);
-                            const float c0 = b0 - bf_hi(__float_as_uint(b0)), c1 = b1 - bf_hi(__float_as_uint(b1));
-                            lo[k] = __byte_perm(__float_as_uint(c0), __float_as_uint(c1), 0x7632);
+                            const float d0 = b0 - bf_hi(__float_as_uint(b0)), d1 = b1 - bf_hi(__float_as_uint(b1));
+                            lo[k] = __byte_perm(__float_as_uint(d0), __float_as_uint(d1), 0x7632);
                         }
+                        const uint32_t at = piece(row, c0 / 8 + j);
+                        st_shared_v4(xt + at, hi[0], hi[1], hi[2], hi[3]);
+                        st_shared_v4(mid + at, md[0], md[1], md[2], md[3]);
+                        st_shared_v4(mid + 32768 + at, lo[0], lo[1], lo[2], lo[3]);
                     }
-                    st_shared_v4(xt + piece(row, j), hi[0], hi[1], hi[2], hi[3]);
-                    st_shared_v4(mid + piece(row, j), md[0], md[1], md[2], md[3]);
-                    st_shared_v4(mid + 32768 + piece(row, j), lo[0], lo[1], lo[2], lo[3]);
                 }
                 fence_proxy_async();
                 tc_fence_before();
@@ -249,57 +297,56 @@ scan_state_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constan
             if (i > 0) {
                 ok = __all_sync(0xffffffffu, ok && wait_bar(&dfull[(i - 1) & 1], ((i - 1) >> 1) & 1, abort_flag));
                 tc_fence_after();
-                const uint32_t d = tmem + ((uint32_t)((warp & 3) * 32) << 16) + ((i - 1) & 1) * 128 + unit_of * kPT;
+                if (ok) {
+                    float v[kHalf];
+                    tmem_ld32(tmem + ((uint32_t)(wr * 32) << 16) + ((i - 1) & 1) * 128 + unit_of * kPT + c0, v);
 #pragma unroll
-                for (int half = 0; ok && half < 2; ++half) {
-                    float v[32];
-                    tmem_ld32(d + 32 * half, v);
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) st[32 * half + k] = fmaf(decay_prev, st[32 * half + k], v[k]);
+                    for (int k = 0; k < kHalf; ++k) st[k] = fmaf(decay_prev, st[k], v[k]);
+                    if (i < chunks) keep(i);
                 }
-                if (ok && i < chunks) keep(i);
             }
             decay_prev = decay;
         }
         if (!ok) fail();
         if (real && ok) {
-            if (q.ends_only) {
+            float *out = q.ends_only ? seg : at_last && q.last ? q.last + user : nullptr;
+            if (out)
 #pragma unroll
-                for (int i = 0; i < kPT; ++i) q.seg[seg_at + (size_t)i * K] = st[i];
-                if (row == 0 && col0 == 0) q.seg_gam[(size_t)blockIdx.x * p.H + h] = gam_sum;
-            } else if (at_last && q.last) {
-#pragma unroll
-                for (int i = 0; i < kPT / 4; ++i)
-                    *reinterpret_cast<float4 *>(q.last + user + 4 * i) =
-                        make_float4(st[4 * i], st[4 * i + 1], st[4 * i + 2], st[4 * i + 3]);
-            }
+                for (int i = 0; i < kHalf; i += 4)
+                    *reinterpret_cast<float4 *>(out + i) = make_float4(st[i], st[i + 1], st[i + 2], st[i + 3]);
+            if (q.ends_only && row == 0 && c0 == 0 && u % p.S == 0) q.seg_gam[(size_t)blockIdx.x * p.H + h] = gam_sum;
         }
         tc_fence_before();
     }
     __syncthreads();
-    if (warp == 8) {
+    if (warp == 16) {
         tc_fence_after();
         tmem_dealloc(tmem, 256);
     }
 }
 
-// Start states of the segments, in place of their ends: start' = e^{gam} start + end. A
-// thread per state element walks a sequence's segments.
+// Start states of the segments, in place of their ends: start' = 2^gam start + end. A
+// thread per four state elements walks a sequence's segments.
 template <int K, bool REVERSE>
 __global__ void __launch_bounds__(256)
 scan_compose_kernel(Params p, int seg_tokens, const float *__restrict__ first, float *__restrict__ seg, const float *__restrict__ seg_gam) {
-    const int n = blockIdx.x, unit = blockIdx.y, e = blockIdx.z * 256 + threadIdx.x;  // e = column * K + row
+    const int n = blockIdx.x, unit = blockIdx.y, e = (blockIdx.z * 256 + threadIdx.x) * 4;  // e = row * 64 + column
     const int len = p.m.end(n) - p.m.begin(n), segs = (len + seg_tokens - 1) / seg_tokens;
     if (segs < 2) return;
-    const int h = p.head(unit / p.U, unit % p.U), col = (unit % p.U % p.S) * kPT + e / K;
+    const int h = p.head(unit / p.U, unit % p.U), col = (unit % p.U % p.S) * kPT + e % kPT;
     const size_t slot0 = p.m.slot0(n, seg_tokens), units = (size_t)p.G * p.U;
-    float cur = first ? first[(((size_t)n * p.H + h) * K + e % K) * p.P + col] : 0.f;
-    for (int i = 0; i < segs; ++i) {
-        const size_t s = slot0 + (REVERSE ? segs - 1 - i : i);
-        float *at = seg + (s * units + unit) * kPT * K + e;
-        const float end = i + 1 < segs ? *at : 0.f;
-        *at = cur;
-        if (i + 1 < segs) cur = fmaf(expf(seg_gam[s * p.H + h]), cur, end);
+    float4 cur = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (first) cur = *reinterpret_cast<const float4 *>(first + (((size_t)n * p.H + h) * K + e / kPT) * p.P + col);
+    auto slot = [&](int i) { return slot0 + (REVERSE ? segs - 1 - i : i); };
+    auto at = [&](int i) { return reinterpret_cast<float4 *>(seg + (slot(i) * units + unit) * (K * kPT) + e); };
+    float4 end = *at(0);
+    float gam = seg_gam[slot(0) * p.H + h];
+    for (int i = 0; i + 1 < segs; ++i) {
+        const float4 v = end;
+        const float d = ex2(gam);
+        if (i + 2 < segs) end = *at(i + 1), gam = seg_gam[slot(i + 1) * p.H + h];
+        cur = make_float4(fmaf(d, cur.x, v.x), fmaf(d, cur.y, v.y), fmaf(d, cur.z, v.z), fmaf(d, cur.w, v.w));
+        *at(i + 1) = cur;  // the first segment starts from `first` itself
     }
 }
 
@@ -312,12 +359,11 @@ cudaError_t run(const StateArgs &s) {
                             !token_map(&mx, x, a.P, a.H, s.reverse ? (long long)a.H * a.P : a.xs, a.seq.total)))
         return cudaErrorInvalidValue;
     StateP q{};
-    q.p = params(a);
+    q.p = params(a, s.gates);
     q.first = s.first, q.last = s.last, q.seg = s.seg, q.seg_gam = s.seg_gam, q.tiles = s.tiles;
     const bool split = s.chunks_per_seg > 0;
     // without a split a segment is longer than any sequence
     q.seg_tokens = split ? s.chunks_per_seg * kC : std::max(kC, (a.seq.cu ? a.seq.total : a.seq.T) / kC * kC + kC);
-    if (a.seq.total == 0 && !a.seq.cu) q.seg_tokens = kC;
     const int slots = a.seq.total == 0 ? a.seq.N : a.seq.slots(q.seg_tokens);
     const int pairs = (q.p.U + 1) / 2;
     auto kernel = scan_state_kernel<K, REVERSE>;
@@ -332,7 +378,7 @@ cudaError_t run(const StateArgs &s) {
         }
         q.ends_only = false;
         TimedLaunch t("scan_compose", a.stream);
-        scan_compose_kernel<K, REVERSE><<<dim3(a.seq.N, a.G * q.p.U, K * kPT / 256), 256, 0, a.stream>>>(q.p, q.seg_tokens, s.first, s.seg,
+        scan_compose_kernel<K, REVERSE><<<dim3(a.seq.N, a.G * q.p.U, K * kPT / 1024), 256, 0, a.stream>>>(q.p, q.seg_tokens, s.first, s.seg,
                                                                                                      s.seg_gam);
     }
     TimedLaunch t(REVERSE ? "scan_state_bwd" : "scan_state", a.stream);
@@ -341,6 +387,14 @@ cudaError_t run(const StateArgs &s) {
 }
 
 }  // namespace
+
+cudaError_t launch_gates(const ScanArgs &a, const Gates &g) {
+    // the kernels behind this one read the offsets unchecked
+    const int slots = std::max(1, a.seq.total ? a.seq.slots(kC) : 0);
+    TimedLaunch t("scan_gates", a.stream);
+    scan_gates_tc_kernel<<<dim3(slots, (a.H + 7) / 8), 256, 0, a.stream>>>(params(a, g));
+    return cudaGetLastError();
+}
 
 // One CTA per SM at a time: where sequences x unit pairs fill less than the SMs, a sequence is
 // cut into as many segments as fit beside each other, of at least 4 chunks (a packed batch, of

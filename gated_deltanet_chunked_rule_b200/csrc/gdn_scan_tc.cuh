@@ -27,6 +27,20 @@ namespace scan_tc {
 constexpr int kC = 128;   // tokens of a chunk
 constexpr int kPT = 64;   // state columns of a unit
 
+// The gates of every (chunk slot, head), from one small kernel: step sizes, and the log
+// decay's sums (times log2 e) within blocks of 32 tokens, forwards up to and with the token
+// and backwards after it, each summed from the end that matters so that it keeps its relative
+// precision far into a chunk; tot: the four blocks' totals. A token past the sequence has
+// delta 0 and decay 1.
+struct Gates {
+    float *v;    // [slots, H, 3, 128]: delta, forward, backward
+    float *tot;  // [slots, H, 4]
+    __device__ __forceinline__ const float *at(size_t slot, int H, int h) const { return v + (slot * H + h) * (3 * kC); }
+    __device__ __forceinline__ float4 totals(size_t slot, int H, int h) const {
+        return *reinterpret_cast<const float4 *>(tot + (slot * H + h) * 4);
+    }
+};
+
 struct Params {
     SeqMap m;
     int G, H, K, P, S, U;  // U: units of a group
@@ -35,6 +49,7 @@ struct Params {
     long long dts;
     const void *dt;
     const float *A, *D, *dt_bias;
+    Gates gates;
     unsigned *status;
     __device__ __forceinline__ int head(int g, int u) const { return g * (H / G) + u / S; }
     __device__ __forceinline__ float raw_dt(int t, int h) const {
@@ -42,19 +57,43 @@ struct Params {
         const float v = dt_f32 ? ((const float *)dt)[at] : __bfloat162float(((const __nv_bfloat16 *)dt)[at]);
         return v + (dt_bias ? dt_bias[h] : 0.f);
     }
-    // log1p(exp(v)), or v itself above 20 (where they agree to fp32 precision)
-    __device__ __forceinline__ float delta(float raw) const {
-        return softplus ? (raw > 20.f ? raw : log1pf(expf(raw))) : raw;
-    }
 };
 
-inline Params params(const ScanArgs &a) {
+inline size_t gates_bytes(const ScanArgs &a) { return align_up((size_t)a.seq.slots(kC) * a.H * (3 * kC + 4) * 4); }
+
+inline Gates gates_at(char *at, const ScanArgs &a) {
+    Gates g;
+    g.v = (float *)at;
+    g.tot = g.v + (size_t)a.seq.slots(kC) * a.H * 3 * kC;
+    return g;
+}
+
+inline Params params(const ScanArgs &a, const Gates &gates) {
     Params p;
     p.m = a.seq;
     p.G = a.G, p.H = a.H, p.K = a.K, p.P = a.P, p.S = a.P / kPT, p.U = a.H / a.G * p.S;
     p.softplus = a.softplus, p.dt_f32 = a.dt_dtype == GDN_DTYPE_F32, p.dts = a.dts, p.dt = a.dt;
-    p.A = a.A, p.D = a.D, p.dt_bias = a.dt_bias, p.status = a.status;
+    p.A = a.A, p.D = a.D, p.dt_bias = a.dt_bias, p.gates = gates, p.status = a.status;
     return p;
+}
+
+// 2^x (relative error 2^-22)
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Sums of a chunk's block totals before and after block w, and all of them.
+__device__ __forceinline__ void around(const float4 &t, int w, float *before, float *after, float *all) {
+    const float a[4] = {t.x, t.y, t.z, t.w};
+    float lo = 0.f, hi = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        lo += k < w ? a[k] : 0.f;
+        hi += k > w ? a[k] : 0.f;
+    }
+    *before = lo, *after = hi, *all = (a[0] + a[1]) + (a[2] + a[3]);
 }
 
 // Per-chunk tiles: hi, then lo, of every (chunk slot, unit).
@@ -74,22 +113,40 @@ inline bool token_map(CUtensorMap *m, const void *base, int width, int heads, lo
     return warp::make_bf16_map(m, base, 3, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Operand descriptors. Token tiles ([128 rows][64 columns] bf16, 128-byte swizzle, 16384 bytes;
-// the next 64 columns 16384 bytes on): contraction along the columns, or along the rows.
-__device__ __forceinline__ uint64_t by_cols(uint32_t base, int ks) {
-    return sm100::smem_desc(base + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024, sm100::kSw128);
-}
-__device__ __forceinline__ uint64_t by_rows(uint32_t base, int ks) {
-    return sm100::smem_desc(base + ks * 2048, 16384, 1024, sm100::kSw128);
-}
-// Blocked state tiles ([K rows][64 columns]): contraction along the rows, or the columns.
+// Operand descriptors as two words: the low one (address, leading offset) varies, k-step
+// offsets are added to it; the high one (stride, version, layout) is a constant of the kind,
+// so that an issuing thread holds one register per operand. Token tiles ([128 rows][64
+// columns] bf16, 128-byte swizzle, 16384 bytes; the next 64 columns 16384 bytes on):
+// contraction along the columns, or along the rows.
+constexpr uint32_t kTokenHi = (1024u >> 4) | (1u << 14) | ((uint32_t)sm100::kSw128 << 29);
+__device__ __forceinline__ uint32_t cols(uint32_t base) { return ((base >> 4) & 0x3fffu) | ((16u >> 4) << 16); }
+__device__ __forceinline__ uint32_t rows(uint32_t base) { return ((base >> 4) & 0x3fffu) | ((16384u >> 4) << 16); }
+constexpr uint32_t cstep(int k) { return (uint32_t)((k >> 2) * 16384 + (k & 3) * 32) >> 4; }
+constexpr uint32_t rstep(int k) { return (uint32_t)(k * 2048) >> 4; }
+// Blocked state tiles ([K rows][64 columns], no swizzle): contraction along the rows, or the
+// columns.
 template <int K>
-__device__ __forceinline__ uint64_t state_by_rows(uint32_t base, int ks) {
-    return sm100::smem_desc(base + ks * 256, 128, K * 16, sm100::kSwNone);
-}
+constexpr uint32_t kStateRowsHi = (uint32_t)K | (1u << 14);  // stride K * 16
+constexpr uint32_t kStateColsHi = (128u >> 4) | (1u << 14);
+__device__ __forceinline__ uint32_t state_rows(uint32_t base) { return ((base >> 4) & 0x3fffu) | ((128u >> 4) << 16); }
 template <int K>
-__device__ __forceinline__ uint64_t state_by_cols(uint32_t base, int ks) {
-    return sm100::smem_desc(base + ks * (2 * K * 16), K * 16, 128, sm100::kSwNone);
+__device__ __forceinline__ uint32_t state_cols(uint32_t base) { return ((base >> 4) & 0x3fffu) | ((uint32_t)K << 16); }
+constexpr uint32_t srstep(int k) { return (uint32_t)(k * 256) >> 4; }
+template <int K>
+constexpr uint32_t scstep(int k) {
+    return (uint32_t)(k * 2 * K * 16) >> 4;
+}
+
+// D[tmem] (+)= A B of one k-step.
+template <uint32_t A_HI, uint32_t B_HI>
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %6};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "n"(A_HI), "n"(B_HI)
+        : "memory");
 }
 
 // Byte offset of 16-byte piece j of row r of a token tile.
@@ -110,24 +167,26 @@ __device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 
 // State pass over the chunks: REVERSE walks them backwards with C and dY in place of B and x.
 struct StateArgs {
     const ScanArgs *a;
+    Gates gates;
     bool reverse;
     int chunks_per_seg;  // 0: whole sequences
-    float *seg;          // [segment slots, units, 64, K] scratch (segments only)
+    float *seg;          // [segment slots, units, K, 64] scratch (segments only)
     float *seg_gam;      // [segment slots, H]
     const float *first;  // h0 or dht, nullable
     float *last;         // final state or dh0, nullable
     Tiles tiles;         // hi nullable: no tiles kept
 };
+cudaError_t launch_gates(const ScanArgs &a, const Gates &g);
 cudaError_t launch_states(const StateArgs &s);
 // Segments that a problem's state passes are cut into, and their scratch.
 int chunks_per_segment(const ScanArgs &a);
 size_t segment_bytes(const ScanArgs &a);
 
-cudaError_t launch_out(const ScanArgs &a, const __nv_bfloat16 *tiles_hi);
+cudaError_t launch_out(const ScanArgs &a, const Gates &g, const __nv_bfloat16 *tiles_hi);
 
 // Gradients from every chunk's entry state h and exit gradient g; scratch of grad_bytes.
 size_t grad_bytes(const ScanArgs &a);
-cudaError_t launch_grad(const ScanArgs &a, const Tiles &h, const Tiles &g, char *ws);
+cudaError_t launch_grad(const ScanArgs &a, const Gates &gates, const Tiles &h, const Tiles &g, char *ws);
 
 }  // namespace scan_tc
 }  // namespace gdn
