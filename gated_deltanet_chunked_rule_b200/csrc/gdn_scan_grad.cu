@@ -436,12 +436,15 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const int k = 4 * k4 + j;
-                            const float qv = __uint_as_float(vr[k]), L = k <= lane ? ex2(me - e[j]) : 0.f;
+                            // masked by bits, not by a branch: all ones where column <= row, where < row
+                            const uint32_t on = (uint32_t)((k - 1 - lane) >> 31), below = (uint32_t)((k - lane) >> 31);
+                            const float qv = __uint_as_float(vr[k]);
+                            const float L = __uint_as_float(__float_as_uint(ex2(me - e[j])) & on);
                             const float s = L * __uint_as_float(sr[k]), ww = s * qv;
                             msum[bb][k] = fmaf(L * d[j], qv, msum[bb][k]);
                             sr[k] = __float_as_uint(s);
-                            diag = k == lane ? ww : diag;
-                            w[k] = k == lane ? 0.f : ww;
+                            diag += __uint_as_float(__float_as_uint(ww) & (on ^ below));
+                            w[k] = __uint_as_float(__float_as_uint(ww) & below);
                             rs = fmaf(w[k], d[j], rs);
                         }
                     }

@@ -14,7 +14,9 @@
 //
 // The fp32 state keeps fp32 precision although the tensor core takes bf16: B is bf16 as it
 // is, and Xs is cut into three bf16 terms that hold its 24 bits exactly (8 + 8 + 8, by
-// truncation); two terms left 2.5e-6 in the final state. The second and third term are
+// truncation); two terms left 2.5e-6 in the final state. (Splitting x times the scale's bf16 terms
+// exactly by packed bf16 multiply-adds takes half the instructions, and half as long again.) The
+// second and third term are
 // multiplied first, so that their buffer is free for the next chunk while the first one's
 // product still runs, and the accumulator has two buffers.
 //

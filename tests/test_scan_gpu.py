@@ -150,6 +150,15 @@ def test_sequences_cut_into_segments(gdn, lens, packed, K, P, H):
     verify(v, lens, True, train(gdn, v))
 
 
+@pytest.mark.parametrize("H,G,P,lens", [(24, 1, 128, [300]), (40, 1, 64, [128, 200]), (48, 2, 128, [129]), (7, 1, 128, [256])])
+def test_many_heads_of_one_group(gdn, H, G, P, lens):
+    # long runs of heads in one block of the output and gradient kernels
+    v = make(lens, H, G, 128, P, torch.bfloat16, seed=H)
+    for _ in range(3):
+        got = train(gdn, v)
+    verify(v, lens, True, got)
+
+
 def test_large_and_small_steps(gdn):
     # delta near 0 and above softplus's switch; decays that underflow to 0
     for dtype in (torch.float32, torch.bfloat16):
