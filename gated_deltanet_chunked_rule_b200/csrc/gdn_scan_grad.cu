@@ -51,7 +51,7 @@ struct Vec {
     float v[4][kC];     // e^{(start of row block w) - gam_s} for s left of block w
     float gl[kC];       // log2 decay from the row block's start
     float delta[kC];
-    float rsum[4][kC];  // row sums of W delta per column block (strictly below the diagonal)
+    float rsum[2][4][kC];  // row sums of W delta per column half and block (strictly below the diagonal)
     float csum[4][kC];  // column sums of W per row block (strictly below the diagonal)
     float wdiag[kC];    // W_tt
     float rowi[2][kC];  // e^{gam_r} dY_r.(C h)_r, per column half
@@ -74,18 +74,24 @@ struct GradP {
     float *part;     // [slots, 3, H]: dA, ddt_bias, dD
 };
 
-// Sum over the warp's lanes of v[i], delivered to lane i.
-__device__ __forceinline__ float lane_sums(float (&v)[32], int lane) {
+// Sum over the warp's lanes of a[i], b[i], delivered to lane i (a), 16 + i (b).
+__device__ __forceinline__ float lane_sums(float (&a)[16], const float (&b)[16], int lane) {
+    const bool upper = lane & 16;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+    for (int i = 0; i < 16; ++i) {
+        const float send = upper ? a[i] : b[i], keep = upper ? b[i] : a[i];
+        a[i] = keep + __shfl_xor_sync(0xffffffffu, send, 16);
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
         const bool up = lane & o;
 #pragma unroll
         for (int i = 0; i < o; ++i) {
-            const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+            const float send = up ? a[i] : a[i + o], keep = up ? a[i + o] : a[i];
+            a[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
         }
     }
-    return v[0];
+    return a[0];
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -237,7 +243,7 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
             auto load_rows = [&](int at, uint64_t *bar, const CUtensorMap *map, int i) {
                 const int u = u_first + i;
                 mbar_arrive_expect_tx(bar, 16384);
-                tma_load_3d(smem + at, map, bar, (u % p.S) * kPT, p.head(g, u), t0);
+                tma_load_3d(smem + at, map, bar, p.col0(u), p.head(g, u), t0);
             };
             mbar_arrive_expect_tx(cb_full, 2 * (K / 64) * 16384);
             for (int j = 0; j < K / 64; ++j) {
@@ -263,7 +269,7 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                 if (more) load_rows(kY, y_full, &tm_dy, i + 1), ++ys;
                 if (full_chunk) {  // dx stands in the scaled dY's tile
                     const int u = u_first + i;
-                    tma_store_3d(&tm_dx, sb + kSy, (u % p.S) * kPT, p.head(g, u), t0);
+                    tma_store_3d(&tm_dx, sb + kSy, p.col0(u), p.head(g, u), t0);
                     bulk_commit();
                     bulk_wait_read<0>();
                 }
@@ -297,12 +303,14 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
         fence_proxy_async();
         mbar_arrive(cb_ready);
 
-        float msum[2][32] = {};  // masked Q summed over the units: column blocks half, half + 2
+        // masked Q summed over the units: columns 16 half .. of every block of 32 (so that a row block's
+        // two warps share its diagonal block)
+        float msum[4][16] = {};
         float u_r = 0.f, e_r = 0.f, tail = 0.f, decay = 0.f, delta = 0.f, D = 0.f;
         float dgam = 0.f, wsum = 0.f, dD = 0.f;  // of the head so far (dgam, wsum: half 0)
         for (int i = 0; i < units; ++i) {
             const int u = u_first + i, h = p.head(g, u);
-            if (i % p.S == 0) {  // another head: its gates
+            if ((i & (p.S - 1)) == 0) {  // another head: its gates
                 const float *gt = p.gates.at(blockIdx.x, p.H, h) + row;
                 const float g_f = gt[kC], g_r = gt[2 * kC];
                 const float4 tot = p.gates.totals(blockIdx.x, p.H, h);
@@ -390,77 +398,86 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
             }
             fence_proxy_async();
             mbar_arrive(s_ready);
-            // ---- the mask: column blocks half and half + 2
+            // ---- the mask, two column blocks at a time
 #pragma unroll
-            for (int bb = 0; bb < 2; ++bb) {
-                const int blk = half + 2 * bb;
-                const uint32_t pt = sb + kPm + bb * 16384;
-                if (blk > wr) {  // right of the diagonal
-                    if (i == 0)
+            for (int kp = 0; kp < 2; ++kp) {
+                float w[2][16];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) st_shared_v4(pt + piece(row, half * 4 + j), 0u, 0u, 0u, 0u);
-                    continue;
-                }
-                if (!ok) continue;
-                uint32_t sr[32], vr[32];
-                tmem_ld32_nowait(tmem + lanes + kColS + 32 * blk, sr);
-                tmem_ld32_nowait(tmem + lanes + kColR + 32 * blk, vr);
-                tmem_landed(sr);
-                tmem_landed(vr);
-                const float4 *dl = reinterpret_cast<const float4 *>(vec.delta + 32 * blk);
-                float w[32], rs = 0.f;
-                if (blk < wr) {
-                    const float4 *ve = reinterpret_cast<const float4 *>(vec.v[wr] + 32 * blk);
+                for (int b = 0; b < 2; ++b) {
+                    const int k = 2 * kp + b;
+                    const uint32_t pt = sb + kPm + kp * 16384;
+                    const uint32_t at[2] = {pt + piece(row, 4 * b + 2 * half), pt + piece(row, 4 * b + 2 * half + 1)};
+                    if (k > wr || !ok) {  // right of the diagonal
 #pragma unroll
-                    for (int k4 = 0; k4 < 8; ++k4) {
-                        const float4 d4 = dl[k4], v4 = ve[k4];
-                        const float d[4] = {d4.x, d4.y, d4.z, d4.w}, e[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int k = 4 * k4 + j;
-                            const float qv = __uint_as_float(vr[k]), L = u_r * e[j], s = L * __uint_as_float(sr[k]);
-                            msum[bb][k] = fmaf(L * d[j], qv, msum[bb][k]);
-                            sr[k] = __float_as_uint(s);
-                            w[k] = s * qv;
-                            rs = fmaf(w[k], d[j], rs);
+                        for (int j = 0; j < 16; ++j) w[b][j] = 0.f;
+                        if (i == 0) {
+                            st_shared_v4(at[0], 0u, 0u, 0u, 0u);
+                            st_shared_v4(at[1], 0u, 0u, 0u, 0u);
                         }
+                        continue;
                     }
-                } else {
-                    const float4 *gl = reinterpret_cast<const float4 *>(vec.gl + 32 * blk);
-                    const float me = vec.gl[row];
-                    float diag = 0.f;
+                    uint32_t sr[16], vr[16];
+                    tmem_ld16_nowait(tmem + lanes + kColS + 32 * k + 16 * half, sr);
+                    tmem_ld16_nowait(tmem + lanes + kColR + 32 * k + 16 * half, vr);
+                    tmem_landed(sr);
+                    tmem_landed(vr);
+                    const float4 *dl = reinterpret_cast<const float4 *>(vec.delta + 32 * k + 16 * half);
+                    float rs = 0.f;
+                    if (k < wr) {
+                        const float4 *ve = reinterpret_cast<const float4 *>(vec.v[wr] + 32 * k + 16 * half);
 #pragma unroll
-                    for (int k4 = 0; k4 < 8; ++k4) {
-                        const float4 d4 = dl[k4], v4 = gl[k4];
-                        const float d[4] = {d4.x, d4.y, d4.z, d4.w}, e[4] = {v4.x, v4.y, v4.z, v4.w};
+                        for (int j4 = 0; j4 < 4; ++j4) {
+                            const float4 d4 = dl[j4], v4 = ve[j4];
+                            const float d[4] = {d4.x, d4.y, d4.z, d4.w}, e[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int k = 4 * k4 + j;
-                            // masked by bits, not by a branch: all ones where column <= row, where < row
-                            const uint32_t on = (uint32_t)((k - 1 - lane) >> 31), below = (uint32_t)((k - lane) >> 31);
-                            const float qv = __uint_as_float(vr[k]);
-                            const float L = __uint_as_float(__float_as_uint(ex2(me - e[j])) & on);
-                            const float s = L * __uint_as_float(sr[k]), ww = s * qv;
-                            msum[bb][k] = fmaf(L * d[j], qv, msum[bb][k]);
-                            sr[k] = __float_as_uint(s);
-                            diag += __uint_as_float(__float_as_uint(ww) & (on ^ below));
-                            w[k] = __uint_as_float(__float_as_uint(ww) & below);
-                            rs = fmaf(w[k], d[j], rs);
+                            for (int jj = 0; jj < 4; ++jj) {
+                                const int j = 4 * j4 + jj;
+                                const float qv = __uint_as_float(vr[j]), L = u_r * e[jj], s = L * __uint_as_float(sr[j]);
+                                msum[k][j] = fmaf(L * d[jj], qv, msum[k][j]);
+                                sr[j] = __float_as_uint(s);
+                                w[b][j] = s * qv;
+                                rs = fmaf(w[b][j], d[jj], rs);
+                            }
                         }
+                    } else {
+                        const float4 *gl = reinterpret_cast<const float4 *>(vec.gl + 32 * k + 16 * half);
+                        const float me = vec.gl[row];
+                        float diag = 0.f;
+#pragma unroll
+                        for (int j4 = 0; j4 < 4; ++j4) {
+                            const float4 d4 = dl[j4], v4 = gl[j4];
+                            const float d[4] = {d4.x, d4.y, d4.z, d4.w}, e[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+                            for (int jj = 0; jj < 4; ++jj) {
+                                const int j = 4 * j4 + jj;
+                                // masked by bits, not by a branch: all ones where column <= row, where < row
+                                const uint32_t on = (uint32_t)((16 * half + j - 1 - lane) >> 31), below = (uint32_t)((16 * half + j - lane) >> 31);
+                                const float qv = __uint_as_float(vr[j]);
+                                const float L = __uint_as_float(__float_as_uint(ex2(me - e[jj])) & on);
+                                const float s = L * __uint_as_float(sr[j]), ww = s * qv;
+                                msum[k][j] = fmaf(L * d[jj], qv, msum[k][j]);
+                                sr[j] = __float_as_uint(s);
+                                diag += __uint_as_float(__float_as_uint(ww) & (on ^ below));
+                                w[b][j] = __uint_as_float(__float_as_uint(ww) & below);
+                                rs = fmaf(w[b][j], d[jj], rs);
+                            }
+                        }
+                        if (half == lane >> 4) vec.wdiag[row] = diag;
                     }
-                    vec.wdiag[row] = diag;
-                }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t o[4];
+                    for (int j = 0; j < 2; ++j) {
+                        uint32_t o[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        o[k] = pack_bf16(__uint_as_float(sr[8 * j + 2 * k]), __uint_as_float(sr[8 * j + 2 * k + 1]));
-                    st_shared_v4(pt + piece(row, half * 4 + j), o[0], o[1], o[2], o[3]);
+                        for (int c = 0; c < 4; ++c)
+                            o[c] = pack_bf16(__uint_as_float(sr[8 * j + 2 * c]), __uint_as_float(sr[8 * j + 2 * c + 1]));
+                        st_shared_v4(at[j], o[0], o[1], o[2], o[3]);
+                    }
+                    vec.rsum[half][k][row] = rs;
                 }
-                vec.rsum[blk][row] = rs;
-                const float cs = lane_sums(w, lane);
-                vec.csum[wr][32 * blk + lane] = cs;
+                if (2 * kp <= wr) {
+                    const float cs = lane_sums(w[0], w[1], lane);
+                    vec.csum[wr][64 * kp + 32 * (lane >> 4) + 16 * half + (lane & 15)] = cs;
+                }
             }
             fence_proxy_async();
             tc_fence_before();
@@ -515,7 +532,7 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                     if (full_chunk)
                         st_shared_v4(sb + kSy + piece(row, half * 4 + j), o[0], o[1], o[2], o[3]);
                     else if (live)
-                        *reinterpret_cast<uint4 *>(q.dx + ((size_t)(t0 + row) * p.H + h) * p.P + (u % p.S) * kPT + half * 32 + 8 * j) =
+                        *reinterpret_cast<uint4 *>(q.dx + ((size_t)(t0 + row) * p.H + h) * p.P + p.col0(u) + half * 32 + 8 * j) =
                             make_uint4(o[0], o[1], o[2], o[3]);
                 }
                 vec.bt[half][row] = live ? tail * s : 0.f;
@@ -528,9 +545,9 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                 // strictly lower W: sums of this token's row left of its block, of its column below it, and
                 // of both inside it
                 float roff = 0.f, coff = 0.f;
-                for (int k = 0; k < wr; ++k) roff += vec.rsum[k][row];
+                for (int k = 0; k < wr; ++k) roff += vec.rsum[0][k][row] + vec.rsum[1][k][row];
                 for (int k = wr + 1; k < 4; ++k) coff += vec.csum[k][row];
-                const float rd = vec.rsum[wr][row], cd = vec.csum[wr][row];
+                const float rd = vec.rsum[0][wr][row] + vec.rsum[1][wr][row], cd = vec.csum[wr][row];
                 const float rw = vec.rowi[0][row] + vec.rowi[1][row];
                 const float bt = vec.bt[0][row] + vec.bt[1][row];
                 float suf = rw + roff + rd - delta * cd, pre = delta * (bt + coff);
@@ -542,7 +559,8 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                     if (lane >= o) pre += b;
                 }
                 const float t_ri = warp_sum(rw), t_bt = warp_sum(delta * bt);
-                const float r0 = warp_sum(wr > 0 ? vec.rsum[0][row] : 0.f), r1 = warp_sum(wr > 1 ? vec.rsum[1][row] : 0.f);
+                const float r0 = warp_sum(wr > 0 ? vec.rsum[0][0][row] + vec.rsum[1][0][row] : 0.f);
+                const float r1 = warp_sum(wr > 1 ? vec.rsum[0][1][row] + vec.rsum[1][1][row] : 0.f);
                 if (lane == 0) vec.tot[wr][0] = t_ri, vec.tot[wr][1] = t_bt, vec.tot[wr][2] = r0, vec.tot[wr][3] = r1;
                 named_sync<128>(2);
                 float dg = suf + (pre - pre_own);
@@ -558,7 +576,7 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                 dgam += dg + decay * e;
                 wsum += cd + coff + vec.wdiag[row] + bt;
             }
-            if (i % p.S == p.S - 1) {  // the head's last slice
+            if ((i & (p.S - 1)) == p.S - 1) {  // the head's last slice
                 float ddt = 0.f;
                 if (half == 0 && live) {
                     ddt = fmaf(p.A[h], dgam, wsum);
@@ -580,13 +598,13 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
         }
         // ---- the summed masked Q, in P's place (its last product has completed: dx_full)
 #pragma unroll
-        for (int bb = 0; bb < 2; ++bb) {
-            if (half + 2 * bb > wr) continue;  // zeros stand there
+        for (int k = 0; k < 4; ++k) {
+            if (k > wr) continue;  // zeros stand there
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                st_shared_v4(sb + kPm + bb * 16384 + piece(row, half * 4 + j), pack_bf16(msum[bb][8 * j], msum[bb][8 * j + 1]),
-                             pack_bf16(msum[bb][8 * j + 2], msum[bb][8 * j + 3]), pack_bf16(msum[bb][8 * j + 4], msum[bb][8 * j + 5]),
-                             pack_bf16(msum[bb][8 * j + 6], msum[bb][8 * j + 7]));
+            for (int j = 0; j < 2; ++j)
+                st_shared_v4(sb + kPm + (k >> 1) * 16384 + piece(row, 4 * (k & 1) + 2 * half + j), pack_bf16(msum[k][8 * j], msum[k][8 * j + 1]),
+                             pack_bf16(msum[k][8 * j + 2], msum[k][8 * j + 3]), pack_bf16(msum[k][8 * j + 4], msum[k][8 * j + 5]),
+                             pack_bf16(msum[k][8 * j + 6], msum[k][8 * j + 7]));
         }
         fence_proxy_async();
         tc_fence_before();

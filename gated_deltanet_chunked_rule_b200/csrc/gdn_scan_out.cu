@@ -120,7 +120,7 @@ scan_out_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant_
                 ok = wait_bar(&x_full[i % 3], (i / 3) & 1, abort_flag) && wait_bar(&p_ready[i & 1], (i >> 1) & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t pm = cols(sb + kP + ((i / p.S) & 1) * 32768), x = rows(sb + kX + i % 3 * 16384);
+                const uint32_t pm = cols(sb + kP + ((i >> p.sh) & 1) * 32768), x = rows(sb + kX + i % 3 * 16384);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) mma<kTokenHi, kTokenHi>(d, pm + cstep(k), x + rstep(k), id, k > 0);
                 mma_commit(&y_full[i & 1]);
@@ -132,7 +132,7 @@ scan_out_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant_
             auto load_x = [&](int i) {
                 const int u = u_first + i;
                 mbar_arrive_expect_tx(&x_full[i % 3], 16384);
-                tma_load_3d(smem + kX + i % 3 * 16384, &tm_x, &x_full[i % 3], (u % p.S) * kPT, p.head(g, u), t0);
+                tma_load_3d(smem + kX + i % 3 * 16384, &tm_x, &x_full[i % 3], p.col0(u), p.head(g, u), t0);
             };
             auto load_h = [&](int i) {
                 mbar_arrive_expect_tx(&h_full[i & 1], K * kPT * 2);
@@ -155,7 +155,7 @@ scan_out_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant_
                 if (!ok) break;
                 if (full_chunk) {
                     const int u = u_first + i;
-                    tma_store_3d(&tm_y, sb + kX + i % 3 * 16384, (u % p.S) * kPT, p.head(g, u), t0);
+                    tma_store_3d(&tm_y, sb + kX + i % 3 * 16384, p.col0(u), p.head(g, u), t0);
                     bulk_commit();
                     bulk_wait_read<0>();
                 }
@@ -173,7 +173,7 @@ scan_out_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant_
         const int w2 = warp - 18;
         bool ok = true;
         for (int i = 0; i < units; i += p.S) {
-            const int hb = (i / p.S) & 1, h = p.head(g, u_first + i);
+            const int hb = (i >> p.sh) & 1, h = p.head(g, u_first + i);
             const float *gt = p.gates.at(blockIdx.x, p.H, h);
             const float4 tot = p.gates.totals(blockIdx.x, p.H, h);
             const float t[4] = {tot.x, tot.y, tot.z, tot.w};
@@ -184,7 +184,7 @@ scan_out_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant_
                 gd[k] = gt[row], gf[k] = gt[kC + row], gr[k] = gt[2 * kC + row];
             }
             // the factors of two heads before are read
-            const int j = i / p.S;
+            const int j = i >> p.sh;
             if (j >= 2) ok = __all_sync(0xffffffffu, ok && wait_bar(&v_free[hb], ((j - 2) >> 1) & 1, abort_flag));
             Vec &vec = reinterpret_cast<Vec *>(smem + kVec)[hb];
 #pragma unroll
@@ -222,8 +222,8 @@ scan_out_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant_
         float e_next = 0.f, d_next = 0.f;  // e^{gam_r} and D of the head masked last
         // unit i's P (where it begins a head), and leave for its product
         auto mask = [&](int i) {
-            if (i % p.S == 0) {
-                const int hb = (i / p.S) & 1;
+            if ((i & (p.S - 1)) == 0) {
+                const int hb = (i >> p.sh) & 1;
                 Vec &vec = reinterpret_cast<Vec *>(smem + kVec)[hb];
                 float before, after, all;
                 around(g_tot, wr, &before, &after, &all);
@@ -231,45 +231,45 @@ scan_out_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant_
                 d_next = g_d;
                 const float me = g_f;
                 if (i + p.S < units) fetch(i + p.S);
-                ok = __all_sync(0xffffffffu, ok && wait_bar(&v_full[hb], (i / p.S >> 1) & 1, abort_flag));
-                const uint32_t at = sb + kP + hb * 32768 + (qd >> 1) * 16384;
-                const uint32_t j0 = (qd & 1) * 4;
-                if (qd > wr) {  // right of the diagonal: zeros, once per buffer
-                    if (i < 2 * p.S)
+                ok = __all_sync(0xffffffffu, ok && wait_bar(&v_full[hb], (i >> p.sh >> 1) & 1, abort_flag));
+                const uint32_t at = sb + kP + hb * 32768;
+                // this warp's columns: 8 qd .. of every block of 32, so that a row block's warps share its
+                // diagonal block
+                uint32_t v[4][8];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) st_shared_v4(at + piece(row, j0 + j), 0u, 0u, 0u, 0u);
-                } else if (ok) {
-                    float v[32];
-                    tmem_ld32(tmem + lanes + kColS + 32 * qd, v);
-                    const float4 *vs = reinterpret_cast<const float4 *>(vec.col[wr] + 32 * qd);
-                    if (qd < wr) {
-                        const float u_r = ex2(me);
+                for (int k = 0; k < 4; ++k)
+                    if (k <= wr && ok) tmem_ld8_nowait(tmem + lanes + kColS + 32 * k + 8 * qd, v[k]);
+                tmem_landed(v);
+                const float u_r = ex2(me);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float4 c = vs[k];
-                            v[4 * k] *= u_r * c.x, v[4 * k + 1] *= u_r * c.y, v[4 * k + 2] *= u_r * c.z, v[4 * k + 3] *= u_r * c.w;
-                        }
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t to = at + (k >> 1) * 16384 + piece(row, (k & 1) * 4 + qd);
+                    if (k > wr) {  // right of the diagonal: zeros, once per buffer
+                        if (i < 2 * p.S) st_shared_v4(to, 0u, 0u, 0u, 0u);
+                        continue;
+                    }
+                    const float4 *vs = reinterpret_cast<const float4 *>(vec.col[wr] + 32 * k + 8 * qd);
+                    const float4 ca = vs[0], cb = vs[1];
+                    const float c[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
+                    float o[8];
+                    if (k < wr) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) o[j] = u_r * c[j] * __uint_as_float(v[k][j]);
                     } else {
-                        const float4 *gs = reinterpret_cast<const float4 *>(vec.gl + 32 * qd);
+                        const float4 *gs = reinterpret_cast<const float4 *>(vec.gl + 32 * k + 8 * qd);
+                        const float4 la = gs[0], lb = gs[1];
+                        const float l[8] = {la.x, la.y, la.z, la.w, lb.x, lb.y, lb.z, lb.w};
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float4 c4 = vs[k], l4 = gs[k];
-                            const float c[4] = {c4.x, c4.y, c4.z, c4.w}, l[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {  // masked by bits: as 32 branches this took 1900 cycles
-                                const uint32_t on = (uint32_t)((4 * k + j - 1 - lane) >> 31);  // all ones where column <= row
-                                v[4 * k + j] = __uint_as_float(__float_as_uint(ex2(me - l[j]) * c[j] * v[4 * k + j]) & on);
-                            }
+                        for (int j = 0; j < 8; ++j) {
+                            const uint32_t on = (uint32_t)((8 * qd + j - 1 - lane) >> 31);  // all ones where column <= row
+                            o[j] = __uint_as_float(__float_as_uint(ex2(me - l[j]) * c[j] * __uint_as_float(v[k][j])) & on);
                         }
                     }
                     if (!full_chunk) {  // rows and columns of the next sequence
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) v[k] = live && 32 * qd + k < len ? v[k] : 0.f;
+                        for (int j = 0; j < 8; ++j) o[j] = live && 32 * k + 8 * qd + j < len ? o[j] : 0.f;
                     }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        st_shared_v4(at + piece(row, j0 + j), pack_bf16(v[8 * j], v[8 * j + 1]), pack_bf16(v[8 * j + 2], v[8 * j + 3]),
-                                     pack_bf16(v[8 * j + 4], v[8 * j + 5]), pack_bf16(v[8 * j + 6], v[8 * j + 7]));
+                    st_shared_v4(to, pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
                 }
                 mbar_arrive(&v_free[hb]);
             }
@@ -319,7 +319,7 @@ scan_out_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant_
                     if (full_chunk)
                         st_shared_v4(xb + piece(row, 2 * qd + j), o[0], o[1], o[2], o[3]);
                     else if (live)
-                        *reinterpret_cast<uint4 *>(q.y + ((size_t)(t0 + row) * p.H + h) * p.P + (u % p.S) * kPT + qd * 16 + 8 * j) =
+                        *reinterpret_cast<uint4 *>(q.y + ((size_t)(t0 + row) * p.H + h) * p.P + p.col0(u) + qd * 16 + 8 * j) =
                             make_uint4(o[0], o[1], o[2], o[3]);
                 }
             }

@@ -114,7 +114,7 @@ scan_state_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constan
     const int u = u0 + unit_of;
     const bool mine = tid < kRowThreads && u < p.U, real = mine && row < K;
     const int h = mine ? p.head(g, u) : 0;
-    const size_t user = (((size_t)n * p.H + h) * K + row) * p.P + (mine ? (u % p.S) * kPT : 0) + c0;  // in the user's states
+    const size_t user = (((size_t)n * p.H + h) * K + row) * p.P + (mine ? p.col0(u) : 0) + c0;  // in the user's states
     if (!used) {  // an empty sequence keeps its state
         if (local == 0 && s_len == 0 && !q.ends_only && q.last && real)
             for (int i = 0; i < kHalf; ++i) q.last[user + i] = q.first ? q.first[user + i] : 0.f;
@@ -162,7 +162,7 @@ scan_state_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constan
                 mbar_arrive_expect_tx(&full[st], (K / 64 + nx) * 16384);
                 for (int j = 0; j < K / 64; ++j) tma_load_3d(dst + j * 16384, &tm_b, &full[st], 64 * j, g, t0);
                 for (int j = 0; j < nx; ++j)
-                    tma_load_3d(dst + 32768 + j * 16384, &tm_x, &full[st], ((u0 + j) % p.S) * kPT, p.head(g, u0 + j), t0);
+                    tma_load_3d(dst + 32768 + j * 16384, &tm_x, &full[st], p.col0(u0 + j), p.head(g, u0 + j), t0);
             }
             if (!ok) fail();
             // no copy outlives the CTA: the last two stages issued are waited for
@@ -316,7 +316,7 @@ scan_state_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constan
 #pragma unroll
                 for (int i = 0; i < kHalf; i += 4)
                     *reinterpret_cast<float4 *>(out + i) = make_float4(st[i], st[i + 1], st[i + 2], st[i + 3]);
-            if (q.ends_only && row == 0 && c0 == 0 && u % p.S == 0) q.seg_gam[(size_t)blockIdx.x * p.H + h] = gam_sum;
+            if (q.ends_only && row == 0 && c0 == 0 && (u & (p.S - 1)) == 0) q.seg_gam[(size_t)blockIdx.x * p.H + h] = gam_sum;
         }
         tc_fence_before();
     }
@@ -335,7 +335,7 @@ scan_compose_kernel(Params p, int seg_tokens, const float *__restrict__ first, f
     const int n = blockIdx.x, unit = blockIdx.y, e = (blockIdx.z * 256 + threadIdx.x) * 4;  // e = row * 64 + column
     const int len = p.m.end(n) - p.m.begin(n), segs = (len + seg_tokens - 1) / seg_tokens;
     if (segs < 2) return;
-    const int h = p.head(unit / p.U, unit % p.U), col = (unit % p.U % p.S) * kPT + e % kPT;
+    const int h = p.head(unit / p.U, unit % p.U), col = p.col0(unit % p.U) + e % kPT;
     const size_t slot0 = p.m.slot0(n, seg_tokens), units = (size_t)p.G * p.U;
     float4 cur = make_float4(0.f, 0.f, 0.f, 0.f);
     if (first) cur = *reinterpret_cast<const float4 *>(first + (((size_t)n * p.H + h) * K + e / kPT) * p.P + col);

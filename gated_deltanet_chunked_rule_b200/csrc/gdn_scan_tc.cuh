@@ -44,6 +44,7 @@ struct Gates {
 struct Params {
     SeqMap m;
     int G, H, K, P, S, U;  // U: units of a group
+    int hg, sh;            // heads of a group; S = 1 << sh
     bool softplus;
     int dt_f32;
     long long dts;
@@ -51,7 +52,8 @@ struct Params {
     const float *A, *D, *dt_bias;
     Gates gates;
     unsigned *status;
-    __device__ __forceinline__ int head(int g, int u) const { return g * (H / G) + u / S; }
+    __device__ __forceinline__ int head(int g, int u) const { return g * hg + (u >> sh); }
+    __device__ __forceinline__ int col0(int u) const { return (u & (S - 1)) * kPT; }  // a unit's first column
     __device__ __forceinline__ float raw_dt(int t, int h) const {
         const size_t at = (size_t)t * dts + h;
         const float v = dt_f32 ? ((const float *)dt)[at] : __bfloat162float(((const __nv_bfloat16 *)dt)[at]);
@@ -71,7 +73,7 @@ inline Gates gates_at(char *at, const ScanArgs &a) {
 inline Params params(const ScanArgs &a, const Gates &gates) {
     Params p;
     p.m = a.seq;
-    p.G = a.G, p.H = a.H, p.K = a.K, p.P = a.P, p.S = a.P / kPT, p.U = a.H / a.G * p.S;
+    p.G = a.G, p.H = a.H, p.K = a.K, p.P = a.P, p.S = a.P / kPT, p.U = a.H / a.G * p.S, p.hg = a.H / a.G, p.sh = p.S == 2;
     p.softplus = a.softplus, p.dt_f32 = a.dt_dtype == GDN_DTYPE_F32, p.dts = a.dts, p.dt = a.dt;
     p.A = a.A, p.D = a.D, p.dt_bias = a.dt_bias, p.gates = gates, p.status = a.status;
     return p;

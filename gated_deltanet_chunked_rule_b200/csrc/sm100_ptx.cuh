@@ -248,6 +248,11 @@ __device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, uint32_t (&r)[1
           "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_ld8_nowait(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
 // Waits for every tcgen05.ld of this thread; the "+r" operands tie the given registers to
 // the wait, so that the compiler cannot read them before it. Of several loads in flight the
 // first call waits, the others only tie their registers.
@@ -268,6 +273,14 @@ __device__ __forceinline__ void tmem_landed(uint32_t (&r)[16]) {
                    "+r"(r[14]), "+r"(r[15])
                  :
                  : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tmem_landed(uint32_t (&r)[N][8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        asm volatile("" : "+r"(r[i][0]), "+r"(r[i][1]), "+r"(r[i][2]), "+r"(r[i][3]), "+r"(r[i][4]), "+r"(r[i][5]),
+                          "+r"(r[i][6]), "+r"(r[i][7]));
 }
 
 // 32 lanes x 16 consecutive 32-bit columns: thread t gets lane (warp's lane
