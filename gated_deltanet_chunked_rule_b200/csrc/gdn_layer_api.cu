@@ -272,7 +272,7 @@ int gdn_scan_fwd(const gdn_scan_problem *p, const void *x, const void *dt, const
     if (!(a.status = status_ptr())) return GDN_ERR_CUDA;
     if (scan_on_tensor_cores(a)) return finish(scan_fwd_tc(a));
     TimedLaunch t("scan_fwd", a.stream);
-    return finish(launch_scan_step(a));
+    return finish(launch_scan_simt_fwd(a));
 }
 
 int gdn_scan_step(const gdn_scan_problem *p, const void *x, const void *dt, const float *A, const void *B, const void *C,

@@ -203,6 +203,51 @@ scan_forward_kernel(ScanP p, const Tin *__restrict__ x, const Tdt *__restrict__ 
         for (int i = 0; i < 32; ++i) final_state[at + (size_t)(32 * w + i) * p.P] = hr[i];
 }
 
+// The decode step: a few tokens per sequence. The state's loads are issued before anything else and
+// nothing is staged ahead, so that few registers and seven CTAs per SM keep the memory busy:
+// 256 sequences x 64 heads of 128 x 64 (1.07 GB of state in and out) at 90 % of the copy rate; through
+// the prompt kernel's 16-token tiles it was half of that.
+template <typename Tin, typename Tdt, int K>
+__global__ void __launch_bounds__(K)
+scan_step_kernel(ScanP p, const Tin *__restrict__ x, const Tdt *__restrict__ dt, const Tin *__restrict__ B, const Tin *__restrict__ C,
+                 const float *h0, Tin *__restrict__ y, float *final_state, unsigned *status) {
+    __shared__ float bs[K], cs[K], red[K / 32][kCols];
+    const int n = blockIdx.x, h = blockIdx.y, c0 = blockIdx.z * kCols, g = h / (p.H / p.G);
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    if (p.m.cu && n == 0 && h == 0 && blockIdx.z == 0) check_cu(p.m, status, tid, K);
+    const int t0 = p.m.begin(n), len = p.m.end(n) - t0;
+    const size_t at = ((size_t)n * p.H + h) * K * p.P + c0 + lane;
+    float hr[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) hr[i] = h0 ? h0[at + (size_t)(32 * w + i) * p.P] : 0.f;
+    const float A = p.A[h], D = p.D ? p.D[h] : 0.f, bias = p.dt_bias ? p.dt_bias[h] : 0.f;
+    for (int i = 0; i < len; ++i) {
+        const size_t t = (size_t)(t0 + i);
+        bs[tid] = to_f32(B[t * p.bs + (size_t)g * K + tid]);
+        cs[tid] = to_f32(C[t * p.cs + (size_t)g * K + tid]);
+        const float xv = to_f32(x[t * p.xs + (size_t)h * p.P + c0 + lane]);
+        const float d = delta_of(to_f32(dt[t * p.dts + h]) + bias, p.softplus), a = expf(d * A), dx = d * xv;
+        __syncthreads();
+        float yv = 0.f;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+            hr[k] = fmaf(bs[32 * w + k], dx, a * hr[k]);
+            yv = fmaf(cs[32 * w + k], hr[k], yv);
+        }
+        red[w][lane] = yv;
+        __syncthreads();
+        if (w == 0) {
+            yv = 0.f;
+#pragma unroll
+            for (int k = 0; k < K / 32; ++k) yv += red[k][lane];
+            y[(t * p.H + h) * p.P + c0 + lane] = from_f32<Tin>(fmaf(D, xv, yv));
+        }
+    }
+    if (final_state)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) final_state[at + (size_t)(32 * w + i) * p.P] = hr[i];
+}
+
 // The gradient's reverse half: dx, dB parts (without delta), v and w, <h, i> at the end of every
 // tile [slots, H, P/32], dh0.
 template <typename Tin, typename Tdt, int K>
@@ -389,6 +434,14 @@ cudaError_t forward(const ScanArgs &a) {
 }
 
 template <typename Tin, typename Tdt, int K>
+cudaError_t step(const ScanArgs &a) {
+    const dim3 grid(a.seq.N, a.H, a.P / kCols);
+    scan_step_kernel<Tin, Tdt, K><<<grid, K, 0, a.stream>>>(params(a), (const Tin *)a.x, (const Tdt *)a.dt, (const Tin *)a.B,
+                                                           (const Tin *)a.C, a.h0, (Tin *)a.y, a.final_state, a.status);
+    return cudaGetLastError();
+}
+
+template <typename Tin, typename Tdt, int K>
 cudaError_t backward(const ScanArgs &a) {
     const ScanP p = params(a);
     const SimtWs w = simt_ws(a);
@@ -409,16 +462,22 @@ cudaError_t backward(const ScanArgs &a) {
     return launch_scan_sum(part, slots, a);
 }
 
-template <typename Tin, typename Tdt>
-cudaError_t by_k(const ScanArgs &a, bool bwd) {
-    if (a.K == 128) return bwd ? backward<Tin, Tdt, 128>(a) : forward<Tin, Tdt, 128>(a);
-    return bwd ? backward<Tin, Tdt, 64>(a) : forward<Tin, Tdt, 64>(a);
+enum Pass { kForward, kStep, kBackward };
+
+template <typename Tin, typename Tdt, int K>
+cudaError_t run_pass(const ScanArgs &a, Pass pass) {
+    return pass == kForward ? forward<Tin, Tdt, K>(a) : pass == kStep ? step<Tin, Tdt, K>(a) : backward<Tin, Tdt, K>(a);
 }
 
-cudaError_t dispatch(const ScanArgs &a, bool bwd) {
+template <typename Tin, typename Tdt>
+cudaError_t by_k(const ScanArgs &a, Pass pass) {
+    return a.K == 128 ? run_pass<Tin, Tdt, 128>(a, pass) : run_pass<Tin, Tdt, 64>(a, pass);
+}
+
+cudaError_t dispatch(const ScanArgs &a, Pass pass) {
     if (a.seq.N == 0) return cudaSuccess;
-    if (a.dtype == GDN_DTYPE_F32) return by_k<float, float>(a, bwd);
-    return a.dt_dtype == GDN_DTYPE_F32 ? by_k<__nv_bfloat16, float>(a, bwd) : by_k<__nv_bfloat16, __nv_bfloat16>(a, bwd);
+    if (a.dtype == GDN_DTYPE_F32) return by_k<float, float>(a, pass);
+    return a.dt_dtype == GDN_DTYPE_F32 ? by_k<__nv_bfloat16, float>(a, pass) : by_k<__nv_bfloat16, __nv_bfloat16>(a, pass);
 }
 
 }  // namespace
@@ -428,8 +487,9 @@ cudaError_t launch_scan_sum(const float *part, int slots, const ScanArgs &a) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_scan_step(const ScanArgs &a) { return dispatch(a, false); }
+cudaError_t launch_scan_step(const ScanArgs &a) { return dispatch(a, kStep); }
+cudaError_t launch_scan_simt_fwd(const ScanArgs &a) { return dispatch(a, kForward); }
 size_t scan_simt_bwd_bytes(const ScanArgs &a) { return simt_ws(a).total; }
-cudaError_t launch_scan_simt_bwd(const ScanArgs &a) { return dispatch(a, true); }
+cudaError_t launch_scan_simt_bwd(const ScanArgs &a) { return dispatch(a, kBackward); }
 
 }  // namespace gdn

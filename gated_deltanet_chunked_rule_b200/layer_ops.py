@@ -18,41 +18,53 @@ off a 16-byte boundary) is copied first. This module only marshals arguments, as
 """
 from __future__ import annotations
 
-import ctypes
+from ctypes import byref
+
 import torch
 from torch.autograd.function import once_differentiable
 
 from . import _binding as _b
-from .api import _DTYPES, _ptr, _stream
+from .api import _DTYPES
 
 _F32 = torch.float32
 
 
-class _on:
-    """Makes `dev` current for a launch (cheaply, where it already is)."""
-
-    def __init__(self, dev):
-        self.guard = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *e):
-        if self.guard is not None:
-            self.guard.__exit__(*e)
+def _call(dev, name, *args):
+    """Launches with `dev` current, on its current stream (the last argument)."""
+    fn = getattr(_b.lib(), name)
+    index = dev.index
+    if index == torch.cuda.current_device():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if rc:
+        _b.check(name, rc)
 
 
-def _check(dev, want):
-    """Every tensor the library reads or writes: {name: (tensor or None, shape, dtype)}."""
-    for name, (t, shape, dtype) in want.items():
+def _size(dev, name, P):
+    """A size query with `dev` current."""
+    fn = getattr(_b.lib(), name)
+    if dev.index == torch.cuda.current_device():
+        return fn(byref(P))
+    with torch.cuda.device(dev):
+        return fn(byref(P))
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _check(dev, *want):
+    """Every tensor the library reads or writes: (name, tensor or None, shape, dtype)."""
+    for name, t, shape, dtype in want:
         if t is None:
             continue
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
         if t.device != dev:
             raise ValueError(f"{name} is on {t.device}, expected {dev}")
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
         if t.shape != shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
@@ -61,7 +73,7 @@ def _check(dev, want):
 def _cuda(x, name="x"):
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if x.device.type != "cuda":
+    if not x.is_cuda:
         raise ValueError(f"inputs must be CUDA tensors (got {x.device}); the library has no CPU path")
     if x.dtype not in _DTYPES:
         raise TypeError(f"unsupported dtype {x.dtype}")
@@ -84,17 +96,20 @@ def _in_place(name, t):
 def _tokens(t, width, step=1, align=16):
     """(tensor, token stride in elements) of a [B, T, ...] input whose tokens are `width`
     contiguous elements, a constant stride apart that is a multiple of `step`."""
-    B, T = t.shape[0], t.shape[1]
+    if t.is_contiguous():
+        return (t if t.data_ptr() % align == 0 else t.clone()), width
+    shape, stride = t.shape, t.stride()
+    B, T = shape[0], shape[1]
     n, ok = 1, True
-    for size, st in zip(reversed(t.shape[2:]), reversed(t.stride()[2:])):
-        ok &= size == 1 or st == n
-        n *= size
-    st = width if B * T <= 1 else t.stride(0) if T == 1 else t.stride(1)
+    for i in range(len(shape) - 1, 1, -1):
+        ok &= shape[i] == 1 or stride[i] == n
+        n *= shape[i]
+    st = width if B * T <= 1 else stride[0] if T == 1 else stride[1]
     if T > 1 and B > 1:
-        ok &= t.stride(0) == T * st
+        ok &= stride[0] == T * st
     if ok and st >= width and st % step == 0 and t.data_ptr() % align == 0:
         return t, st
-    return (t.contiguous() if not t.is_contiguous() else t.clone()), width
+    return t.contiguous(), width
 
 
 def _packed(cu_seqlens, B, dev):
@@ -121,7 +136,7 @@ def _conv(x, weight, bias, activation, cu_seqlens):
         raise ValueError(f"weight must be [C, W] with W in 2..4, got {tuple(weight.shape)}")
     W = weight.shape[1]
     cu, ns, N = _packed(cu_seqlens, B, dev)
-    _check(dev, {"weight": (weight, (C, W), x.dtype), "bias": (bias, (C,), x.dtype)})
+    _check(dev, ("weight", weight, (C, W), x.dtype), ("bias", bias, (C,), x.dtype))
     x, st = _tokens(x, C)
     P = _b.gdn_conv_problem(B, T, C, W, ns, None if cu is None else cu.data_ptr(), _DTYPES[x.dtype],
                             activation is not None, st)
@@ -134,33 +149,28 @@ def causal_conv1d_fwd(x, weight, bias=None, activation=None, initial_state=None,
     states [N, W-1, C] (the inputs before the first and up to the last token, oldest first),
     all of one dtype; activation None or "silu". Returns (y, final_state or None)."""
     dev, x, weight, bias, P, cu, state = _conv(x, weight, bias, activation, cu_seqlens)
-    _check(dev, {"initial_state": (initial_state, state, x.dtype)})
+    _check(dev, ("initial_state", initial_state, state, x.dtype))
     initial_state = _dense(initial_state)
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    fin = torch.empty(state, dtype=x.dtype, device=dev) if output_final_state else None
-    with _on(dev):
-        rc = _b.lib().gdn_conv_fwd(ctypes.byref(P), _ptr(x), _ptr(weight), _ptr(bias), _ptr(initial_state), _ptr(y),
-                                   _ptr(fin), _stream(dev))
-    _b.check("gdn_conv_fwd", rc)
+    y = x.new_empty(x.shape)
+    fin = x.new_empty(state) if output_final_state else None
+    _call(dev, "gdn_conv_fwd", byref(P), x.data_ptr(), _p(weight), _p(bias), _p(initial_state), y.data_ptr(), _p(fin))
     return y, fin
 
 
 def causal_conv1d_bwd(x, weight, bias, dy, dfinal=None, activation=None, initial_state=None, cu_seqlens=None):
     """Returns (dx, dweight, dbias or None, dinitial_state or None)."""
     dev, x, weight, bias, P, cu, state = _conv(x, weight, bias, activation, cu_seqlens)
-    _check(dev, {"initial_state": (initial_state, state, x.dtype), "dy": (dy, x.shape, x.dtype),
-                 "dfinal": (dfinal, state, x.dtype)})
+    _check(dev, ("initial_state", initial_state, state, x.dtype), ("dy", dy, x.shape, x.dtype),
+           ("dfinal", dfinal, state, x.dtype))
     initial_state, dy, dfinal = _dense(initial_state), _dense(dy), _dense(dfinal)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    dx = x.new_empty(x.shape)
     dw = torch.empty_like(weight)
     db = torch.empty_like(bias) if bias is not None else None
     ds = torch.empty_like(initial_state) if initial_state is not None else None
-    n = _b.lib().gdn_conv_bwd_workspace_size(ctypes.byref(P))
-    ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    with _on(dev):
-        rc = _b.lib().gdn_conv_bwd(ctypes.byref(P), _ptr(x), _ptr(weight), _ptr(bias), _ptr(initial_state), _ptr(dy),
-                                   _ptr(dfinal), _ptr(dx), _ptr(dw), _ptr(db), _ptr(ds), _ptr(ws), n, _stream(dev))
-    _b.check("gdn_conv_bwd", rc)
+    n = _size(dev, "gdn_conv_bwd_workspace_size", P)
+    ws = x.new_empty(n, dtype=torch.uint8)
+    _call(dev, "gdn_conv_bwd", byref(P), x.data_ptr(), _p(weight), _p(bias), _p(initial_state), _p(dy), _p(dfinal),
+          dx.data_ptr(), dw.data_ptr(), _p(db), _p(ds), ws.data_ptr(), n)
     return dx, dw, db, ds
 
 
@@ -168,15 +178,12 @@ def causal_conv1d_update(x, conv_state, weight, bias=None, activation=None):
     """The next few tokens of every sequence: x [B, T, C]; conv_state [B, W-1, C] is updated
     in place. Returns y [B, T, C]."""
     dev, x, weight, bias, P, _, state = _conv(x, weight, bias, activation, None)
-    _check(dev, {"conv_state": (conv_state, state, x.dtype)})
+    _check(dev, ("conv_state", conv_state, state, x.dtype))
     if conv_state is None:
         raise ValueError("conv_state is required")
     _in_place("conv_state", conv_state)
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    with _on(dev):
-        rc = _b.lib().gdn_conv_update(ctypes.byref(P), _ptr(x), _ptr(weight), _ptr(bias), _ptr(conv_state), _ptr(y),
-                                      _stream(dev))
-    _b.check("gdn_conv_update", rc)
+    y = x.new_empty(x.shape)
+    _call(dev, "gdn_conv_update", byref(P), x.data_ptr(), _p(weight), _p(bias), conv_state.data_ptr(), y.data_ptr())
     return y
 
 
@@ -220,9 +227,9 @@ class _Scan:
             raise TypeError(f"dt has dtype {dt.dtype}, expected {x.dtype} or {_F32}")
         self.cu, ns, N = _packed(cu_seqlens, b, dev)
         self.state = (N, H, K, V)
-        _check(dev, {"B": (B, (b, T, G, K), x.dtype), "C": (C, (b, T, G, K), x.dtype), "dt": (dt, (b, T, H), dt.dtype),
-                     "A": (A, (H,), _F32), "D": (D, (H,), _F32), "dt_bias": (dt_bias, (H,), _F32),
-                     "initial_state": (h0, self.state, _F32)})
+        _check(dev, ("B", B, (b, T, G, K), x.dtype), ("C", C, (b, T, G, K), x.dtype), ("dt", dt, (b, T, H), dt.dtype),
+               ("A", A, (H,), _F32), ("D", D, (H,), _F32), ("dt_bias", dt_bias, (H,), _F32),
+               ("initial_state", h0, self.state, _F32))
         step = 16 // x.element_size()
         self.x, xs = _tokens(x, H * V, step)
         self.B, bs = _tokens(B, G * K, step)
@@ -232,18 +239,18 @@ class _Scan:
         self.P = _b.gdn_scan_problem(b, T, G, H, K, V, ns, None if self.cu is None else self.cu.data_ptr(),
                                      _DTYPES[x.dtype], _DTYPES[dt.dtype], bool(dt_softplus), xs, bs, cs, ds)
 
-    def ref(self):
-        return ctypes.byref(self.P)
-
     def inputs(self):
-        return (_ptr(self.x), _ptr(self.dt), _ptr(self.A), _ptr(self.B), _ptr(self.C), _ptr(self.D), _ptr(self.dt_bias),
-                _ptr(self.h0))
+        return (byref(self.P), self.x.data_ptr(), self.dt.data_ptr(), self.A.data_ptr(), self.B.data_ptr(), self.C.data_ptr(),
+                _p(self.D), _p(self.dt_bias), _p(self.h0))
 
     def empty(self, like):
-        return torch.empty(like.shape, dtype=like.dtype, device=self.dev)
+        return like.new_empty(like.shape)
 
     def bytes(self, n):
-        return torch.empty(n, dtype=torch.uint8, device=self.dev)
+        return self.x.new_empty(n, dtype=torch.uint8)
+
+    def states(self):
+        return self.x.new_empty(self.state, dtype=_F32)
 
 
 def chunk_selective_scan_fwd(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus=False, initial_state=None,
@@ -252,15 +259,12 @@ def chunk_selective_scan_fwd(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus=F
     dtype), A, D, dt_bias [H] fp32, B and C [B, T, G, K] (H a multiple of G), states
     [N, H, K, V] fp32. Returns (y, final_state or None, saved or None)."""
     s = _Scan(x, dt, A, B, C, D, dt_bias, dt_softplus, initial_state, cu_seqlens)
-    L = _b.lib()
     y = s.empty(x)
-    fin = torch.empty(s.state, dtype=_F32, device=s.dev) if output_final_state else None
-    with _on(s.dev):
-        saved = s.bytes(L.gdn_scan_saved_size(s.ref())) if save_for_backward else None
-        n = L.gdn_scan_fwd_workspace_size(s.ref())
-        ws = s.bytes(n) if n else None
-        rc = L.gdn_scan_fwd(s.ref(), *s.inputs(), _ptr(y), _ptr(fin), _ptr(saved), _ptr(ws), n, _stream(s.dev))
-    _b.check("gdn_scan_fwd", rc)
+    fin = s.states() if output_final_state else None
+    saved = s.bytes(_size(s.dev, "gdn_scan_saved_size", s.P)) if save_for_backward else None
+    n = _size(s.dev, "gdn_scan_fwd_workspace_size", s.P)
+    ws = s.bytes(n) if n else None
+    _call(s.dev, "gdn_scan_fwd", *s.inputs(), y.data_ptr(), _p(fin), _p(saved), _p(ws), n)
     return y, fin, saved
 
 
@@ -269,25 +273,23 @@ def chunk_selective_scan_bwd(x, dt, A, B, C, D, dt_bias, dt_softplus, saved, dy,
     """Returns (dx, ddt, dA, dB, dC, dD, ddt_bias, dh0); dD, ddt_bias None where the input is.
     `saved` is what the forward kept, or None (recomputed)."""
     s = _Scan(x, dt, A, B, C, D, dt_bias, dt_softplus, initial_state, cu_seqlens)
-    L = _b.lib()
-    _check(s.dev, {"dy": (dy, x.shape, x.dtype), "dht": (dht, s.state, _F32)})
+    _check(s.dev, ("dy", dy, x.shape, x.dtype), ("dht", dht, s.state, _F32))
     dy, dht = _dense(dy), _dense(dht)
     dx, ddt, dB, dC, dA = s.empty(x), s.empty(dt), s.empty(B), s.empty(C), s.empty(A)
     dD = s.empty(D) if D is not None else None
     db = s.empty(dt_bias) if dt_bias is not None else None
-    dh0 = torch.empty(s.state, dtype=_F32, device=s.dev)
-    with _on(s.dev):
-        if saved is not None:
-            _check(s.dev, {"saved": (saved, saved.shape, torch.uint8)})
-            need = L.gdn_scan_saved_size(s.ref())
-            if saved.numel() < need:
-                raise ValueError(f"saved holds {saved.numel()} bytes, the problem needs {need}")
-        n = L.gdn_scan_bwd_workspace_size(s.ref())
-        ws = s.bytes(n)
-        rc = L.gdn_scan_bwd(s.ref(), *s.inputs(), _ptr(saved if saved is not None and saved.numel() else None), _ptr(dy),
-                            _ptr(dht), _ptr(dx), _ptr(ddt), _ptr(dA), _ptr(dB), _ptr(dC), _ptr(dD), _ptr(db), _ptr(dh0),
-                            _ptr(ws), n, _stream(s.dev))
-    _b.check("gdn_scan_bwd", rc)
+    dh0 = s.states()
+    if saved is not None:
+        _check(s.dev, ("saved", saved, saved.shape, torch.uint8))
+        need = _size(s.dev, "gdn_scan_saved_size", s.P)
+        if saved.numel() < need:
+            raise ValueError(f"saved holds {saved.numel()} bytes, the problem needs {need}")
+        if not need:
+            saved = None
+    n = _size(s.dev, "gdn_scan_bwd_workspace_size", s.P)
+    ws = s.bytes(n)
+    _call(s.dev, "gdn_scan_bwd", *s.inputs(), _p(_dense(saved)), dy.data_ptr(), _p(dht), dx.data_ptr(), ddt.data_ptr(),
+          dA.data_ptr(), dB.data_ptr(), dC.data_ptr(), _p(dD), _p(db), dh0.data_ptr(), ws.data_ptr(), n)
     return dx, ddt, dA, dB, dC, dD, db, dh0
 
 
@@ -296,15 +298,13 @@ def recurrent_selective_scan(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus=F
     """Token by token, for a few tokens per sequence (decoding). Returns (y, final_state);
     `final_state` may be `initial_state` itself (updated in place)."""
     s = _Scan(x, dt, A, B, C, D, dt_bias, dt_softplus, initial_state, cu_seqlens)
-    _check(s.dev, {"final_state": (final_state, s.state, _F32)})
+    _check(s.dev, ("final_state", final_state, s.state, _F32))
     if final_state is None:
-        final_state = torch.empty(s.state, dtype=_F32, device=s.dev)
+        final_state = s.states()
     else:
         _in_place("final_state", final_state)
     y = s.empty(x)
-    with _on(s.dev):
-        rc = _b.lib().gdn_scan_step(s.ref(), *s.inputs(), _ptr(y), _ptr(final_state), _stream(s.dev))
-    _b.check("gdn_scan_step", rc)
+    _call(s.dev, "gdn_scan_step", *s.inputs(), y.data_ptr(), final_state.data_ptr())
     return y, final_state
 
 
@@ -350,7 +350,7 @@ def _norm(x, weight, bias, gate, eps, center, gate_first):
     if gate_first and gate is None:
         raise ValueError("gate_first needs a gate")
     D = x.shape[-1]
-    _check(dev, {"weight": (weight, (D,), weight.dtype), "bias": (bias, (D,), weight.dtype), "gate": (gate, x.shape, x.dtype)})
+    _check(dev, ("weight", weight, (D,), weight.dtype), ("bias", bias, (D,), weight.dtype), ("gate", gate, x.shape, x.dtype))
     P = _b.gdn_norm_problem(x.numel() // D, D, _DTYPES[x.dtype], _DTYPES[weight.dtype], bool(center), bool(gate_first),
                             float(eps))
     return dev, _dense(x), _dense(weight), _dense(bias), _dense(gate), P
@@ -362,28 +362,23 @@ def layer_norm_fwd(x, weight, bias=None, gate=None, eps=1e-5, center=True, gate_
     x's dtype). Returns (y, stats); stats [rows, 2] fp32 is the backward's."""
     dev, x, weight, bias, gate, P = _norm(x, weight, bias, gate, eps, center, gate_first)
     y = torch.empty_like(x)
-    stats = torch.empty((P.rows, 2), dtype=_F32, device=dev)
-    with _on(dev):
-        rc = _b.lib().gdn_norm_fwd(ctypes.byref(P), _ptr(x), _ptr(weight), _ptr(bias), _ptr(gate), _ptr(y), _ptr(stats),
-                                   _stream(dev))
-    _b.check("gdn_norm_fwd", rc)
+    stats = x.new_empty((P.rows, 2), dtype=_F32)
+    _call(dev, "gdn_norm_fwd", byref(P), x.data_ptr(), weight.data_ptr(), _p(bias), _p(gate), y.data_ptr(), stats.data_ptr())
     return y, stats
 
 
 def layer_norm_bwd(x, weight, bias, gate, dy, stats, eps=1e-5, center=True, gate_first=False):
     """Returns (dx, dweight, dbias or None, dgate or None)."""
     dev, x, weight, bias, gate, P = _norm(x, weight, bias, gate, eps, center, gate_first)
-    _check(dev, {"dy": (dy, x.shape, x.dtype), "stats": (stats, (P.rows, 2), _F32)})
+    _check(dev, ("dy", dy, x.shape, x.dtype), ("stats", stats, (P.rows, 2), _F32))
     dy, stats = _dense(dy), _dense(stats)
     dx, dw = torch.empty_like(x), torch.empty_like(weight)
     db = torch.empty_like(bias) if bias is not None else None
     dg = torch.empty_like(gate) if gate is not None else None
-    with _on(dev):
-        n = _b.lib().gdn_norm_bwd_workspace_size(ctypes.byref(P))
-        ws = torch.empty(n, dtype=torch.uint8, device=dev)
-        rc = _b.lib().gdn_norm_bwd(ctypes.byref(P), _ptr(x), _ptr(weight), _ptr(bias), _ptr(gate), _ptr(dy), _ptr(stats),
-                                   _ptr(dx), _ptr(dw), _ptr(db), _ptr(dg), _ptr(ws), n, _stream(dev))
-    _b.check("gdn_norm_bwd", rc)
+    n = _size(dev, "gdn_norm_bwd_workspace_size", P)
+    ws = x.new_empty(n, dtype=torch.uint8)
+    _call(dev, "gdn_norm_bwd", byref(P), x.data_ptr(), weight.data_ptr(), _p(bias), _p(gate), dy.data_ptr(), stats.data_ptr(),
+          dx.data_ptr(), dw.data_ptr(), _p(db), _p(dg), ws.data_ptr(), n)
     return dx, dw, db, dg
 
 
