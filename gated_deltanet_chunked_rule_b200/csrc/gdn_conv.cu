@@ -25,6 +25,7 @@ constexpr int kWarps = 4;   // runs per block
 constexpr int kRunF = 32;   // tokens of a forward run
 constexpr int kRunB = 32;   // tokens of a backward run
 constexpr int kAhead = 8;   // rows loaded together
+constexpr int kAheadB = 4;  // (each of x and dy) in the backward
 
 struct ConvP {
     SeqMap m;
@@ -33,10 +34,11 @@ struct ConvP {
     long long xs;
 };
 
-// VEC consecutive channels of a row as loaded: four words of one or two elements (or one element).
+// VEC consecutive channels of a row as loaded: two or four words of one or two elements (or one
+// element).
 template <typename T, int VEC>
 struct Pack {
-    static constexpr int kWords = VEC == 1 ? 1 : 4, kPer = VEC / kWords;
+    static constexpr int kWords = VEC == 1 ? 1 : VEC * (int)sizeof(T) / 4, kPer = VEC / kWords;
     uint32_t w[kWords];
     __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -45,6 +47,9 @@ struct Pack {
     __device__ __forceinline__ void load(const T *p) {
         if constexpr (VEC == 1) {
             w[0] = __float_as_uint(to_f32(*p));
+        } else if constexpr (kWords == 2) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(p);
+            w[0] = v.x, w[1] = v.y;
         } else {
             const uint4 v = *reinterpret_cast<const uint4 *>(p);
             w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
@@ -52,6 +57,7 @@ struct Pack {
     }
     __device__ __forceinline__ void store(T *p) const {
         if constexpr (VEC == 1) *p = from_f32<T>(__uint_as_float(w[0]));
+        else if constexpr (kWords == 2) *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
         else *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     }
     __device__ __forceinline__ float get(int k, int e) const {
@@ -68,7 +74,7 @@ struct Pack {
     }
 };
 
-// The taps and bias of VEC channels: contiguous in memory, 16-byte pieces where VEC > 1.
+// The taps and bias of VEC channels, contiguous in memory.
 template <typename T, int VEC, int W>
 struct Taps {
     using P = Pack<T, VEC>;
@@ -236,13 +242,13 @@ __device__ __forceinline__ void backward_rows(const Taps<T, VEC, W> &t, bool sil
     for (int i = 0; i < W - 1; ++i) hist[i] = next[i];
 }
 
-template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(32 * kWarps, 3)
+template <typename T, int VEC, int W, int UB>
+__global__ void __launch_bounds__(32 * kWarps, VEC == 8 ? 3 : VEC * sizeof(T) == 16 ? 4 : 5)
 conv_bwd_kernel(ConvP p, const T *__restrict__ x, const T *__restrict__ weight, const T *__restrict__ bias,
                 const T *__restrict__ state, const T *__restrict__ dy, const T *__restrict__ dfinal, T *__restrict__ dx,
                 float *__restrict__ part, unsigned *status) {
     using P = Pack<T, VEC>;
-    constexpr int U = kAhead / 2;
+    constexpr int U = UB;
     __shared__ float red[kWarps][(W + 1) * VEC][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (blockIdx.x == 0 && blockIdx.y == 0) check_cu(p.m, status, threadIdx.x, blockDim.x);
@@ -455,7 +461,7 @@ cudaError_t run_pass(const ConvArgs &a, Pass pass) {
         const int blocks = (a.seq.total + kRunB * kWarps - 1) / (kRunB * kWarps);
         if (blocks) {
             TimedLaunch tl("conv_bwd", a.stream);
-            conv_bwd_kernel<T, VEC, W><<<dim3(blocks, cb), 32 * kWarps, 0, a.stream>>>(p, x, w, b, st, dy, df, (T *)a.dx, a.part,
+            conv_bwd_kernel<T, VEC, W, kAheadB><<<dim3(blocks, cb), 32 * kWarps, 0, a.stream>>>(p, x, w, b, st, dy, df, (T *)a.dx, a.part,
                                                                                       a.status);
         }
         TimedLaunch tl("conv_bwd_sums", a.stream);
@@ -487,8 +493,9 @@ cudaError_t by_taps(const ConvArgs &a, Pass pass) {
 
 cudaError_t dispatch(const ConvArgs &a, Pass pass) {
     const bool v = vectorized(a);
+    // the backward holds ten registers per channel: four channels per thread let twice as many warps run
     if (a.dtype == GDN_DTYPE_BF16)
-        return v ? by_taps<__nv_bfloat16, 8>(a, pass) : by_taps<__nv_bfloat16, 1>(a, pass);
+        return !v ? by_taps<__nv_bfloat16, 1>(a, pass) : pass == kBwd ? by_taps<__nv_bfloat16, 4>(a, pass) : by_taps<__nv_bfloat16, 8>(a, pass);
     return v ? by_taps<float, 4>(a, pass) : by_taps<float, 1>(a, pass);
 }
 

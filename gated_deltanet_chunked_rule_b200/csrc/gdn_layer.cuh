@@ -171,6 +171,7 @@ struct ScanArgs {
 };
 cudaError_t launch_scan_step(const ScanArgs &a);
 cudaError_t launch_scan_simt_fwd(const ScanArgs &a);
+size_t scan_simt_fwd_bytes(const ScanArgs &a);
 size_t scan_simt_bwd_bytes(const ScanArgs &a);
 cudaError_t launch_scan_simt_bwd(const ScanArgs &a);
 // dA, ddt_bias, dD from parts [slots, 3, H].

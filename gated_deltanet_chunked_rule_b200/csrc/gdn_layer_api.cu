@@ -239,7 +239,8 @@ size_t gdn_scan_saved_size(const gdn_scan_problem *p) {
 
 size_t gdn_scan_fwd_workspace_size(const gdn_scan_problem *p) {
     ScanArgs a;
-    return scan_args(p, &a) == GDN_OK && scan_on_tensor_cores(a) ? scan_fwd_layout(a).total : 0;
+    if (scan_args(p, &a) != GDN_OK) return 0;
+    return scan_on_tensor_cores(a) ? scan_fwd_layout(a).total : scan_simt_fwd_bytes(a);
 }
 
 size_t gdn_scan_bwd_workspace_size(const gdn_scan_problem *p) {

@@ -8,7 +8,8 @@
 //
 // Memory-bound. A group of 8, 16, 32 or 256 threads owns a row and keeps it in registers
 // between its passes (mean, then the centred sum of squares, then the result), so every
-// tensor moves once. Groups walk the rows with a stride, the weights and the weight
+// tensor moves once, and the next row's loads are in flight meanwhile. Groups walk the rows with
+// a stride, as many blocks as fit at once (one wave), the weights and the weight
 // gradient's sums staying in registers; the sums (fp32) are joined over a block's groups in
 // shared memory and over the blocks by a second kernel, in a fixed order. Rows that are
 // too long for the registers, or whose width or addresses do not allow 16-byte accesses,
@@ -87,25 +88,32 @@ norm_fwd_kernel(NormP p, const T *__restrict__ x, const void *__restrict__ weigh
             b[i][e] = v < nv && bias ? load_w(bias, wf32, v * VEC + e) : 0.f;
         }
     int phase = 0;
-    // whole blocks walk together, so that the barriers and shuffles stay uniform
-    for (long long r0 = (long long)blockIdx.x * kGroups; r0 < p.R; r0 += (long long)gridDim.x * kGroups) {
-        const long long r = r0 + g;
-        const bool live = r < p.R;
-        float u[NV][VEC];
-        Raw<T, VEC> z[NV];
-        float s[1] = {0.f};
+    Raw<T, VEC> q[NV], z[NV];
+    auto fetch = [&](long long r) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int v = i * TPR + l;
-            const bool in = live && v < nv;
-            Raw<T, VEC> q;
-            q.v = make_uint4(0, 0, 0, 0);
-            z[i].v = make_uint4(0, 0, 0, 0);
-            if (in) q.load(x + r * p.D + v * VEC);
-            if (GATE && in) z[i].load(gate + r * p.D + v * VEC);
+            q[i].v = z[i].v = make_uint4(0, 0, 0, 0);
+            if (r >= p.R || v >= nv) continue;
+            q[i].load(x + r * p.D + v * VEC);
+            if (GATE) z[i].load(gate + r * p.D + v * VEC);
+        }
+    };
+    const long long stride = (long long)gridDim.x * kGroups;
+    fetch((long long)blockIdx.x * kGroups + g);
+    // whole blocks walk together, so that the barriers and shuffles stay uniform
+    for (long long r0 = (long long)blockIdx.x * kGroups; r0 < p.R; r0 += stride) {
+        const long long r = r0 + g;
+        const bool live = r < p.R;
+        float u[NV][VEC];
+        Raw<T, VEC> zc[NV];
+        float s[1] = {0.f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            zc[i] = z[i];
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                u[i][e] = q.get(e);
+                u[i][e] = q[i].get(e);
                 if (GATE == 1) {
                     const float zz = z[i].get(e);
                     u[i][e] *= zz * sigmoid<kFast>(zz);
@@ -113,6 +121,7 @@ norm_fwd_kernel(NormP p, const T *__restrict__ x, const void *__restrict__ weigh
                 s[0] += u[i][e];
             }
         }
+        fetch(r + stride);
         float mean = 0.f;
         if (CENTER) {
             row_sum<TPR, 1>(s, buf, phase);
@@ -144,7 +153,7 @@ norm_fwd_kernel(NormP p, const T *__restrict__ x, const void *__restrict__ weigh
             for (int e = 0; e < VEC; ++e) {
                 o[e] = fmaf(u[i][e] * rstd, w[i][e], b[i][e]);
                 if (GATE == 2) {
-                    const float zz = z[i].get(e);
+                    const float zz = zc[i].get(e);
                     o[e] *= zz * sigmoid<kFast>(zz);
                 }
             }
@@ -174,40 +183,61 @@ norm_bwd_kernel(NormP p, const T *__restrict__ x, const void *__restrict__ weigh
             dw[i][e] = db[i][e] = 0.f;
         }
     int phase = 0;
-    for (long long r0 = (long long)blockIdx.x * kGroups; r0 < p.R; r0 += (long long)gridDim.x * kGroups) {
-        const long long r = r0 + g;
-        const bool live = r < p.R;
-        Raw<T, VEC> q[NV], z[NV], d[NV];
-        const float mean = live ? stats[2 * r] : 0.f, rstd = live ? stats[2 * r + 1] : 0.f;
+    Raw<T, VEC> q[NV], z[NV], d[NV];
+    float mean = 0.f, rstd = 0.f;
+    auto fetch = [&](long long r) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int v = i * TPR + l;
             q[i].v = z[i].v = d[i].v = make_uint4(0, 0, 0, 0);
-            if (live && v < nv) {
-                q[i].load(x + r * p.D + v * VEC);
-                d[i].load(dy + r * p.D + v * VEC);
-                if (GATE) z[i].load(gate + r * p.D + v * VEC);
-            }
+            if (r >= p.R || v >= nv) continue;
+            q[i].load(x + r * p.D + v * VEC);
+            d[i].load(dy + r * p.D + v * VEC);
+            if (GATE) z[i].load(gate + r * p.D + v * VEC);
         }
+        mean = r < p.R ? stats[2 * r] : 0.f;
+        rstd = r < p.R ? stats[2 * r + 1] : 0.f;
+    };
+    const long long stride = (long long)gridDim.x * kGroups;
+    // short rows keep what the second pass needs, and the next row is fetched meanwhile; long ones
+    // keep the row as it was loaded and compute it again
+    constexpr bool kKeep = NV <= 2;
+    if (kKeep) fetch((long long)blockIdx.x * kGroups + g);
+    for (long long r0 = (long long)blockIdx.x * kGroups; r0 < p.R; r0 += stride) {
+        const long long r = r0 + g;
+        const bool live = r < p.R;
+        if (!kKeep) fetch(r);
+        const float mu = mean, rs = rstd;
         float s[2] = {0.f, 0.f};
+        // n; dn; gate first: silu(z), x silu'(z)
+        float kn[kKeep ? NV : 1][VEC], kd[kKeep ? NV : 1][VEC], ka[kKeep && GATE == 1 ? NV : 1][VEC], kb[kKeep && GATE == 1 ? NV : 1][VEC];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (i * TPR + l >= nv) continue;
+            const int v = i * TPR + l;
+            if (v >= nv) continue;
+            float og[VEC];
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                float u = q[i].get(e), dl = d[i].get(e);
+                const float xe = q[i].get(e), de = d[i].get(e);
+                float u = xe, dl = de, dsilu = 0.f;
                 if (GATE) {
-                    const float zz = z[i].get(e), si = zz * sigmoid<kFast>(zz);
+                    const float zz = z[i].get(e), sg = sigmoid<kFast>(zz), si = zz * sg;
+                    dsilu = fmaf(si, 1.f - sg, sg);
                     if (GATE == 1) u *= si;
                     else dl *= si;
+                    if (kKeep && GATE == 1) ka[i][e] = si, kb[i][e] = xe * dsilu;
                 }
-                const float n = (u - mean) * rstd, dn = dl * w[i][e];
+                const float n = (u - mu) * rs, dn = dl * w[i][e];
                 dw[i][e] = fmaf(dl, n, dw[i][e]);
                 db[i][e] += dl;
                 s[0] = fmaf(dn, n, s[0]);
                 s[1] += dn;
+                if (kKeep) kn[i][e] = n, kd[i][e] = dn;
+                if (GATE == 2) og[e] = dsilu * de * fmaf(n, w[i][e], b[GATE == 2 ? i : 0][e]);
             }
+            if (GATE == 2 && live) store_vec<T, VEC>(dgate + r * p.D + v * VEC, og);
         }
+        if (kKeep) fetch(r + stride);
         row_sum<TPR, 2>(s, buf, phase);
         if (!live) continue;
         const float m0 = s[0] * p.inv_d, m1 = CENTER ? s[1] * p.inv_d : 0.f;
@@ -218,24 +248,25 @@ norm_bwd_kernel(NormP p, const T *__restrict__ x, const void *__restrict__ weigh
             float o[VEC], og[VEC];
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                const float xe = q[i].get(e), de = d[i].get(e);
-                float u = xe, dl = de, zz = 0.f, sg = 0.f;
-                if (GATE) {
-                    zz = z[i].get(e);
-                    sg = sigmoid<kFast>(zz);
-                    if (GATE == 1) u *= zz * sg;
-                    else dl *= zz * sg;
+                float n, dn, a = 1.f, bb = 0.f;
+                if (kKeep) {
+                    n = kn[i][e], dn = kd[i][e];
+                    if (GATE == 1) a = ka[i][e], bb = kb[i][e];
+                } else {
+                    float u = q[i].get(e), dl = d[i].get(e);
+                    if (GATE) {
+                        const float zz = z[i].get(e), sg = sigmoid<kFast>(zz), si = zz * sg;
+                        if (GATE == 1) bb = u * fmaf(si, 1.f - sg, sg), a = si, u *= si;
+                        else dl *= si;
+                    }
+                    n = (u - mu) * rs, dn = dl * w[i][e];
                 }
-                const float n = (u - mean) * rstd;
-                const float du = rstd * (dl * w[i][e] - n * m0 - m1);
-                o[e] = GATE == 1 ? du * zz * sg : du;
-                if (GATE) {
-                    const float dsilu = sg * (1.f + zz * (1.f - sg));
-                    og[e] = dsilu * (GATE == 1 ? du * xe : de * fmaf(n, w[i][e], b[GATE == 2 ? i : 0][e]));
-                }
+                const float du = rs * (dn - n * m0 - m1);
+                o[e] = GATE == 1 ? du * a : du;
+                if (GATE == 1) og[e] = du * bb;
             }
             store_vec<T, VEC>(dx + r * p.D + v * VEC, o);
-            if (GATE) store_vec<T, VEC>(dgate + r * p.D + v * VEC, og);
+            if (GATE == 1) store_vec<T, VEC>(dgate + r * p.D + v * VEC, og);
         }
     }
     // the block's sums of dweight, dbias
@@ -428,14 +459,21 @@ bool in_registers(const NormArgs &a) {
     return a.D % el == 0 && a.D / el <= kThreads * (el == 8 ? 4 : 8);
 }
 
-// Blocks that walk the rows: eight per SM of the row-in-registers kernels' forward, four
-// of their backward (its partial sums are one row per block), at most one per row group.
+// Blocks that walk the rows: as many as run at once, at most one per row group (and at most eight
+// per SM: a backward's partial sums are one row per block).
+constexpr int kMostPerSm = 8;
+
 int walk_blocks(long long groups, int per_sm) {
     const long long most = (long long)sm_count() * per_sm;
     return (int)(groups < most ? groups : most);
 }
 
-constexpr int kFwdPerSm = 8, kBwdPerSm = 4;
+template <typename Kernel>
+int resident(Kernel kernel) {
+    int n = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, 0) != cudaSuccess || n < 1) n = 1;
+    return n < kMostPerSm ? n : kMostPerSm;
+}
 
 template <typename T, int TPR, int NV, int GATE, bool CENTER>
 cudaError_t run(const NormArgs &a, bool bwd) {
@@ -443,11 +481,15 @@ cudaError_t run(const NormArgs &a, bool bwd) {
     const long long groups = (a.R + kThreads / TPR - 1) / (kThreads / TPR);
     const int wf32 = a.wdtype == GDN_DTYPE_F32;
     if (!bwd) {
-        norm_fwd_kernel<T, TPR, NV, GATE, CENTER><<<walk_blocks(groups, kFwdPerSm), kThreads, 0, a.stream>>>(
+        auto kernel = norm_fwd_kernel<T, TPR, NV, GATE, CENTER>;
+        static const int per_sm = resident(kernel);  // the kernel's own, the same on every such device
+        kernel<<<walk_blocks(groups, per_sm), kThreads, 0, a.stream>>>(
             p, (const T *)a.x, a.weight, a.bias, wf32, (const T *)a.gate, (T *)a.y, a.stats);
     } else {
-        const int blocks = walk_blocks(groups, kBwdPerSm);
-        norm_bwd_kernel<T, TPR, NV, GATE, CENTER><<<blocks, kThreads, 0, a.stream>>>(
+        auto kernel = norm_bwd_kernel<T, TPR, NV, GATE, CENTER>;
+        static const int per_sm = resident(kernel);
+        const int blocks = walk_blocks(groups, per_sm);
+        kernel<<<blocks, kThreads, 0, a.stream>>>(
             p, (const T *)a.x, a.weight, a.bias, wf32, (const T *)a.gate, (const T *)a.dy, a.stats, (T *)a.dx, (T *)a.dgate, a.part);
         norm_dw_kernel<<<dim3((a.D + 31) / 32, a.dbias ? 2 : 1), 1024, 0, a.stream>>>(a.part, blocks, a.D, wf32, a.dweight, a.dbias);
     }
@@ -515,7 +557,7 @@ cudaError_t dispatch(const NormArgs &a, bool bwd) {
 }  // namespace
 
 size_t norm_part_bytes(const NormArgs &a) {
-    const int blocks = in_registers(a) ? sm_count() * kBwdPerSm : any_dw_blocks(a);
+    const int blocks = in_registers(a) ? sm_count() * kMostPerSm : any_dw_blocks(a);
     return (size_t)blocks * 2 * a.D * sizeof(float);
 }
 

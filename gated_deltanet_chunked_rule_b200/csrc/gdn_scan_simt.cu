@@ -19,11 +19,15 @@
 // taken anew from a kept state, and neither holds the token's own product (which would cancel):
 // with it and 64 tokens the sums' rounding reached 1e-4 of dA where the decay is fast.
 //
-// One CTA per (sequence, head, 32 columns of P): warp w holds state rows 32w .. 32w+31, lane
-// l column l, in registers across the call's tokens. Tokens come in tiles of 16, the next
+// One CTA per (sequence or segment of one, head, 32 columns of P): warp w holds state rows
+// 32w .. 32w+31, lane l column l, in registers across its tokens. Where sequences, heads and
+// slices are too few to fill the device a sequence is cut into segments: a first pass takes each
+// from a zero state (the states alone), a small kernel composes their starts, a second pass
+// does the work (1000 tokens, 4 heads of 64 x 64, fp32: 198 -> 30 us forward). Tokens come in tiles of 16, the next
 // tile's loads in flight while one is worked on. The decode step is memory-bound by its
 // state, in and out once; the prompts are bound by the FMAs and shared-memory reads of the
 // 32-row columns.
+#include "gdn_host.cuh"
 #include "gdn_layer.cuh"
 
 namespace gdn {
@@ -31,8 +35,16 @@ namespace {
 
 constexpr int kCols = 32, kTile = 16, kKeep = kTile;
 
+// Segments of a sequence (a multiple of the tile; longer than any sequence where there is no split).
+struct Segments {
+    int tokens;
+    float *state;  // [slots, H, K, P]: each segment's end, then its start
+    float *decay;  // [slots, H]: log decay of a segment
+};
+
 struct ScanP {
     SeqMap m;
+    Segments seg;
     int G, H, P;
     bool softplus;
     long long xs, bs, cs, dts;
@@ -65,20 +77,20 @@ struct Tile {
     float b[kTile], c[kTile], x[kX], dy[kX], dt;
 
     // tokens t0 + i (step dir) for i < n; Bm, Cm at this group, x at this head and slice
-    template <bool GRAD>
+    template <bool GRAD, bool ENDS = false, bool REV = false>
     __device__ __forceinline__ void load(const ScanP &p, const Tin *x_, const Tdt *dt_, const Tin *B, const Tin *C, const Tin *dy_,
                                          int h, int g, int c0, int t0, int dir, int n, int tid) {
 #pragma unroll
         for (int i = 0; i < kTile; ++i) {
             const size_t t = (size_t)(t0 + dir * i);
-            b[i] = i < n ? to_f32(B[t * p.bs + (size_t)g * K + tid]) : 0.f;
-            c[i] = i < n ? to_f32(C[t * p.cs + (size_t)g * K + tid]) : 0.f;
+            if (!(ENDS && REV)) b[i] = i < n ? to_f32(B[t * p.bs + (size_t)g * K + tid]) : 0.f;
+            if (!(ENDS && !REV)) c[i] = i < n ? to_f32(C[t * p.cs + (size_t)g * K + tid]) : 0.f;
         }
 #pragma unroll
         for (int j = 0; j < kX; ++j) {
             const int i = j * (K / kCols) + tid / kCols, col = c0 + tid % kCols;
             const size_t t = (size_t)(t0 + dir * i);
-            x[j] = i < n ? to_f32(x_[t * p.xs + (size_t)h * p.P + col]) : 0.f;
+            if (!(ENDS && REV)) x[j] = i < n ? to_f32(x_[t * p.xs + (size_t)h * p.P + col]) : 0.f;
             if (GRAD) dy[j] = i < n ? to_f32(dy_[(t * p.H + h) * p.P + col]) : 0.f;
         }
         dt = 0.f;
@@ -112,14 +124,17 @@ __device__ __forceinline__ float dot_row(const float (&red)[K / 32][kCols], floa
     return v;
 }
 
-template <typename Tin, typename Tdt, int K, bool GRAD>
+template <typename Tin, typename Tdt, int K, bool GRAD, bool ENDS = false, bool REV = false>
 __device__ __forceinline__ void put_tile(TileSmem<K> &s, const Tile<Tin, Tdt, K> &r, const ScanP &p, float A, float bias, int n, int tid) {
 #pragma unroll
-    for (int i = 0; i < kTile; ++i) s.b[i][tid] = r.b[i], s.c[i][tid] = r.c[i];
+    for (int i = 0; i < kTile; ++i) {
+        if (!(ENDS && REV)) s.b[i][tid] = r.b[i];
+        if (!(ENDS && !REV)) s.c[i][tid] = r.c[i];
+    }
 #pragma unroll
     for (int j = 0; j < Tile<Tin, Tdt, K>::kX; ++j) {
         const int i = j * (K / kCols) + tid / kCols;
-        s.x[i][tid % kCols] = r.x[j];
+        if (!(ENDS && REV)) s.x[i][tid % kCols] = r.x[j];
         if (GRAD) s.dy[i][tid % kCols] = r.dy[j];
     }
     if (tid < n) {
@@ -129,48 +144,77 @@ __device__ __forceinline__ void put_tile(TileSmem<K> &s, const Tile<Tin, Tdt, K>
     }
 }
 
-// Forward; with GRAD instead the gradient's forward half: dC parts [total, H, P/32, K], r and
-// x.dy, kept states [slots of 16, H, K, P] at each tile's end.
-template <typename Tin, typename Tdt, int K, bool GRAD>
+// What a CTA walks: segment `local` of sequence n.
+struct Walk {
+    int n, local, t0, len, s_begin, s_len;
+    size_t at;      // this thread's first state element in the user's states
+    size_t seg_at;  // and in the segments'
+    __device__ __forceinline__ bool find(const ScanP &p, int slot, int h, int K, int row, int col) {
+        const bool used = p.m.slot(slot, p.seg.tokens, &n, &local);
+        s_begin = p.m.begin(n), s_len = p.m.end(n) - s_begin;
+        t0 = s_begin + local * p.seg.tokens;
+        len = used ? min(p.seg.tokens, s_begin + s_len - t0) : 0;
+        at = (((size_t)n * p.H + h) * K + row) * p.P + col;
+        seg_at = (((size_t)slot * p.H + h) * K + row) * p.P + col;
+        return used || (local == 0 && s_len == 0);  // an empty sequence keeps its state
+    }
+    __device__ __forceinline__ bool first() const { return local == 0; }
+    __device__ __forceinline__ bool last() const { return t0 + len == s_begin + s_len; }
+};
+
+// Forward. GRAD: the gradient's forward half instead: dC parts [total, H, P/32, K], r and x.dy,
+// kept states [slots of 16, H, K, P] at each tile's end. ENDS: only the state at the segment's
+// end from zero, and its log decay.
+template <typename Tin, typename Tdt, int K, bool GRAD, bool ENDS>
 __global__ void __launch_bounds__(K)
 scan_forward_kernel(ScanP p, const Tin *__restrict__ x, const Tdt *__restrict__ dt, const Tin *__restrict__ B, const Tin *__restrict__ C,
                     const Tin *__restrict__ dy, const float *h0, Tin *__restrict__ y, float *final_state, float *__restrict__ dc_part,
                     float *__restrict__ keep, Dots dots, unsigned *status) {
     __shared__ TileSmem<K> s;
-    const int n = blockIdx.x, h = blockIdx.y, c0 = blockIdx.z * kCols, g = h / (p.H / p.G);
+    const int h = blockIdx.y, c0 = blockIdx.z * kCols, g = h / (p.H / p.G);
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-    if (n == 0 && h == 0 && blockIdx.z == 0) check_cu(p.m, status, tid, K);
-    const int t0 = p.m.begin(n), len = p.m.end(n) - t0;
-    const size_t at = ((size_t)n * p.H + h) * K * p.P + c0 + lane;
+    if (blockIdx.x == 0 && h == 0 && blockIdx.z == 0) check_cu(p.m, status, tid, K);
+    Walk wk;
+    if (!wk.find(p, blockIdx.x, h, K, 32 * w, c0 + lane) || (ENDS && (wk.last() || wk.len == 0))) return;
+    const int n = wk.n, t0 = wk.t0, len = wk.len;
+    const float *src = ENDS ? nullptr : wk.first() ? (h0 ? h0 + wk.at : nullptr) : p.seg.state + wk.seg_at;
     float hr[32];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) hr[i] = h0 ? h0[at + (size_t)(32 * w + i) * p.P] : 0.f;
+    for (int i = 0; i < 32; ++i) hr[i] = src ? src[(size_t)i * p.P] : 0.f;
     const float A = p.A[h], D = p.D ? p.D[h] : 0.f, bias = p.dt_bias ? p.dt_bias[h] : 0.f;
+    const int tile0 = p.m.slot0(n, kKeep) + (t0 - wk.s_begin) / kKeep;
+    float total = 0.f;
     Tile<Tin, Tdt, K> r;
-    if (len) r.template load<GRAD>(p, x, dt, B, C, dy, h, g, c0, t0, 1, min(kTile, len), tid);
+    if (len) r.template load<GRAD, ENDS>(p, x, dt, B, C, dy, h, g, c0, t0, 1, min(kTile, len), tid);
     for (int q = 0; q < len; q += kTile) {
         const int cnt = min(kTile, len - q);
-        put_tile<Tin, Tdt, K, GRAD>(s, r, p, A, bias, cnt, tid);
+        put_tile<Tin, Tdt, K, GRAD, ENDS>(s, r, p, A, bias, cnt, tid);
         __syncthreads();
-        if (q + kTile < len) r.template load<GRAD>(p, x, dt, B, C, dy, h, g, c0, t0 + q + kTile, 1, min(kTile, len - q - kTile), tid);
+        if (q + kTile < len) r.template load<GRAD, ENDS>(p, x, dt, B, C, dy, h, g, c0, t0 + q + kTile, 1, min(kTile, len - q - kTile), tid);
         for (int i = 0; i < cnt; ++i) {
             const float a = s.a[i], dx = s.d[i] * s.x[i][lane];
             float yv = 0.f;
+            if constexpr (ENDS) {
+                total = fmaf(s.d[i], A, total);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-                const float ah = a * hr[k];
-                if (GRAD) yv = fmaf(s.c[i][32 * w + k], ah, yv);
-                hr[k] = fmaf(s.b[i][32 * w + k], dx, ah);
-                if (!GRAD) yv = fmaf(s.c[i][32 * w + k], hr[k], yv);
-            }
-            s.red[i][w][lane] = yv;
-            if (GRAD) {
-                float v[32];
-                const float d = s.dy[i][lane];
+                for (int k = 0; k < 32; ++k) hr[k] = fmaf(s.b[i][32 * w + k], dx, a * hr[k]);
+            } else {
 #pragma unroll
-                for (int k = 0; k < 32; ++k) v[k] = hr[k] * d;
-                const float sum = lane_sums(v, lane);
-                dc_part[(((size_t)(t0 + q + i) * p.H + h) * gridDim.z + blockIdx.z) * K + 32 * w + lane] = sum;
+                for (int k = 0; k < 32; ++k) {
+                    const float ah = a * hr[k];
+                    if (GRAD) yv = fmaf(s.c[i][32 * w + k], ah, yv);
+                    hr[k] = fmaf(s.b[i][32 * w + k], dx, ah);
+                    if (!GRAD) yv = fmaf(s.c[i][32 * w + k], hr[k], yv);
+                }
+                s.red[i][w][lane] = yv;
+                if (GRAD) {
+                    float v[32];
+                    const float d = s.dy[i][lane];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) v[k] = hr[k] * d;
+                    const float sum = lane_sums(v, lane);
+                    dc_part[(((size_t)(t0 + q + i) * p.H + h) * gridDim.z + blockIdx.z) * K + 32 * w + lane] = sum;
+                }
             }
         }
         __syncthreads();
@@ -184,10 +228,10 @@ scan_forward_kernel(ScanP p, const Tin *__restrict__ x, const Tdt *__restrict__ 
                 const size_t e = ((size_t)(t0 + q + i) * p.H + h) * gridDim.z + blockIdx.z;
                 if (lane == 0) *dots(kR, e) = rv, *dots(kXd, e) = xd;
             }
-            float *dst = keep + ((size_t)(p.m.slot0(n, kKeep) + q / kKeep) * p.H + h) * K * p.P + c0 + lane;
+            float *dst = keep + ((size_t)(tile0 + q / kKeep) * p.H + h) * K * p.P + c0 + lane;
 #pragma unroll
             for (int k = 0; k < 32; ++k) dst[(size_t)(32 * w + k) * p.P] = hr[k];
-        } else {
+        } else if (!ENDS) {
             for (int e = tid; e < cnt * kCols; e += K) {
                 const int i = e / kCols, col = e % kCols;
                 float v = 0.f;
@@ -198,9 +242,30 @@ scan_forward_kernel(ScanP p, const Tin *__restrict__ x, const Tdt *__restrict__ 
         }
         __syncthreads();
     }
-    if (final_state)
+    float *out = ENDS ? p.seg.state + wk.seg_at : wk.last() && final_state ? final_state + wk.at : nullptr;
+    if (out)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) final_state[at + (size_t)(32 * w + i) * p.P] = hr[i];
+        for (int i = 0; i < 32; ++i) out[(size_t)i * p.P] = hr[i];
+    if (ENDS && blockIdx.z == 0 && tid == 0) p.seg.decay[(size_t)blockIdx.x * p.H + h] = total;
+}
+
+// Start states of the segments (REV: gradients at their ends), in place of what a pass from zero
+// left: start' = e^{decay} start + end. A thread per state element walks a sequence's segments.
+template <bool REV>
+__global__ void __launch_bounds__(256) scan_segments_kernel(ScanP p, int elements, const float *__restrict__ from) {
+    const int n = blockIdx.x, h = blockIdx.y, e = blockIdx.z * 256 + threadIdx.x;
+    const int len = p.m.end(n) - p.m.begin(n), segs = (len + p.seg.tokens - 1) / p.seg.tokens;
+    if (segs < 2) return;
+    const size_t slot0 = p.m.slot0(n, p.seg.tokens);
+    auto slot = [&](int i) { return slot0 + (REV ? segs - 1 - i : i); };
+    auto at = [&](int i) { return p.seg.state + (slot(i) * p.H + h) * elements + e; };
+    float cur = from ? from[((size_t)n * p.H + h) * elements + e] : 0.f, end = *at(0);
+    for (int i = 0; i + 1 < segs; ++i) {
+        const float v = end;
+        if (i + 2 < segs) end = *at(i + 1);  // before its place is taken
+        cur = fmaf(expf(p.seg.decay[slot(i) * p.H + h]), cur, v);
+        *at(i + 1) = cur;
+    }
 }
 
 // The decode step: a few tokens per sequence. The state's loads are issued before anything else and
@@ -250,31 +315,36 @@ scan_step_kernel(ScanP p, const Tin *__restrict__ x, const Tdt *__restrict__ dt,
 
 // The gradient's reverse half: dx, dB parts (without delta), v and w, <h, i> at the end of every
 // tile [slots, H, P/32], dh0.
-template <typename Tin, typename Tdt, int K>
+// ENDS: only the gradient at the segment's start from zero, and its log decay.
+template <typename Tin, typename Tdt, int K, bool ENDS>
 __global__ void __launch_bounds__(K)
 scan_reverse_kernel(ScanP p, const Tin *__restrict__ x, const Tdt *__restrict__ dt, const Tin *__restrict__ B, const Tin *__restrict__ C,
                     const Tin *__restrict__ dy, const float *__restrict__ dht, const float *__restrict__ keep, Tin *__restrict__ dx,
                     float *__restrict__ db_part, float *__restrict__ chunk_q, float *__restrict__ dh0, Dots dots) {
     __shared__ TileSmem<K> s;
     __shared__ float qs[K / 32];
-    const int n = blockIdx.x, h = blockIdx.y, c0 = blockIdx.z * kCols, g = h / (p.H / p.G);
+    const int h = blockIdx.y, c0 = blockIdx.z * kCols, g = h / (p.H / p.G);
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-    const int t0 = p.m.begin(n), len = p.m.end(n) - t0;
-    const size_t at = ((size_t)n * p.H + h) * K * p.P + c0 + lane;
+    Walk wk;
+    if (!wk.find(p, blockIdx.x, h, K, 32 * w, c0 + lane) || (ENDS && (wk.first() || wk.len == 0))) return;
+    const int n = wk.n, t0 = wk.t0, len = wk.len;
+    const float *from = ENDS ? nullptr : wk.last() ? (dht ? dht + wk.at : nullptr) : p.seg.state + wk.seg_at;
     float gr[32];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) gr[i] = dht ? dht[at + (size_t)(32 * w + i) * p.P] : 0.f;
+    for (int i = 0; i < 32; ++i) gr[i] = from ? from[(size_t)i * p.P] : 0.f;
+    const int tile0 = p.m.slot0(n, kKeep) + (t0 - wk.s_begin) / kKeep;
+    float total = 0.f;
     const float A = p.A[h], D = p.D ? p.D[h] : 0.f, bias = p.dt_bias ? p.dt_bias[h] : 0.f;
     // tiles in reverse: token i of a tile is t0 + q - i; the ragged tile comes first, so that the
     // tiles are the forward half's
     const int first = len ? (len - 1) % kTile + 1 : 0;
     Tile<Tin, Tdt, K> r;
-    if (len) r.template load<true>(p, x, dt, B, C, dy, h, g, c0, t0 + len - 1, -1, first, tid);
+    if (len) r.template load<true, ENDS, true>(p, x, dt, B, C, dy, h, g, c0, t0 + len - 1, -1, first, tid);
     int cnt = first;
     for (int q = len - 1; q >= 0; q -= cnt, cnt = kTile) {
-        put_tile<Tin, Tdt, K, true>(s, r, p, A, bias, cnt, tid);
-        {
-            const size_t slot = p.m.slot0(n, kKeep) + q / kKeep;
+        put_tile<Tin, Tdt, K, true, ENDS, true>(s, r, p, A, bias, cnt, tid);
+        if (!ENDS) {
+            const size_t slot = (size_t)tile0 + q / kKeep;
             const float *src = keep + (slot * p.H + h) * K * p.P + c0 + lane;
             float v = 0.f;
 #pragma unroll
@@ -291,41 +361,50 @@ scan_reverse_kernel(ScanP p, const Tin *__restrict__ x, const Tdt *__restrict__ 
             }
         }
         __syncthreads();
-        if (q - cnt >= 0) r.template load<true>(p, x, dt, B, C, dy, h, g, c0, t0 + q - cnt, -1, kTile, tid);
+        if (q - cnt >= 0) r.template load<true, ENDS, true>(p, x, dt, B, C, dy, h, g, c0, t0 + q - cnt, -1, kTile, tid);
         for (int i = 0; i < cnt; ++i) {
-            const float d = s.dy[i][lane], xv = s.x[i][lane], a = s.a[i];
-            float u = 0.f, ui = 0.f, v[32];
+            const float d = s.dy[i][lane], a = s.a[i];
+            if constexpr (ENDS) {
+                total = fmaf(s.d[i], A, total);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-                ui = fmaf(s.b[i][32 * w + k], gr[k], ui);
-                gr[k] = fmaf(s.c[i][32 * w + k], d, gr[k]);
-                u = fmaf(s.b[i][32 * w + k], gr[k], u);
-                v[k] = gr[k] * xv;
-                gr[k] *= a;
+                for (int k = 0; k < 32; ++k) gr[k] = a * fmaf(s.c[i][32 * w + k], d, gr[k]);
+            } else {
+                const float xv = s.x[i][lane];
+                float u = 0.f, ui = 0.f, v[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    ui = fmaf(s.b[i][32 * w + k], gr[k], ui);
+                    gr[k] = fmaf(s.c[i][32 * w + k], d, gr[k]);
+                    u = fmaf(s.b[i][32 * w + k], gr[k], u);
+                    v[k] = gr[k] * xv;
+                    gr[k] *= a;
+                }
+                s.red[i][w][lane] = u;
+                s.red2[i][w][lane] = ui;
+                const float sum = lane_sums(v, lane);
+                db_part[(((size_t)(t0 + q - i) * p.H + h) * gridDim.z + blockIdx.z) * K + 32 * w + lane] = sum;
             }
-            s.red[i][w][lane] = u;
-            s.red2[i][w][lane] = ui;
-            const float sum = lane_sums(v, lane);
-            db_part[(((size_t)(t0 + q - i) * p.H + h) * gridDim.z + blockIdx.z) * K + 32 * w + lane] = sum;
         }
         __syncthreads();
-        for (int e = tid; e < cnt * kCols; e += K) {
+        for (int e = tid; !ENDS && e < cnt * kCols; e += K) {
             const int i = e / kCols, col = e % kCols;
             float u = 0.f;
 #pragma unroll
             for (int k = 0; k < K / 32; ++k) u += s.red[i][k][col];
             dx[((size_t)(t0 + q - i) * p.H + h) * p.P + c0 + col] = from_f32<Tin>(fmaf(s.d[i], u, D * s.dy[i][col]));
         }
-        for (int i = w; i < cnt; i += K / 32) {
+        for (int i = w; !ENDS && i < cnt; i += K / 32) {
             const float xv = s.x[i][lane], wv = dot_row<K>(s.red[i], xv, lane), vv = dot_row<K>(s.red2[i], xv, lane);
             const size_t e = ((size_t)(t0 + q - i) * p.H + h) * gridDim.z + blockIdx.z;
             if (lane == 0) *dots(kWt, e) = wv, *dots(kV, e) = vv;
         }
         __syncthreads();
     }
-    if (dh0)
+    float *out = ENDS ? p.seg.state + wk.seg_at : wk.first() && dh0 ? dh0 + wk.at : nullptr;
+    if (out)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) dh0[at + (size_t)(32 * w + i) * p.P] = gr[i];
+        for (int i = 0; i < 32; ++i) out[(size_t)i * p.P] = gr[i];
+    if (ENDS && blockIdx.z == 0 && tid == 0) p.seg.decay[(size_t)blockIdx.x * p.H + h] = total;
 }
 
 // Per token: dC, dB summed over a group's heads.
@@ -402,59 +481,110 @@ __global__ void __launch_bounds__(256) scan_sum_kernel(const float *__restrict__
     if (threadIdx.x == 0 && out) out[h] = red[0];
 }
 
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+// Tokens of a segment; 0: whole sequences. Four CTAs of these kernels run on an SM; where there are
+// fewer than two per SM a sequence is cut into about as many segments as would fill them, of at
+// least four tiles (a packed batch, of unknown lengths, by its total).
+int segment_tokens(const ScanArgs &a) {
+    const long long ctas = (long long)(a.seq.cu ? 1 : a.seq.N) * a.H * (a.P / kCols);
+    const int tokens = a.seq.cu ? a.seq.total : a.seq.T;
+    if (ctas >= 2 * sm_count() || tokens < 8 * kTile) return 0;
+    const long long want = (4ll * sm_count() + ctas - 1) / ctas, per = (tokens + want - 1) / want;
+    return (int)((per < 4 * kTile ? 4 * kTile : per) + kTile - 1) / kTile * kTile;
+}
+
+size_t segments_bytes(const ScanArgs &a) {
+    const int q = segment_tokens(a);
+    if (!q) return 0;
+    const size_t slots = a.seq.slots(q);
+    return up256(slots * a.H * a.K * a.P * 4) + up256(slots * a.H * 4);
+}
+
+Segments segments(const ScanArgs &a, char *ws) {
+    Segments s;
+    s.tokens = segment_tokens(a);
+    s.state = (float *)ws;
+    s.decay = s.tokens ? (float *)(ws + up256((size_t)a.seq.slots(s.tokens) * a.H * a.K * a.P * 4)) : nullptr;
+    if (!s.tokens) s.tokens = ((a.seq.cu ? a.seq.total : a.seq.T) / kTile + 1) * kTile;  // longer than any sequence
+    return s;
+}
+
 struct SimtWs {
-    size_t keep, dc, db, q, rw, part, total;
+    size_t seg, keep, dc, db, q, rw, part, total;
 };
 
 SimtWs simt_ws(const ScanArgs &a) {
-    auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     const size_t tok = a.seq.total, S = a.P / kCols, slots = a.seq.slots(kKeep);
     SimtWs w;
-    w.keep = 0;
-    w.dc = w.keep + up(slots * a.H * a.K * a.P * 4);
-    w.db = w.dc + up(tok * a.H * S * a.K * 4);
-    w.q = w.db + up(tok * a.H * S * a.K * 4);
-    w.rw = w.q + up(slots * a.H * S * 4);
-    w.part = w.rw + up(kDots * tok * a.H * S * 4);
-    w.total = w.part + up(slots * 3 * a.H * 4);
+    w.seg = 0;
+    w.keep = w.seg + segments_bytes(a);
+    w.dc = w.keep + up256(slots * a.H * a.K * a.P * 4);
+    w.db = w.dc + up256(tok * a.H * S * a.K * 4);
+    w.q = w.db + up256(tok * a.H * S * a.K * 4);
+    w.rw = w.q + up256(slots * a.H * S * 4);
+    w.part = w.rw + up256(kDots * tok * a.H * S * 4);
+    w.total = w.part + up256(slots * 3 * a.H * 4);
     return w;
 }
 
-ScanP params(const ScanArgs &a) {
-    return ScanP{a.seq, a.G, a.H, a.P, a.softplus, a.xs, a.bs, a.cs, a.dts, a.A, a.D, a.dt_bias};
+ScanP params(const ScanArgs &a, const Segments &seg) {
+    return ScanP{a.seq, seg, a.G, a.H, a.P, a.softplus, a.xs, a.bs, a.cs, a.dts, a.A, a.D, a.dt_bias};
+}
+
+// CTAs along the sequences: one per segment slot (T = 0: one per sequence, for its state).
+int walks(const ScanArgs &a, const Segments &seg) { return a.seq.total ? a.seq.slots(seg.tokens) : a.seq.N; }
+
+// Start states of the segments (REV: gradients at their ends); nothing for whole sequences.
+template <typename Tin, typename Tdt, int K, bool REV>
+void compose(const ScanArgs &a, const ScanP &p) {
+    if (!segment_tokens(a)) return;
+    const Tin *x = (const Tin *)a.x, *B = (const Tin *)a.B, *C = (const Tin *)a.C, *dy = (const Tin *)a.dy;
+    const dim3 grid(walks(a, p.seg), a.H, a.P / kCols);
+    if (REV)
+        scan_reverse_kernel<Tin, Tdt, K, true><<<grid, K, 0, a.stream>>>(p, x, (const Tdt *)a.dt, B, C, dy, nullptr, nullptr, nullptr, nullptr,
+                                                                        nullptr, nullptr, Dots{});
+    else
+        scan_forward_kernel<Tin, Tdt, K, false, true><<<grid, K, 0, a.stream>>>(p, x, (const Tdt *)a.dt, B, C, nullptr, nullptr, nullptr,
+                                                                               nullptr, nullptr, nullptr, Dots{}, a.status);
+    scan_segments_kernel<REV><<<dim3(a.seq.N, a.H, K * a.P / 256), 256, 0, a.stream>>>(p, K * a.P, REV ? a.dht : a.h0);
 }
 
 template <typename Tin, typename Tdt, int K>
 cudaError_t forward(const ScanArgs &a) {
-    const dim3 grid(a.seq.N, a.H, a.P / kCols);
-    scan_forward_kernel<Tin, Tdt, K, false><<<grid, K, 0, a.stream>>>(params(a), (const Tin *)a.x, (const Tdt *)a.dt, (const Tin *)a.B,
-                                                                     (const Tin *)a.C, nullptr, a.h0, (Tin *)a.y, a.final_state, nullptr,
-                                                                     nullptr, Dots{}, a.status);
+    const ScanP p = params(a, segments(a, (char *)a.ws));
+    compose<Tin, Tdt, K, false>(a, p);
+    const dim3 grid(walks(a, p.seg), a.H, a.P / kCols);
+    scan_forward_kernel<Tin, Tdt, K, false, false><<<grid, K, 0, a.stream>>>(p, (const Tin *)a.x, (const Tdt *)a.dt, (const Tin *)a.B,
+                                                                            (const Tin *)a.C, nullptr, a.h0, (Tin *)a.y, a.final_state,
+                                                                            nullptr, nullptr, Dots{}, a.status);
     return cudaGetLastError();
 }
 
 template <typename Tin, typename Tdt, int K>
 cudaError_t step(const ScanArgs &a) {
     const dim3 grid(a.seq.N, a.H, a.P / kCols);
-    scan_step_kernel<Tin, Tdt, K><<<grid, K, 0, a.stream>>>(params(a), (const Tin *)a.x, (const Tdt *)a.dt, (const Tin *)a.B,
+    scan_step_kernel<Tin, Tdt, K><<<grid, K, 0, a.stream>>>(params(a, Segments{}), (const Tin *)a.x, (const Tdt *)a.dt, (const Tin *)a.B,
                                                            (const Tin *)a.C, a.h0, (Tin *)a.y, a.final_state, a.status);
     return cudaGetLastError();
 }
 
 template <typename Tin, typename Tdt, int K>
 cudaError_t backward(const ScanArgs &a) {
-    const ScanP p = params(a);
     const SimtWs w = simt_ws(a);
     char *ws = (char *)a.ws;
+    const ScanP p = params(a, segments(a, ws + w.seg));
     float *keep = (float *)(ws + w.keep), *dc = (float *)(ws + w.dc), *db = (float *)(ws + w.db), *q = (float *)(ws + w.q);
     float *part = (float *)(ws + w.part);
     const Dots dots{(float *)(ws + w.rw), (size_t)a.seq.total * a.H * (a.P / kCols)};
     const Tin *x = (const Tin *)a.x, *B = (const Tin *)a.B, *C = (const Tin *)a.C, *dy = (const Tin *)a.dy;
     const Tdt *dt = (const Tdt *)a.dt;
-    const dim3 grid(a.seq.N, a.H, a.P / kCols);
+    const dim3 grid(walks(a, p.seg), a.H, a.P / kCols);
     const int slots = a.seq.slots(kKeep);
-    scan_forward_kernel<Tin, Tdt, K, true><<<grid, K, 0, a.stream>>>(p, x, dt, B, C, dy, a.h0, nullptr, nullptr, dc, keep, dots, a.status);
-    scan_reverse_kernel<Tin, Tdt, K><<<grid, K, 0, a.stream>>>(p, x, dt, B, C, dy, a.dht, keep, (Tin *)a.dx, db, q, a.dh0, dots);
+    compose<Tin, Tdt, K, false>(a, p);
+    scan_forward_kernel<Tin, Tdt, K, true, false><<<grid, K, 0, a.stream>>>(p, x, dt, B, C, dy, a.h0, nullptr, nullptr, dc, keep, dots, a.status);
+    compose<Tin, Tdt, K, true>(a, p);
+    scan_reverse_kernel<Tin, Tdt, K, false><<<grid, K, 0, a.stream>>>(p, x, dt, B, C, dy, a.dht, keep, (Tin *)a.dx, db, q, a.dh0, dots);
     if (a.seq.total)
         scan_gather_kernel<Tin, Tdt, K><<<a.seq.total, K, 0, a.stream>>>(p, dt, dc, db, (Tin *)a.dB, (Tin *)a.dC);
     if (slots)
@@ -489,6 +619,7 @@ cudaError_t launch_scan_sum(const float *part, int slots, const ScanArgs &a) {
 
 cudaError_t launch_scan_step(const ScanArgs &a) { return dispatch(a, kStep); }
 cudaError_t launch_scan_simt_fwd(const ScanArgs &a) { return dispatch(a, kForward); }
+size_t scan_simt_fwd_bytes(const ScanArgs &a) { return segments_bytes(a); }
 size_t scan_simt_bwd_bytes(const ScanArgs &a) { return simt_ws(a).total; }
 cudaError_t launch_scan_simt_bwd(const ScanArgs &a) { return dispatch(a, kBackward); }
 

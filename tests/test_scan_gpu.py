@@ -146,8 +146,9 @@ def test_batch_of_slices_without_saved(gdn, dtype, slow):
 def test_sequences_cut_into_segments(gdn, lens, packed, K, P, H):
     # few heads and many chunks: state passes over segments of a sequence, composed; ends on and
     # off the segments' borders, beside short and empty sequences
-    v = make(lens, H, 1, K, P, torch.bfloat16, seed=21, packed=packed, slow=True)
-    verify(v, lens, True, train(gdn, v))
+    for dtype in (torch.bfloat16, torch.float32):
+        v = make(lens, H, 1, K, P, dtype, seed=21, packed=packed, slow=True)
+        verify(v, lens, True, train(gdn, v))
 
 
 @pytest.mark.parametrize("H,G,P,lens", [(24, 1, 128, [300]), (40, 1, 64, [128, 200]), (48, 2, 128, [129]), (7, 1, 128, [256])])
