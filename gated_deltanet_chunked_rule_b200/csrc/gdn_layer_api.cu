@@ -114,6 +114,7 @@ scan_tc::StateArgs state_pass(const ScanArgs &a, const scan_tc::Gates &gates, bo
     if (s.chunks_per_seg) {
         const size_t slots = a.seq.slots(s.chunks_per_seg * scan_tc::kC);
         s.seg = (float *)seg;
+        s.products = scan_tc::by_products(a);
         s.seg_gam = (float *)(seg + align_up(slots * a.H * a.P * a.K * sizeof(float)));
     }
     s.first = reverse ? a.dht : a.h0;

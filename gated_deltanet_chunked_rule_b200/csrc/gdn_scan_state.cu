@@ -20,9 +20,13 @@
 // multiplied first, so that their buffer is free for the next chunk while the first one's
 // product still runs, and the accumulator has two buffers.
 //
-// A sequence is cut into segments where units and sequences alone would not fill the SMs: a
-// first pass takes every segment from a zero state, one small kernel composes the segments'
-// starts (their operator is one scalar decay), a second pass walks them again.
+// A sequence is cut into segments where units and sequences alone would not fill the SMs. Then,
+// where every chunk's product fits the L2 cache in fp32, the segments only write those products and
+// a second kernel runs the recurrence over the chunks element by element; it reads what it needs
+// from L2. Beyond that size the products would go through memory twice, and instead a first pass
+// takes every segment from a zero state, one small kernel composes the segments' starts (their
+// operator is one scalar decay), and a second pass walks them again. 2 x 4096 tokens, 16 heads of
+// 128 (67 MB of products): SPLIT_FIGURES.
 #include <algorithm>
 
 #include "gdn_scan_tc.cuh"
@@ -82,14 +86,21 @@ constexpr int kSmall = kMid + 65536;    // barriers
 constexpr int kSmem = kSmall + 256 + 1024;
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
+enum Pass { kWalk, kEnds, kProducts };  // the states; segment ends from zero; every chunk's product
+
 struct StateP {
     Params p;
     int seg_tokens;   // tokens of a segment
-    bool ends_only;   // the first pass: segment ends from zero
+    Pass pass;
     const float *first;
     float *last, *seg, *seg_gam;
     Tiles tiles;
 };
+
+// A chunk's product in fp32: [column / 4][row][4], so that a lane-per-row store is contiguous.
+__device__ __forceinline__ size_t product_at(size_t slot, size_t units, size_t unit, int K, int quad, int row) {
+    return (slot * units + unit) * (size_t)(K * kPT) + ((size_t)quad * K + row) * 4;
+}
 
 template <int K, bool REVERSE>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -116,14 +127,14 @@ scan_state_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constan
     const int h = mine ? p.head(g, u) : 0;
     const size_t user = (((size_t)n * p.H + h) * K + row) * p.P + (mine ? p.col0(u) : 0) + c0;  // in the user's states
     if (!used) {  // an empty sequence keeps its state
-        if (local == 0 && s_len == 0 && !q.ends_only && q.last && real)
+        if (local == 0 && s_len == 0 && q.pass == kWalk && q.last && real)
             for (int i = 0; i < kHalf; ++i) q.last[user + i] = q.first ? q.first[user + i] : 0.f;
         return;
     }
     const int seg_begin = s_begin + local * q.seg_tokens, seg_len = min(q.seg_tokens, s_begin + s_len - seg_begin);
     const bool at_first = REVERSE ? seg_begin + seg_len == s_begin + s_len : local == 0;
     const bool at_last = REVERSE ? local == 0 : seg_begin + seg_len == s_begin + s_len;
-    if (q.ends_only && at_last) return;  // nothing follows it
+    if (q.pass == kEnds && at_last) return;  // nothing follows it
     const int chunks = (seg_len + kC - 1) / kC;
 
     if (tid == 0) {
@@ -198,7 +209,7 @@ scan_state_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constan
         float st[kHalf];  // this thread's part of the state
         const size_t units = (size_t)p.G * p.U, unit = (size_t)g * p.U + u;
         float *const seg = q.seg + (((size_t)blockIdx.x * units + unit) * K + row) * kPT + c0;
-        const float *src = q.ends_only ? nullptr : at_first ? (q.first ? q.first + user : nullptr) : seg;
+        const float *src = q.pass != kWalk ? nullptr : at_first ? (q.first ? q.first + user : nullptr) : seg;
         if (real && src) {
 #pragma unroll
             for (int i = 0; i < kHalf; i += 4) {
@@ -210,7 +221,7 @@ scan_state_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constan
             for (int i = 0; i < kHalf; ++i) st[i] = 0.f;
         }
         const size_t slot0 = (size_t)p.m.slot0(n, kC) + (seg_begin - s_begin) / kC;
-        const bool keeps = q.tiles.hi && real && !q.ends_only;
+        const bool keeps = q.tiles.hi && real && q.pass == kWalk;
         auto keep = [&](int i) {  // the state on entry to chunk i of the walk
             if (!keeps) return;
             const size_t at = ((slot0 + chunk_at(i)) * units + unit) * (K * kPT) + (size_t)(c0 / 8) * K * 8 + row * 8;
@@ -302,21 +313,30 @@ scan_state_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constan
                 if (ok) {
                     float v[kHalf];
                     tmem_ld32(tmem + ((uint32_t)(wr * 32) << 16) + ((i - 1) & 1) * 128 + unit_of * kPT + c0, v);
+                    if (q.pass == kProducts) {
+                        if (real) {
+                            float *out = q.seg + product_at(slot0 + chunk_at(i - 1), units, unit, K, c0 / 4, row);
 #pragma unroll
-                    for (int k = 0; k < kHalf; ++k) st[k] = fmaf(decay_prev, st[k], v[k]);
-                    if (i < chunks) keep(i);
+                            for (int k = 0; k < kHalf; k += 4)
+                                *reinterpret_cast<float4 *>(out + (size_t)k * K) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < kHalf; ++k) st[k] = fmaf(decay_prev, st[k], v[k]);
+                        if (i < chunks) keep(i);
+                    }
                 }
             }
             decay_prev = decay;
         }
         if (!ok) fail();
-        if (real && ok) {
-            float *out = q.ends_only ? seg : at_last && q.last ? q.last + user : nullptr;
+        if (real && ok && q.pass != kProducts) {
+            float *out = q.pass == kEnds ? seg : at_last && q.last ? q.last + user : nullptr;
             if (out)
 #pragma unroll
                 for (int i = 0; i < kHalf; i += 4)
                     *reinterpret_cast<float4 *>(out + i) = make_float4(st[i], st[i + 1], st[i + 2], st[i + 3]);
-            if (q.ends_only && row == 0 && c0 == 0 && (u & (p.S - 1)) == 0) q.seg_gam[(size_t)blockIdx.x * p.H + h] = gam_sum;
+            if (q.pass == kEnds && row == 0 && c0 == 0 && (u & (p.S - 1)) == 0) q.seg_gam[(size_t)blockIdx.x * p.H + h] = gam_sum;
         }
         tc_fence_before();
     }
@@ -352,6 +372,58 @@ scan_compose_kernel(Params p, int seg_tokens, const float *__restrict__ first, f
     }
 }
 
+// The recurrence over a sequence's chunks from their products: tiles of every chunk's entry state
+// and the last state. A thread per row and eight columns, four chunks' loads ahead.
+template <int K, bool REVERSE>
+__global__ void __launch_bounds__(256)
+scan_chunks_kernel(Params p, const float *__restrict__ products, const float *__restrict__ first, float *__restrict__ last, Tiles tiles) {
+    constexpr int kAhead = 4;
+    const int n = blockIdx.x, unit = blockIdx.y, e = blockIdx.z * 256 + threadIdx.x, row = e % K, c8 = e / K;
+    const int len = p.m.end(n) - p.m.begin(n), chunks = (len + kC - 1) / kC;
+    const int h = p.head(unit / p.U, unit % p.U);
+    const size_t slot0 = p.m.slot0(n, kC), units = (size_t)p.G * p.U;
+    const size_t user = (((size_t)n * p.H + h) * K + row) * p.P + p.col0(unit % p.U) + c8 * 8;
+    auto slot = [&](int i) { return slot0 + (REVERSE ? chunks - 1 - i : i); };
+    float st[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) st[k] = first ? first[user + k] : 0.f;
+    float4 a[kAhead], b[kAhead], t[kAhead];
+    auto fetch = [&](int i, int at) {
+        if (i >= chunks) return;
+        const float *src = products + product_at(slot(i), units, unit, K, 2 * c8, row);
+        a[at] = *reinterpret_cast<const float4 *>(src);
+        b[at] = *reinterpret_cast<const float4 *>(src + 4 * K);
+        t[at] = p.gates.totals(slot(i), p.H, h);
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) fetch(i, i);
+    for (int i0 = 0; i0 < chunks; i0 += kAhead) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + j;
+            if (i >= chunks) break;
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                hi[k] = pack_bf16(st[2 * k], st[2 * k + 1]);
+                lo[k] = pack_bf16(st[2 * k] - bf_lo(hi[k]), st[2 * k + 1] - bf_hi(hi[k]));
+            }
+            const size_t at = (slot(i) * units + unit) * (K * kPT) + ((size_t)c8 * K + row) * 8;
+            *reinterpret_cast<uint4 *>(tiles.hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if (tiles.lo) *reinterpret_cast<uint4 *>(tiles.lo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            const float d = ex2((t[j].x + t[j].y) + (t[j].z + t[j].w));
+            const float v[8] = {a[j].x, a[j].y, a[j].z, a[j].w, b[j].x, b[j].y, b[j].z, b[j].w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) st[k] = fmaf(d, st[k], v[k]);
+            fetch(i + kAhead, j);
+        }
+    }
+    if (last) {
+        *reinterpret_cast<float4 *>(last + user) = make_float4(st[0], st[1], st[2], st[3]);
+        *reinterpret_cast<float4 *>(last + user + 4) = make_float4(st[4], st[5], st[6], st[7]);
+    }
+}
+
 template <int K, bool REVERSE>
 cudaError_t run(const StateArgs &s) {
     const ScanArgs &a = *s.a;
@@ -372,13 +444,23 @@ cudaError_t run(const StateArgs &s) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const dim3 grid(slots, a.G * pairs);
+    if (s.products) {
+        {
+            TimedLaunch t(REVERSE ? "scan_products_bwd" : "scan_products", a.stream);
+            q.pass = kProducts;
+            kernel<<<grid, kThreads, kSmem, a.stream>>>(mb, mx, q);
+        }
+        TimedLaunch t(REVERSE ? "scan_chunks_bwd" : "scan_chunks", a.stream);
+        scan_chunks_kernel<K, REVERSE><<<dim3(a.seq.N, a.G * q.p.U, K * kPT / 2048), 256, 0, a.stream>>>(q.p, s.seg, s.first, s.last, s.tiles);
+        return cudaGetLastError();
+    }
     if (split) {
-        q.ends_only = true;
+        q.pass = kEnds;
         {
             TimedLaunch t(REVERSE ? "scan_seg_bwd" : "scan_seg", a.stream);
             kernel<<<grid, kThreads, kSmem, a.stream>>>(mb, mx, q);
         }
-        q.ends_only = false;
+        q.pass = kWalk;
         TimedLaunch t("scan_compose", a.stream);
         scan_compose_kernel<K, REVERSE><<<dim3(a.seq.N, a.G * q.p.U, K * kPT / 1024), 256, 0, a.stream>>>(q.p, q.seg_tokens, s.first, s.seg,
                                                                                                      s.seg_gam);
@@ -399,20 +481,28 @@ cudaError_t launch_gates(const ScanArgs &a, const Gates &g) {
 }
 
 // One CTA per SM at a time: where sequences x unit pairs fill less than the SMs, a sequence is
-// cut into as many segments as fit beside each other, of at least 4 chunks (a packed batch, of
+// cut into as many segments as fit beside each other, of at least 2 chunks (a packed batch, of
 // unknown lengths, always by its total). 0: whole sequences.
 int chunks_per_segment(const ScanArgs &a) {
     const int S = a.P / kPT, U = a.H / a.G * S, pairs = a.G * ((U + 1) / 2);
     const int rows = a.seq.cu ? 1 : a.seq.N;
     const long long chunks = a.seq.cu ? (a.seq.total + kC - 1) / kC : (a.seq.T + kC - 1) / kC;
     const int fit = sm_count() / std::max(1, pairs * rows);
-    if (fit < 2 || chunks < 8) return 0;
-    return (int)std::max<long long>(4, (chunks + fit - 1) / fit);
+    if (fit < 2 || chunks < 4) return 0;
+    return (int)std::max<long long>(2, (chunks + fit - 1) / fit);
+}
+
+// The L2 holds 126 MB; the tiles that are written meanwhile pass through it too.
+constexpr size_t kProductBytes = (size_t)100 << 20;
+
+bool by_products(const ScanArgs &a) {
+    return chunks_per_segment(a) > 0 && 2 * tile_bytes(a) <= kProductBytes;
 }
 
 size_t segment_bytes(const ScanArgs &a) {
     const int c = chunks_per_segment(a);
     if (!c) return 0;
+    if (by_products(a)) return align_up(2 * tile_bytes(a));
     const size_t slots = a.seq.slots(c * kC);
     return align_up(slots * a.H * (a.P / kPT) * kPT * a.K * 4) + align_up(slots * a.H * 4);
 }

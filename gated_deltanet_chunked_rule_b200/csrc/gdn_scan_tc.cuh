@@ -172,7 +172,8 @@ struct StateArgs {
     Gates gates;
     bool reverse;
     int chunks_per_seg;  // 0: whole sequences
-    float *seg;          // [segment slots, units, K, 64] scratch (segments only)
+    bool products;       // the segments write their chunks' products (by_products)
+    float *seg;          // those: [chunk slots, units, 64 K]; otherwise [segment slots, units, K, 64]
     float *seg_gam;      // [segment slots, H]
     const float *first;  // h0 or dht, nullable
     float *last;         // final state or dh0, nullable
@@ -182,6 +183,7 @@ cudaError_t launch_gates(const ScanArgs &a, const Gates &g);
 cudaError_t launch_states(const StateArgs &s);
 // Segments that a problem's state passes are cut into, and their scratch.
 int chunks_per_segment(const ScanArgs &a);
+bool by_products(const ScanArgs &a);
 size_t segment_bytes(const ScanArgs &a);
 
 cudaError_t launch_out(const ScanArgs &a, const Gates &g, const __nv_bfloat16 *tiles_hi);
