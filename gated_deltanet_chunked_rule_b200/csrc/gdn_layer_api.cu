@@ -92,16 +92,18 @@ bool scan_on_tensor_cores(const ScanArgs &a) {
 // What the forward keeps: the gates, and every chunk's entry state, hi then lo.
 size_t scan_saved_bytes(const ScanArgs &a) { return scan_tc::gates_bytes(a) + 2 * align_up(scan_tc::tile_bytes(a)); }
 
-// Forward workspace: segment scratch | gates | entry states (hi; both for a call that keeps none).
+// Forward workspace: segment scratch | for a call that keeps nothing: gates | entry states (hi) |
+// segments' starts.
 struct ScanFwdLayout {
-    size_t seg, gates, tiles, total;
+    size_t seg, gates, tiles, local, total;
 };
 ScanFwdLayout scan_fwd_layout(const ScanArgs &a) {
     ScanFwdLayout L;
     L.seg = 0;
     L.gates = L.seg + scan_tc::segment_bytes(a);
     L.tiles = L.gates + scan_tc::gates_bytes(a);
-    L.total = L.tiles + align_up(scan_tc::tile_bytes(a));
+    L.local = L.tiles + align_up(scan_tc::tile_bytes(a));
+    L.total = L.local + scan_tc::local_bytes(a);
     return L;
 }
 
@@ -134,8 +136,15 @@ cudaError_t scan_fwd_tc(const ScanArgs &a) {
     if (e != cudaSuccess) return e;
     scan_tc::StateArgs s = state_pass(a, gates, false, ws + L.seg);
     s.tiles = saved ? tile_pair(saved + scan_tc::gates_bytes(a), a) : scan_tc::Tiles{(__nv_bfloat16 *)(ws + L.tiles), nullptr};
+    scan_tc::Locals locals{};
+    if (!saved && scan_tc::local_bytes(a)) {
+        locals.seg_tokens = s.chunks_per_seg * scan_tc::kC;
+        s.starts = (__nv_bfloat16 *)(ws + L.local);
+        s.before = (float *)(ws + L.local + align_up((size_t)a.seq.slots(locals.seg_tokens) * a.H * a.P * a.K * 2));
+        locals.starts = s.starts, locals.before = s.before;
+    }
     if ((e = scan_tc::launch_states(s)) != cudaSuccess) return e;
-    return scan_tc::launch_out(a, gates, s.tiles.hi);
+    return scan_tc::launch_out(a, gates, s.tiles.hi, locals);
 }
 
 // Backward workspace: segment scratch | exit-state gradients (hi, lo) | the gradient kernel's

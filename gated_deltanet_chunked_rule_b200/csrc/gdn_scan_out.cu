@@ -2,7 +2,9 @@
 //
 //   y_r = sum_s P_rs x_s + e^{gam_r} (C h)_r + D x_r,   P_rs = e^{gam_r - gam_s} delta_s (C B^T)_rs, s <= r
 //
-// from the chunk's entry state h (bf16, kept by the state pass). No chunk depends on another.
+// from the chunk's entry state h (bf16, kept by the state pass), or with LOCAL from the state within
+// its segment, h_l, the segment's start h_s and the decay f between: C h = C h_l + f C h_s (each
+// tile rounded once, on terms of its own). No chunk depends on another.
 // A CTA (one per SM) takes one chunk and a run of heads of one group: S = C B^T is formed once
 // for all of them (tcgen05, 128 x 128 in tensor memory). Per head its rows are read back,
 // scaled and stored as a bf16 P tile; P X and C h are two products of 64 columns per unit,
@@ -33,25 +35,27 @@ constexpr int kThreads = kRowThreads + 128;
 // Registers: 640 threads are launched with 96 each; see the state kernel.
 constexpr int kRowRegs = 104, kAuxRegs = 64;
 static_assert(kRowThreads * kRowRegs + 128 * kAuxRegs <= kThreads * 96, "register split");
-constexpr int kCt = 0, kP = 32768, kX = 98304, kHt = 147456;  // C | P [2] (B first, in the first's) | x [3] | h [2]
+// C | P [2] (B first, in the first's) | x [3] | h [2] | h_s [2]
+constexpr int kCt = 0, kP = 32768, kX = 98304, kHt = 147456, kHs = 180224;
 struct Vec {
     float col[4][kC];  // [w][s]: e^{(start of row block w) - gam_s} delta_s left of block w, delta_s in it
     float gl[kC];      // log2 decay from the block's start
 };
-constexpr int kVec = 180224;
+constexpr int kVec = 212992;
 constexpr int kBarsAt = kVec + 2 * sizeof(Vec);
 constexpr int kSmem = kBarsAt + 256 + 1024;
 static_assert(kSmem <= 227 * 1024, "shared memory");
-constexpr uint32_t kColS = 0, kColY = 128;  // S | [2]: P X, C h
+constexpr uint32_t kColS = 0, kColY = 128, kYCols = 192;  // S | [2]: P X, C h, C h_s
 
 struct OutP {
     Params p;
     int run;  // heads of a CTA
     const __nv_bfloat16 *tiles;
     __nv_bfloat16 *y;
+    Locals locals;
 };
 
-template <int K>
+template <int K, bool LOCAL>
 __global__ void __launch_bounds__(kThreads, 1)
 scan_out_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_c,
                 const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_y, const OutP q) {
@@ -66,6 +70,7 @@ scan_out_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant_
     if (!p.m.slot(blockIdx.x, kC, &n, &local)) return;
     const int t0 = p.m.begin(n) + local * kC, len = min(kC, p.m.end(n) - t0);
     const bool full_chunk = len == kC;
+    const size_t seg_slot = LOCAL ? p.m.slot0(n, q.locals.seg_tokens) + (size_t)local * kC / q.locals.seg_tokens : 0;
 
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kBarsAt);
     uint64_t *cb_full = bars, *s_full = bars + 1, *x_full = bars + 2, *h_full = bars + 5, *y_full = bars + 7, *p_ready = bars + 9,
@@ -110,13 +115,18 @@ scan_out_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant_
             }
             constexpr uint32_t id = idesc_bf16(128, 64, false, true);
             for (int i = 0; i < units && ok; ++i) {
-                const uint32_t d = tmem + kColY + (i & 1) * 128, h = state_rows(sb + kHt + (i & 1) * 16384);
+                const uint32_t d = tmem + kColY + (i & 1) * kYCols, h = state_rows(sb + kHt + (i & 1) * 16384);
                 if (i > 1) ok = wait_bar(&y_done[(i - 2) % 3], ((i - 2) / 3) & 1, abort_flag);  // its accumulators are read
                 ok = ok && wait_bar(&h_full[i & 1], (i >> 1) & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < K / 16; ++k) mma<kTokenHi, kStateRowsHi<K>>(d + 64, c + cstep(k), h + srstep(k), id, k > 0);
+                if (LOCAL) {
+                    const uint32_t hs = state_rows(sb + kHs + (i & 1) * 16384);
+#pragma unroll
+                    for (int k = 0; k < K / 16; ++k) mma<kTokenHi, kStateRowsHi<K>>(d + 128, c + cstep(k), hs + srstep(k), id, k > 0);
+                }
                 ok = wait_bar(&x_full[i % 3], (i / 3) & 1, abort_flag) && wait_bar(&p_ready[i & 1], (i >> 1) & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
@@ -135,7 +145,10 @@ scan_out_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant_
                 tma_load_3d(smem + kX + i % 3 * 16384, &tm_x, &x_full[i % 3], p.col0(u), p.head(g, u), t0);
             };
             auto load_h = [&](int i) {
-                mbar_arrive_expect_tx(&h_full[i & 1], K * kPT * 2);
+                mbar_arrive_expect_tx(&h_full[i & 1], (LOCAL ? 2 : 1) * K * kPT * 2);
+                if (LOCAL)
+                    bulk_load(smem + kHs + (i & 1) * 16384, q.locals.starts + ((seg_slot * p.G + g) * p.U + u_first + i) * (K * kPT), K * kPT * 2,
+                              &h_full[i & 1]);
                 bulk_load(smem + kHt + (i & 1) * 16384, q.tiles + (((size_t)blockIdx.x * p.G + g) * p.U + u_first + i) * (K * kPT),
                           K * kPT * 2, &h_full[i & 1]);
             };
@@ -209,7 +222,7 @@ scan_out_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant_
         const int wr = warp & 3, qd = warp >> 2, row = wr * 32 + lane;  // row block, column quarter
         const bool live = row < len;
         const uint32_t lanes = (uint32_t)(wr * 32) << 16;
-        float g_f, g_d;
+        float g_f, g_d, g_s = 0.f;
         float4 g_tot;
         bool ok = true;
         auto fetch = [&](int i) {
@@ -217,9 +230,10 @@ scan_out_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant_
             g_f = p.gates.at(blockIdx.x, p.H, h)[kC + row];
             g_tot = p.gates.totals(blockIdx.x, p.H, h);
             g_d = p.D ? p.D[h] : 0.f;
+            if (LOCAL) g_s = q.locals.before[(size_t)blockIdx.x * p.H + h];
         };
         fetch(0);
-        float e_next = 0.f, d_next = 0.f;  // e^{gam_r} and D of the head masked last
+        float e_next = 0.f, d_next = 0.f, s_next = 0.f;  // e^{gam_r}, D and e^{gam_r} f of the head masked last
         // unit i's P (where it begins a head), and leave for its product
         auto mask = [&](int i) {
             if ((i & (p.S - 1)) == 0) {
@@ -229,6 +243,7 @@ scan_out_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant_
                 around(g_tot, wr, &before, &after, &all);
                 e_next = ex2(before + g_f);
                 d_next = g_d;
+                if (LOCAL) s_next = ex2(g_s + before + g_f);
                 const float me = g_f;
                 if (i + p.S < units) fetch(i + p.S);
                 ok = __all_sync(0xffffffffu, ok && wait_bar(&v_full[hb], (i >> p.sh >> 1) & 1, abort_flag));
@@ -290,22 +305,29 @@ scan_out_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant_
         mask(0);
         for (int i = 0; i < units; ++i) {
             const int u = u_first + i, h = p.head(g, u);
-            const float e_r = e_next, D = d_next;
+            const float e_r = e_next, D = d_next, s_r = s_next;
             if (i + 1 < units) mask(i + 1);
             const uint32_t xb = sb + kX + i % 3 * 16384;
             ok = __all_sync(0xffffffffu, ok && wait_bar(&y_full[i & 1], (i >> 1) & 1, abort_flag) &&
                                              wait_bar(&x_full[i % 3], (i / 3) & 1, abort_flag));
             tc_fence_after();
             if (ok) {
-                const uint32_t d = tmem + lanes + kColY + (i & 1) * 128 + 16 * qd;
-                uint32_t a[16], b[16];
+                const uint32_t d = tmem + lanes + kColY + (i & 1) * kYCols + 16 * qd;
+                uint32_t a[16], b[16], hs[LOCAL ? 16 : 1];
                 tmem_ld16_nowait(d, a);
                 tmem_ld16_nowait(d + 64, b);
+                if constexpr (LOCAL) tmem_ld16_nowait(d + 128, hs);
                 uint4 xv[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) xv[j] = ld_shared_v4(xb + piece(row, 2 * qd + j));
                 tmem_landed(a);
                 tmem_landed(b);
+                if constexpr (LOCAL) {
+                    tmem_landed(hs);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        a[c] = __float_as_uint(fmaf(s_r, __uint_as_float(hs[c]), __uint_as_float(a[c])));
+                }
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const uint32_t w[4] = {xv[j].x, xv[j].y, xv[j].z, xv[j].w};
@@ -336,14 +358,14 @@ scan_out_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant_
     }
 }
 
-template <int K>
-cudaError_t run(const ScanArgs &a, const Gates &gates, const __nv_bfloat16 *tiles) {
+template <int K, bool LOCAL>
+cudaError_t run(const ScanArgs &a, const Gates &gates, const __nv_bfloat16 *tiles, const Locals &locals) {
     if (a.seq.total == 0) return cudaSuccess;
     CUtensorMap mb, mc, mx, my;
     if (!token_map(&mb, a.B, a.K, a.G, a.bs, a.seq.total) || !token_map(&mc, a.C, a.K, a.G, a.cs, a.seq.total) ||
         !token_map(&mx, a.x, a.P, a.H, a.xs, a.seq.total) || !token_map(&my, a.y, a.P, a.H, (long long)a.H * a.P, a.seq.total))
         return cudaErrorInvalidValue;
-    OutP q{params(a, gates), 1, tiles, (__nv_bfloat16 *)a.y};
+    OutP q{params(a, gates), 1, tiles, (__nv_bfloat16 *)a.y, locals};
     const int slots = a.seq.slots(kC), hg = a.H / a.G, sms = sm_count();
     // Heads per CTA: a CTA costs about four units' time before its first (its tiles, S); the fewest
     // waves times that length.
@@ -353,7 +375,7 @@ cudaError_t run(const ScanArgs &a, const Gates &gates, const __nv_bfloat16 *tile
         const double cost = (double)((ctas + sms - 1) / sms) * (r * q.p.S + 4);
         if (cost < best) best = cost, q.run = r;
     }
-    auto kernel = scan_out_kernel<K>;
+    auto kernel = scan_out_kernel<K, LOCAL>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     TimedLaunch t("scan_out", a.stream);
@@ -363,8 +385,9 @@ cudaError_t run(const ScanArgs &a, const Gates &gates, const __nv_bfloat16 *tile
 
 }  // namespace
 
-cudaError_t launch_out(const ScanArgs &a, const Gates &g, const __nv_bfloat16 *tiles_hi) {
-    return a.K == 128 ? run<128>(a, g, tiles_hi) : run<64>(a, g, tiles_hi);
+cudaError_t launch_out(const ScanArgs &a, const Gates &g, const __nv_bfloat16 *tiles_hi, const Locals &locals) {
+    if (locals.seg_tokens) return a.K == 128 ? run<128, true>(a, g, tiles_hi, locals) : run<64, true>(a, g, tiles_hi, locals);
+    return a.K == 128 ? run<128, false>(a, g, tiles_hi, locals) : run<64, false>(a, g, tiles_hi, locals);
 }
 
 }  // namespace scan_tc

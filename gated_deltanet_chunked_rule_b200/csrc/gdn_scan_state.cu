@@ -26,7 +26,12 @@
 // from L2. Beyond that size the products would go through memory twice, and instead a first pass
 // takes every segment from a zero state, one small kernel composes the segments' starts (their
 // operator is one scalar decay), and a second pass walks them again. 2 x 4096 tokens, 16 heads of
-// 128 (67 MB of products): SPLIT_FIGURES.
+// 128 (67 MB of products): 26 + 22 us against 25 + 10 + 29. A forward that keeps nothing needs no second
+// pass: the tiles of the first one, the segments' starts and one factor per chunk are enough for
+// the outputs (8192 tokens, 64 heads: 40 us less of 162).
+#include <stdlib.h>
+#include <string.h>
+
 #include <algorithm>
 
 #include "gdn_scan_tc.cuh"
@@ -86,14 +91,16 @@ constexpr int kSmall = kMid + 65536;    // barriers
 constexpr int kSmem = kSmall + 256 + 1024;
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
-enum Pass { kWalk, kEnds, kProducts };  // the states; segment ends from zero; every chunk's product
+// The states; segment ends from zero; every chunk's product; states within each segment (the first
+// one's from the start state), its end and the log decay before each chunk.
+enum Pass { kWalk, kEnds, kProducts, kLocal };
 
 struct StateP {
     Params p;
     int seg_tokens;   // tokens of a segment
     Pass pass;
     const float *first;
-    float *last, *seg, *seg_gam;
+    float *last, *seg, *seg_gam, *before;
     Tiles tiles;
 };
 
@@ -127,7 +134,7 @@ scan_state_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constan
     const int h = mine ? p.head(g, u) : 0;
     const size_t user = (((size_t)n * p.H + h) * K + row) * p.P + (mine ? p.col0(u) : 0) + c0;  // in the user's states
     if (!used) {  // an empty sequence keeps its state
-        if (local == 0 && s_len == 0 && q.pass == kWalk && q.last && real)
+        if (local == 0 && s_len == 0 && (q.pass == kWalk || q.pass == kLocal) && q.last && real)
             for (int i = 0; i < kHalf; ++i) q.last[user + i] = q.first ? q.first[user + i] : 0.f;
         return;
     }
@@ -209,7 +216,8 @@ scan_state_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constan
         float st[kHalf];  // this thread's part of the state
         const size_t units = (size_t)p.G * p.U, unit = (size_t)g * p.U + u;
         float *const seg = q.seg + (((size_t)blockIdx.x * units + unit) * K + row) * kPT + c0;
-        const float *src = q.pass != kWalk ? nullptr : at_first ? (q.first ? q.first + user : nullptr) : seg;
+        const bool own = q.pass == kWalk || q.pass == kLocal;
+        const float *src = !own ? nullptr : at_first ? (q.first ? q.first + user : nullptr) : q.pass == kWalk ? seg : nullptr;
         if (real && src) {
 #pragma unroll
             for (int i = 0; i < kHalf; i += 4) {
@@ -221,7 +229,8 @@ scan_state_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constan
             for (int i = 0; i < kHalf; ++i) st[i] = 0.f;
         }
         const size_t slot0 = (size_t)p.m.slot0(n, kC) + (seg_begin - s_begin) / kC;
-        const bool keeps = q.tiles.hi && real && q.pass == kWalk;
+        const bool keeps = q.tiles.hi && real && own;
+        const bool notes = real && row == 0 && c0 == 0 && (u & (p.S - 1)) == 0;  // (one thread per head)
         auto keep = [&](int i) {  // the state on entry to chunk i of the walk
             if (!keeps) return;
             const size_t at = ((slot0 + chunk_at(i)) * units + unit) * (K * kPT) + (size_t)(c0 / 8) * K * 8 + row * 8;
@@ -263,6 +272,7 @@ scan_state_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constan
                 around(g_tot, wr, &before, &after, &all);
                 const float scale = REVERSE ? ex2(before + g_sum) : g_delta * ex2(after + g_sum);
                 decay = ex2(all);
+                if (q.pass == kLocal && notes) q.before[(slot0 + chunk_at(i)) * p.H + h] = gam_sum;
                 gam_sum += all;
                 fetch(i + 1);
                 // a wait that expired: no more work and no more waits, but every barrier of the
@@ -331,12 +341,12 @@ scan_state_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constan
         }
         if (!ok) fail();
         if (real && ok && q.pass != kProducts) {
-            float *out = q.pass == kEnds ? seg : at_last && q.last ? q.last + user : nullptr;
+            float *out = q.pass == kEnds || q.pass == kLocal ? seg : at_last && q.last ? q.last + user : nullptr;
             if (out)
 #pragma unroll
                 for (int i = 0; i < kHalf; i += 4)
                     *reinterpret_cast<float4 *>(out + i) = make_float4(st[i], st[i + 1], st[i + 2], st[i + 3]);
-            if (q.pass == kEnds && row == 0 && c0 == 0 && (u & (p.S - 1)) == 0) q.seg_gam[(size_t)blockIdx.x * p.H + h] = gam_sum;
+            if ((q.pass == kEnds || q.pass == kLocal) && notes) q.seg_gam[(size_t)blockIdx.x * p.H + h] = gam_sum;
         }
         tc_fence_before();
     }
@@ -369,6 +379,44 @@ scan_compose_kernel(Params p, int seg_tokens, const float *__restrict__ first, f
         if (i + 2 < segs) end = *at(i + 1), gam = seg_gam[slot(i + 1) * p.H + h];
         cur = make_float4(fmaf(d, cur.x, v.x), fmaf(d, cur.y, v.y), fmaf(d, cur.z, v.z), fmaf(d, cur.w, v.w));
         *at(i + 1) = cur;  // the first segment starts from `first` itself
+    }
+}
+
+// After a pass within the segments: each segment's start as a bf16 tile (zero for a sequence's
+// first, whose chunks have it in them), and the last state. A thread per row and eight columns.
+template <int K>
+__global__ void __launch_bounds__(256)
+scan_starts_kernel(Params p, int seg_tokens, const float *__restrict__ seg, const float *__restrict__ seg_gam,
+                   __nv_bfloat16 *__restrict__ starts, float *__restrict__ last) {
+    const int n = blockIdx.x, unit = blockIdx.y, e = blockIdx.z * 256 + threadIdx.x, row = e % K, c8 = e / K;
+    const int len = p.m.end(n) - p.m.begin(n), segs = (len + seg_tokens - 1) / seg_tokens;
+    if (segs == 0) return;
+    const int h = p.head(unit / p.U, unit % p.U);
+    const size_t slot0 = p.m.slot0(n, seg_tokens), units = (size_t)p.G * p.U;
+    float st[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) st[k] = 0.f;
+    auto end_at = [&](int i) { return seg + (((slot0 + i) * units + unit) * K + row) * kPT + c8 * 8; };
+    float4 a = *reinterpret_cast<const float4 *>(end_at(0)), b = *reinterpret_cast<const float4 *>(end_at(0) + 4);
+    float gam = seg_gam[slot0 * p.H + h];
+    for (int i = 0; i < segs; ++i) {
+        uint32_t hi[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) hi[k] = pack_bf16(st[2 * k], st[2 * k + 1]);
+        *reinterpret_cast<uint4 *>(starts + ((slot0 + i) * units + unit) * (K * kPT) + ((size_t)c8 * K + row) * 8) =
+            make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        const float d = ex2(gam), v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        if (i + 1 < segs) {
+            a = *reinterpret_cast<const float4 *>(end_at(i + 1)), b = *reinterpret_cast<const float4 *>(end_at(i + 1) + 4);
+            gam = seg_gam[(slot0 + i + 1) * p.H + h];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) st[k] = i ? fmaf(d, st[k], v[k]) : v[k];
+    }
+    if (last) {
+        float *out = last + (((size_t)n * p.H + h) * K + row) * p.P + p.col0(unit % p.U) + c8 * 8;
+        *reinterpret_cast<float4 *>(out) = make_float4(st[0], st[1], st[2], st[3]);
+        *reinterpret_cast<float4 *>(out + 4) = make_float4(st[4], st[5], st[6], st[7]);
     }
 }
 
@@ -454,6 +502,18 @@ cudaError_t run(const StateArgs &s) {
         scan_chunks_kernel<K, REVERSE><<<dim3(a.seq.N, a.G * q.p.U, K * kPT / 2048), 256, 0, a.stream>>>(q.p, s.seg, s.first, s.last, s.tiles);
         return cudaGetLastError();
     }
+    if (s.starts) {
+        {
+            TimedLaunch t("scan_state_local", a.stream);
+            q.pass = kLocal;
+            q.before = s.before;
+            kernel<<<grid, kThreads, kSmem, a.stream>>>(mb, mx, q);
+        }
+        TimedLaunch t("scan_starts", a.stream);
+        scan_starts_kernel<K><<<dim3(a.seq.N, a.G * q.p.U, K * kPT / 2048), 256, 0, a.stream>>>(q.p, q.seg_tokens, s.seg, s.seg_gam, s.starts,
+                                                                                            s.last);
+        return cudaGetLastError();
+    }
     if (split) {
         q.pass = kEnds;
         {
@@ -496,6 +556,8 @@ int chunks_per_segment(const ScanArgs &a) {
 constexpr size_t kProductBytes = (size_t)100 << 20;
 
 bool by_products(const ScanArgs &a) {
+    const char *e = getenv("GDN_SCAN_SPLIT");  // "segments": never (the tests reach that path at small sizes by it)
+    if (e && strcmp(e, "segments") == 0) return false;
     return chunks_per_segment(a) > 0 && 2 * tile_bytes(a) <= kProductBytes;
 }
 
@@ -505,6 +567,12 @@ size_t segment_bytes(const ScanArgs &a) {
     if (by_products(a)) return align_up(2 * tile_bytes(a));
     const size_t slots = a.seq.slots(c * kC);
     return align_up(slots * a.H * (a.P / kPT) * kPT * a.K * 4) + align_up(slots * a.H * 4);
+}
+
+size_t local_bytes(const ScanArgs &a) {
+    const int c = chunks_per_segment(a);
+    if (!c || by_products(a)) return 0;
+    return align_up((size_t)a.seq.slots(c * kC) * a.H * a.P * a.K * 2) + align_up((size_t)a.seq.slots(kC) * a.H * 4);
 }
 
 cudaError_t launch_states(const StateArgs &s) {

@@ -175,6 +175,8 @@ struct StateArgs {
     bool products;       // the segments write their chunks' products (by_products)
     float *seg;          // those: [chunk slots, units, 64 K]; otherwise [segment slots, units, K, 64]
     float *seg_gam;      // [segment slots, H]
+    __nv_bfloat16 *starts;  // nullable: one pass within the segments only (forward, nothing kept); their
+    float *before;          // starts as tiles, and the log decay from there to each chunk [slots, H]
     const float *first;  // h0 or dht, nullable
     float *last;         // final state or dh0, nullable
     Tiles tiles;         // hi nullable: no tiles kept
@@ -186,7 +188,14 @@ int chunks_per_segment(const ScanArgs &a);
 bool by_products(const ScanArgs &a);
 size_t segment_bytes(const ScanArgs &a);
 
-cudaError_t launch_out(const ScanArgs &a, const Gates &g, const __nv_bfloat16 *tiles_hi);
+// starts, before: as StateArgs', where the tiles are within segments of seg_tokens only.
+size_t local_bytes(const ScanArgs &a);
+struct Locals {
+    int seg_tokens;  // 0: the tiles are whole
+    const __nv_bfloat16 *starts;
+    const float *before;
+};
+cudaError_t launch_out(const ScanArgs &a, const Gates &g, const __nv_bfloat16 *tiles_hi, const Locals &locals);
 
 // Gradients from every chunk's entry state h and exit gradient g; scratch of grad_bytes.
 size_t grad_bytes(const ScanArgs &a);

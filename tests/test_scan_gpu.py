@@ -141,14 +141,31 @@ def test_batch_of_slices_without_saved(gdn, dtype, slow):
         assert torch.equal(got[k], kept[k]), k
 
 
-@pytest.mark.parametrize("lens,packed", [([1100], False), ([1025, 1, 0, 70, 1300], True), ([640] * 2, False), ([1536], True)])
+SEGMENTED = [([1100], False), ([1025, 1, 0, 70, 1300], True), ([640] * 2, False), ([1536], True)]
+
+
+@pytest.mark.parametrize("lens,packed", SEGMENTED)
 @pytest.mark.parametrize("K,P,H", [(128, 64, 1), (64, 128, 2)])
-def test_sequences_cut_into_segments(gdn, lens, packed, K, P, H):
-    # few heads and many chunks: state passes over segments of a sequence, composed; ends on and
-    # off the segments' borders, beside short and empty sequences
+def test_sequences_cut_into_segments(gdn, monkeypatch, lens, packed, K, P, H):
+    # few heads and many chunks: state passes over segments of a sequence; ends on and off the
+    # segments' borders, beside short and empty sequences. bf16 in every way the segments are joined:
+    # from the chunks' products, from the segments' ends in two passes (something kept), in one (nothing)
     for dtype in (torch.bfloat16, torch.float32):
         v = make(lens, H, 1, K, P, dtype, seed=21, packed=packed, slow=True)
-        verify(v, lens, True, train(gdn, v))
+        got = train(gdn, v)
+        verify(v, lens, True, got)
+        if dtype == torch.float32:
+            continue
+        once = gdn.chunk_selective_scan_fwd(*args(v), True, v["h0"], True, v["cu"])
+        assert torch.equal(once[0], got["y"]) and torch.equal(once[1], got["final"])
+        monkeypatch.setenv("GDN_SCAN_SPLIT", "segments")
+        verify(v, lens, True, train(gdn, v), "two passes ")
+        bare = train(gdn, v, save=False)
+        verify(v, lens, True, bare, "one pass ")
+        v["h0"] = None
+        y, fin, _ = gdn.chunk_selective_scan_fwd(*args(v), True, None, True, v["cu"])
+        verify(v, lens, True, {"y": y, "final": fin}, "one pass, no start ")
+        monkeypatch.delenv("GDN_SCAN_SPLIT")
 
 
 @pytest.mark.parametrize("H,G,P,lens", [(24, 1, 128, [300]), (40, 1, 64, [128, 200]), (48, 2, 128, [129]), (7, 1, 128, [256])])
