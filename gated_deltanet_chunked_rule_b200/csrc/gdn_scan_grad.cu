@@ -305,7 +305,11 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
 
         // masked Q summed over the units: columns 16 half .. of every block of 32 (so that a row block's
         // two warps share its diagonal block)
-        float msum[4][16] = {};
+        F2 msum[4][8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) msum[k][j] = f2(0.f, 0.f);
         float u_r = 0.f, e_r = 0.f, tail = 0.f, decay = 0.f, delta = 0.f, D = 0.f;
         float dgam = 0.f, wsum = 0.f, dD = 0.f;  // of the head so far (dgam, wsum: half 0)
         for (int i = 0; i < units; ++i) {
@@ -341,6 +345,8 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
             float ri = 0.f;
             if (ok) {
                 uint4 yr[4];
+                F2 dd2 = f2(0.f, 0.f);
+                const F2 ee = f2(e_r, e_r);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const uint32_t at = piece(row, half * 4 + j);
@@ -354,8 +360,9 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                     uint32_t o[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        dD = fmaf(bf_lo(w[k]), bf_lo(v[k]), fmaf(bf_hi(w[k]), bf_hi(v[k]), dD));
-                        o[k] = pack_bf16(e_r * bf_lo(w[k]), e_r * bf_hi(w[k]));
+                        const F2 yy = f2(bf_lo(w[k]), bf_hi(w[k]));
+                        dd2 = fma2(yy, f2(bf_lo(v[k]), bf_hi(v[k])), dd2);
+                        o[k] = pack_bf16(mul2(ee, yy));
                     }
                     st_shared_v4(sb + kSy + at, o[0], o[1], o[2], o[3]);
                     if (!live) {
@@ -363,18 +370,21 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                         st_shared_v4(sb + kY + at, 0u, 0u, 0u, 0u);
                     }
                 }
+                dD += get(dd2).x + get(dd2).y;
                 wait(ch_full, i & 1);
                 tc_fence_after();
                 float v[32];
                 if (ok) {
                     tmem_ld32(tmem + lanes + kColR + 32 * half, v);
+                    F2 ri2 = f2(0.f, 0.f);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const uint32_t w[4] = {yr[j].x, yr[j].y, yr[j].z, yr[j].w};
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) ri = fmaf(bf_lo(w[k]), v[8 * j + 2 * k], fmaf(bf_hi(w[k]), v[8 * j + 2 * k + 1], ri));
+                        for (int k = 0; k < 4; ++k)
+                            ri2 = fma2(f2(bf_lo(w[k]), bf_hi(w[k])), f2(v[8 * j + 2 * k], v[8 * j + 2 * k + 1]), ri2);
                     }
-                    ri = live ? e_r * ri : 0.f;
+                    ri = live ? e_r * (get(ri2).x + get(ri2).y) : 0.f;
                 }
             }
             fence_proxy_async();
@@ -422,21 +432,25 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                     tmem_landed(sr);
                     tmem_landed(vr);
                     const float4 *dl = reinterpret_cast<const float4 *>(vec.delta + 32 * k + 16 * half);
-                    float rs = 0.f;
+                    F2 rs2 = f2(0.f, 0.f);
+                    uint32_t o[8];
                     if (k < wr) {
                         const float4 *ve = reinterpret_cast<const float4 *>(vec.v[wr] + 32 * k + 16 * half);
+                        const F2 uu = f2(u_r, u_r);
 #pragma unroll
                         for (int j4 = 0; j4 < 4; ++j4) {
                             const float4 d4 = dl[j4], v4 = ve[j4];
-                            const float d[4] = {d4.x, d4.y, d4.z, d4.w}, e[4] = {v4.x, v4.y, v4.z, v4.w};
+                            const F2 d[2] = {f2(d4.x, d4.y), f2(d4.z, d4.w)}, e[2] = {f2(v4.x, v4.y), f2(v4.z, v4.w)};
 #pragma unroll
-                            for (int jj = 0; jj < 4; ++jj) {
-                                const int j = 4 * j4 + jj;
-                                const float qv = __uint_as_float(vr[j]), L = u_r * e[jj], s = L * __uint_as_float(sr[j]);
-                                msum[k][j] = fmaf(L * d[jj], qv, msum[k][j]);
-                                sr[j] = __float_as_uint(s);
-                                w[b][j] = s * qv;
-                                rs = fmaf(w[b][j], d[jj], rs);
+                            for (int jj = 0; jj < 2; ++jj) {
+                                const int j = 2 * j4 + jj;
+                                const F2 qv = f2(vr[2 * j], vr[2 * j + 1]), L = mul2(uu, e[jj]);
+                                msum[k][j] = fma2(mul2(L, d[jj]), qv, msum[k][j]);
+                                const F2 s = mul2(L, f2(sr[2 * j], sr[2 * j + 1])), ww = mul2(s, qv);
+                                o[j] = pack_bf16(s);
+                                rs2 = fma2(ww, d[jj], rs2);
+                                const float2 w2 = get(ww);
+                                w[b][2 * j] = w2.x, w[b][2 * j + 1] = w2.y;
                             }
                         }
                     } else {
@@ -446,33 +460,31 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
 #pragma unroll
                         for (int j4 = 0; j4 < 4; ++j4) {
                             const float4 d4 = dl[j4], v4 = gl[j4];
-                            const float d[4] = {d4.x, d4.y, d4.z, d4.w}, e[4] = {v4.x, v4.y, v4.z, v4.w};
+                            const F2 d[2] = {f2(d4.x, d4.y), f2(d4.z, d4.w)};
+                            const float e[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
-                            for (int jj = 0; jj < 4; ++jj) {
-                                const int j = 4 * j4 + jj;
+                            for (int jj = 0; jj < 2; ++jj) {
+                                const int j = 2 * j4 + jj, c = 16 * half + 2 * j - lane;
                                 // masked by bits, not by a branch: all ones where column <= row, where < row
-                                const uint32_t on = (uint32_t)((16 * half + j - 1 - lane) >> 31), below = (uint32_t)((16 * half + j - lane) >> 31);
-                                const float qv = __uint_as_float(vr[j]);
-                                const float L = __uint_as_float(__float_as_uint(ex2(me - e[jj])) & on);
-                                const float s = L * __uint_as_float(sr[j]), ww = s * qv;
-                                msum[k][j] = fmaf(L * d[jj], qv, msum[k][j]);
-                                sr[j] = __float_as_uint(s);
-                                diag += __uint_as_float(__float_as_uint(ww) & (on ^ below));
-                                w[b][j] = __uint_as_float(__float_as_uint(ww) & below);
-                                rs = fmaf(w[b][j], d[jj], rs);
+                                const uint32_t on0 = (uint32_t)((c - 1) >> 31), below0 = (uint32_t)(c >> 31), on1 = below0, below1 = (uint32_t)((c + 1) >> 31);
+                                const F2 qv = f2(vr[2 * j], vr[2 * j + 1]);
+                                const F2 L = f2(__float_as_uint(ex2(me - e[2 * jj])) & on0, __float_as_uint(ex2(me - e[2 * jj + 1])) & on1);
+                                msum[k][j] = fma2(mul2(L, d[jj]), qv, msum[k][j]);
+                                const F2 s = mul2(L, f2(sr[2 * j], sr[2 * j + 1]));
+                                const float2 w2 = get(mul2(s, qv));
+                                o[j] = pack_bf16(s);
+                                diag += __uint_as_float(__float_as_uint(w2.x) & (on0 ^ below0)) + __uint_as_float(__float_as_uint(w2.y) & (on1 ^ below1));
+                                w[b][2 * j] = __uint_as_float(__float_as_uint(w2.x) & below0);
+                                w[b][2 * j + 1] = __uint_as_float(__float_as_uint(w2.y) & below1);
+                                rs2 = fma2(f2(w[b][2 * j], w[b][2 * j + 1]), d[jj], rs2);
                             }
                         }
                         if (half == lane >> 4) vec.wdiag[row] = diag;
                     }
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        uint32_t o[4];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            o[c] = pack_bf16(__uint_as_float(sr[8 * j + 2 * c]), __uint_as_float(sr[8 * j + 2 * c + 1]));
-                        st_shared_v4(at[j], o[0], o[1], o[2], o[3]);
-                    }
-                    vec.rsum[half][k][row] = rs;
+                    st_shared_v4(at[0], o[0], o[1], o[2], o[3]);
+                    st_shared_v4(at[1], o[4], o[5], o[6], o[7]);
+                    const float2 rs = get(rs2);
+                    vec.rsum[half][k][row] = rs.x + rs.y;
                 }
                 if (2 * kp <= wr) {
                     const float cs = lane_sums(w[0], w[1], lane);
@@ -516,7 +528,8 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                 for (int j = 0; j < 4; ++j) yr[j] = ld_shared_v4(sb + kY + piece(row, half * 4 + j));
                 tmem_landed(ar);
                 tmem_landed(br);
-                float s = 0.f;
+                F2 s2 = f2(0.f, 0.f);
+                const F2 tt = f2(tail, tail), de = f2(delta, delta), dd = f2(D, D);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const uint32_t y[4] = {yr[j].x, yr[j].y, yr[j].z, yr[j].w}, v[4] = {xr[j].x, xr[j].y, xr[j].z, xr[j].w};
@@ -524,10 +537,9 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int c = 8 * j + 2 * k;
-                        const float b0 = __uint_as_float(br[c]), b1 = __uint_as_float(br[c + 1]);
-                        s = fmaf(bf_lo(v[k]), b0, fmaf(bf_hi(v[k]), b1, s));
-                        o[k] = pack_bf16(fmaf(delta, fmaf(tail, b0, __uint_as_float(ar[c])), D * bf_lo(y[k])),
-                                         fmaf(delta, fmaf(tail, b1, __uint_as_float(ar[c + 1])), D * bf_hi(y[k])));
+                        const F2 bb = f2(br[c], br[c + 1]);
+                        s2 = fma2(f2(bf_lo(v[k]), bf_hi(v[k])), bb, s2);
+                        o[k] = pack_bf16(fma2(de, fma2(tt, bb, f2(ar[c], ar[c + 1])), mul2(dd, f2(bf_lo(y[k]), bf_hi(y[k])))));
                     }
                     if (full_chunk)
                         st_shared_v4(sb + kSy + piece(row, half * 4 + j), o[0], o[1], o[2], o[3]);
@@ -535,7 +547,8 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                         *reinterpret_cast<uint4 *>(q.dx + ((size_t)(t0 + row) * p.H + h) * p.P + p.col0(u) + half * 32 + 8 * j) =
                             make_uint4(o[0], o[1], o[2], o[3]);
                 }
-                vec.bt[half][row] = live ? tail * s : 0.f;
+                const float2 s = get(s2);
+                vec.bt[half][row] = live ? tail * (s.x + s.y) : 0.f;
             }
             fence_proxy_async();
             tc_fence_before();
@@ -602,9 +615,8 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
             if (k > wr) continue;  // zeros stand there
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                st_shared_v4(sb + kPm + (k >> 1) * 16384 + piece(row, 4 * (k & 1) + 2 * half + j), pack_bf16(msum[k][8 * j], msum[k][8 * j + 1]),
-                             pack_bf16(msum[k][8 * j + 2], msum[k][8 * j + 3]), pack_bf16(msum[k][8 * j + 4], msum[k][8 * j + 5]),
-                             pack_bf16(msum[k][8 * j + 6], msum[k][8 * j + 7]));
+                st_shared_v4(sb + kPm + (k >> 1) * 16384 + piece(row, 4 * (k & 1) + 2 * half + j), pack_bf16(msum[k][4 * j]),
+                             pack_bf16(msum[k][4 * j + 1]), pack_bf16(msum[k][4 * j + 2]), pack_bf16(msum[k][4 * j + 3]));
         }
         fence_proxy_async();
         tc_fence_before();
