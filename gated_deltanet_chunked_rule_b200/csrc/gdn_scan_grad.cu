@@ -26,9 +26,19 @@
 // (L o S)^T dY and B g'; e^{gam} dY h^T and X g'^T run while the mask is applied. Warps 0-7: a
 // thread per row and column half; warp 8 issues the products on the work region, warp 9 those of
 // dC and dB, warp 10 loads (TMA, bulk copies) and stores: a tile's next load is issued as soon as
-// its last reader is done, dx leaves through the scaled dY's tile so that dY's can be refilled at
-// once. The row warps need the registers of the copying and issuing ones: beside 220 KB of shared
-// memory the L1 holds no spills, and with 60 spilled words the mask alone took 12000 cycles.
+// its last reader is done; dY has two tiles, and dx leaves through its dY's. The row warps need the
+// registers of the copying and issuing ones: beside 220 KB of shared memory the L1 holds no spills,
+// and with 60 spilled words the mask alone took 12000 cycles. What the gates' gradients are made of
+// (row and column sums) goes to memory, and a small kernel scans it: in the row warps the scans and
+// the barriers they need cost 2500 cycles per head.
+//
+// Bound by the chain of one unit's stages, about 10000 cycles: the mask takes 3400 (row block 3,
+// whose two warps share a scheduler, has four column blocks to row block 0's one), the products
+// after it 1500, reading dx 1000. 2 x 4096 tokens, 16 heads of 128, K = 128: 117 us, and 13 us the
+// gates' gradients (150 with one fp32 operation per instruction, 135 with the scans in the row
+// warps and one dY tile); its tiles and rows alone are 250 MB, 39 us. Tried and not better: Q in two
+// halves with B g' under the mask (the products' operand reads then slow the row warps), 16 row
+// warps (spills).
 #include <algorithm>
 
 #include "gdn_scan_tc.cuh"
@@ -44,34 +54,39 @@ constexpr int kRowThreads = 256;
 constexpr int kThreads = kRowThreads + 128;
 constexpr int kRowRegs = 208, kAuxRegs = 88;  // 384 threads are launched with 168 each
 static_assert(kRowThreads * kRowRegs + 128 * kAuxRegs <= kThreads * 168, "register split");
-// B | C | P (L o S, at the end the summed masked Q) | x, then scaled x | dY | h hi, lo | g' hi, lo | scaled dY, then dx
-constexpr int kB = 0, kCt = 32768, kPm = 65536, kX = 98304, kY = 114688, kH = 131072, kG = 163840, kSy = 196608;
-constexpr int kVec = 212992;
+// B | C | P (L o S, at the end the summed masked Q) | x, then scaled x | dY, then dx | h hi, lo | g' hi, lo | scaled dY |
+// dY, then dx, of every second unit
+constexpr int kB = 0, kCt = 32768, kPm = 65536, kX = 98304, kY = 114688, kH = 131072, kG = 163840, kSy = 196608, kY1 = 212992;
+constexpr int kVec = 229376;
 struct Vec {
-    float v[4][kC];     // e^{(start of row block w) - gam_s} for s left of block w
+    float v[3][kC];     // [w - 1]: e^{(start of row block w) - gam_s} for s left of block w
     float gl[kC];       // log2 decay from the row block's start
     float delta[kC];
-    float rsum[2][4][kC];  // row sums of W delta per column half and block (strictly below the diagonal)
-    float csum[4][kC];  // column sums of W per row block (strictly below the diagonal)
-    float wdiag[kC];    // W_tt
-    float rowi[2][kC];  // e^{gam_r} dY_r.(C h)_r, per column half
-    float bt[2][kC];    // e^{gam_C - gam_s} x_s.(B g')_s, per column half
-    float tot[4][4];    // per row block: sums of rowi, delta bt, R[.][0], R[.][1]
-    float red[3][8];
 };
 constexpr int kBarsAt = kVec + (sizeof(Vec) + 15) / 16 * 16;
-constexpr int kSmem = kBarsAt + 256 + 1024;
+constexpr int kSmem = kBarsAt + 192;
 static_assert(kSmem <= 227 * 1024, "shared memory");
 constexpr uint32_t kColS = 0, kColR = 128, kColC = 256, kColB = 384;
+
+// What the gates' gradients are made of, of one unit (a head's 64 columns), per token; h: column
+// half, w: row block. The entries of blocks right of the diagonal are not written.
+struct Sums {
+    float rowi[2][kC];     // [h]: e^{gam_r} dY_r.(C h)_r
+    float bt[2][kC];       // [h]: e^{gam_C - gam_s} x_s.(B g')_s
+    float dD[2][kC];       // [h]: dY_r.x_r
+    float rsum[4][2][kC];  // [block][h]: row sums of W delta, strictly below the diagonal
+    float csum[4][kC];     // [w]: column sums of W, strictly below the diagonal
+    float wdiag[kC];       // W_tt
+    float hg[32];          // [warp]: <h, g'>
+};
 
 struct GradP {
     Params p;
     int run, runs;
     const __nv_bfloat16 *h_hi, *h_lo, *g_hi, *g_lo;
     __nv_bfloat16 *dx, *dB, *dC;
-    void *ddt;
+    Sums *sums;      // [slots, H, slices of a head]
     float *part_bc;  // [2][runs][total, G, K] where runs > 1
-    float *part;     // [slots, 3, H]: dA, ddt_bias, dD
 };
 
 // Sum over the warp's lanes of a[i], b[i], delivered to lane i (a), 16 + i (b).
@@ -105,35 +120,33 @@ __global__ void __launch_bounds__(kThreads, 1)
 scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_c,
                  const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_dy,
                  const __grid_constant__ CUtensorMap tm_dx, const GradP q) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = align_smem_1024(smem_raw);
+    extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sb = smem_u32(smem);
     const Params &p = q.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (sb & 1023) {  // the swizzled tiles' alignment
+        set_status(p.status, GDN_ERR_CUDA);
+        return;
+    }
     const int g = blockIdx.y / q.runs, run = blockIdx.y % q.runs, u_first = run * q.run;
     const int units = min(q.run, p.U - u_first);
     int n, local;
-    if (!p.m.slot(blockIdx.x, kC, &n, &local)) {  // an unused slot adds nothing
-        for (int i = tid; i < 3 * units; i += kThreads)
-            q.part[((size_t)blockIdx.x * 3 + i / units) * p.H + p.head(g, u_first + i % units)] = 0.f;
-        return;
-    }
+    if (!p.m.slot(blockIdx.x, kC, &n, &local)) return;
     const int t0 = p.m.begin(n) + local * kC, len = min(kC, p.m.end(n) - t0);
     const bool full_chunk = len == kC;
     constexpr int kTile = K * kPT * 2;
 
     Vec &vec = *reinterpret_cast<Vec *>(smem + kVec);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kBarsAt);
-    uint64_t *cb_full = bars, *h_full = bars + 1, *g_full = bars + 2, *x_full = bars + 3, *y_full = bars + 4;  // loads
-    uint64_t *ch_full = bars + 5, *q_full = bars + 6, *cd_full = bars + 7, *dx_full = bars + 8, *end_full = bars + 9;  // products
-    uint64_t *sy_free = bars + 10;                                                                               // dx is stored
+    uint64_t *cb_full = bars, *h_full = bars + 1, *g_full = bars + 2, *x_full = bars + 3, *y_full = bars + 4;  // loads; dY: two
+    uint64_t *ch_full = bars + 6, *q_full = bars + 7, *cd_full = bars + 8, *dx_full = bars + 9, *end_full = bars + 10;  // products
     uint64_t *cb_ready = bars + 11, *r_free = bars + 12, *s_ready = bars + 13, *p_ready = bars + 14, *hg_read = bars + 15,
-             *dx_done = bars + 16, *m_ready = bars + 17;  // the row threads
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 18);
+             *dx_done = bars + 16, *m_ready = bars + 18;  // the row threads; dx_done: two
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 19);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     if (tid == 0) {
         for (int i = 0; i < 11; ++i) mbar_init(bars + i, 1);
-        for (int i = 11; i < 18; ++i) mbar_init(bars + i, kRowThreads);
+        for (int i = 11; i < 19; ++i) mbar_init(bars + i, kRowThreads);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -157,8 +170,8 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
     reg_dec<kAuxRegs>();
     if (warp == 8) {  // products on the work region
         if (lane == 0) {
-            const uint32_t b = cols(sb + kB), c = cols(sb + kCt), y = cols(sb + kY), x = cols(sb + kX), yr = rows(sb + kY),
-                           pm = rows(sb + kPm), h0 = state_rows(sb + kH), h1 = state_rows(sb + kH + kTile),
+            uint32_t b = cols(sb + kB), c = cols(sb + kCt), y = cols(sb + kY), x = cols(sb + kX), yr = rows(sb + kY),
+                     pm = rows(sb + kPm), h0 = state_rows(sb + kH), h1 = state_rows(sb + kH + kTile),
                            g0 = state_rows(sb + kG), g1 = state_rows(sb + kG + kTile);
             bool ok = wait_bar(cb_full, 0, abort_flag) && wait_bar(cb_ready, 0, abort_flag);
             tc_fence_after();
@@ -167,8 +180,11 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                 for (int k = 0; k < K / 16; ++k) mma<kTokenHi, kTokenHi>(tmem + kColS, c + cstep(k), b + cstep(k), idQ, k > 0);
             }
             for (int i = 0; i < units && ok; ++i) {
+                // or the sums below are all formed ahead, in more registers than there are
+                asm volatile("" : "+r"(b), "+r"(c), "+r"(y), "+r"(x), "+r"(yr), "+r"(pm), "+r"(h0), "+r"(h1), "+r"(g0), "+r"(g1));
+                const uint32_t y2 = (i & 1) * ((kY1 - kY) >> 4);
                 // C h
-                if (i > 0) ok = wait_bar(dx_done, (i - 1) & 1, abort_flag);  // the work region is read
+                if (i > 0) ok = wait_bar(&dx_done[(i - 1) & 1], ((i - 1) >> 1) & 1, abort_flag);  // the work region is read
                 ok = ok && wait_bar(h_full, i & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
@@ -179,18 +195,18 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                 }
                 mma_commit(ch_full);
                 // Q = dY X^T
-                ok = wait_bar(x_full, i & 1, abort_flag) && wait_bar(y_full, i & 1, abort_flag) && wait_bar(r_free, i & 1, abort_flag);
+                ok = wait_bar(x_full, i & 1, abort_flag) && wait_bar(&y_full[i & 1], (i >> 1) & 1, abort_flag) && wait_bar(r_free, i & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < 4; ++k) mma<kTokenHi, kTokenHi>(tmem + kColR, y + cstep(k), x + cstep(k), idQ, k > 0);
+                for (int k = 0; k < 4; ++k) mma<kTokenHi, kTokenHi>(tmem + kColR, y + y2 + cstep(k), x + cstep(k), idQ, k > 0);
                 mma_commit(q_full);
                 // (L o S)^T dY and B g'
                 ok = wait_bar(g_full, i & 1, abort_flag) && wait_bar(p_ready, i & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < 8; ++k) mma<kTokenHi, kTokenHi>(tmem + kColR, pm + rstep(k), yr + rstep(k), idX, k > 0);
+                for (int k = 0; k < 8; ++k) mma<kTokenHi, kTokenHi>(tmem + kColR, pm + rstep(k), yr + y2 + rstep(k), idX, k > 0);
 #pragma unroll
                 for (int k = 0; k < K / 16; ++k) {
                     mma<kTokenHi, kStateRowsHi<K>>(tmem + kColR + 64, b + cstep(k), g0 + srstep(k), idH, k > 0);
@@ -253,7 +269,8 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
             int hs = 1, gs = 1, xs = 1, ys = 1;  // loads issued
             load_pair(kH, h_full, q.h_hi, q.h_lo, 0);
             load_rows(kX, x_full, &tm_x, 0);
-            load_rows(kY, y_full, &tm_dy, 0);
+            load_rows(kY, &y_full[0], &tm_dy, 0);
+            if (units > 1) load_rows(kY1, &y_full[1], &tm_dy, 1), ++ys;
             load_pair(kG, g_full, q.g_hi, q.g_lo, 0);
             bool ok = true;
             for (int i = 0; i < units && ok; ++i) {
@@ -264,16 +281,16 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                 if (ok && more) load_pair(kH, h_full, q.h_hi, q.h_lo, i + 1), ++hs;
                 ok = ok && wait_bar(dx_full, i & 1, abort_flag);
                 if (ok && more) load_pair(kG, g_full, q.g_hi, q.g_lo, i + 1), ++gs;
-                ok = ok && wait_bar(dx_done, i & 1, abort_flag);
+                ok = ok && wait_bar(&dx_done[i & 1], (i >> 1) & 1, abort_flag);
                 if (!ok) break;
-                if (more) load_rows(kY, y_full, &tm_dy, i + 1), ++ys;
-                if (full_chunk) {  // dx stands in the scaled dY's tile
+                const int y = i & 1 ? kY1 : kY;
+                if (full_chunk) {  // dx stands in dY's tile
                     const int u = u_first + i;
-                    tma_store_3d(&tm_dx, sb + kSy, p.col0(u), p.head(g, u), t0);
+                    tma_store_3d(&tm_dx, sb + y, p.col0(u), p.head(g, u), t0);
                     bulk_commit();
                     bulk_wait_read<0>();
                 }
-                mbar_arrive(sy_free);
+                if (i + 2 < units) load_rows(y, &y_full[i & 1], &tm_dy, i + 2), ++ys;
             }
             if (!ok) fail();
             // no copy outlives the CTA
@@ -281,7 +298,8 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
             done = drain(h_full, (hs - 1) & 1) && done;
             done = drain(g_full, (gs - 1) & 1) && done;
             done = drain(x_full, (xs - 1) & 1) && done;
-            done = drain(y_full, (ys - 1) & 1) && done;
+            done = drain(&y_full[0], ((ys + 1) / 2 - 1) & 1) && done;
+            if (ys > 1) done = drain(&y_full[1], (ys / 2 - 1) & 1) && done;
             if (!done) fail();
             bulk_wait_all();
         }
@@ -310,37 +328,42 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
         for (int k = 0; k < 4; ++k)
 #pragma unroll
             for (int j = 0; j < 8; ++j) msum[k][j] = f2(0.f, 0.f);
-        float u_r = 0.f, e_r = 0.f, tail = 0.f, decay = 0.f, delta = 0.f, D = 0.f;
-        float dgam = 0.f, wsum = 0.f, dD = 0.f;  // of the head so far (dgam, wsum: half 0)
+        float u_r = 0.f, e_r = 0.f, tail = 0.f, delta = 0.f, D = 0.f;
+        float n_delta, n_f, n_r, n_D;  // the next head's gates, on their way
+        float4 n_tot;
+        auto fetch = [&](int i) {
+            const int h = p.head(g, u_first + min(i, units - 1));
+            const float *gt = p.gates.at(blockIdx.x, p.H, h) + row;
+            n_delta = gt[0], n_f = gt[kC], n_r = gt[2 * kC];
+            n_tot = p.gates.totals(blockIdx.x, p.H, h);
+            n_D = p.D ? p.D[h] : 0.f;
+        };
+        fetch(0);
         for (int i = 0; i < units; ++i) {
             const int u = u_first + i, h = p.head(g, u);
-            if ((i & (p.S - 1)) == 0) {  // another head: its gates
-                const float *gt = p.gates.at(blockIdx.x, p.H, h) + row;
-                const float g_f = gt[kC], g_r = gt[2 * kC];
-                const float4 tot = p.gates.totals(blockIdx.x, p.H, h);
-                delta = gt[0];
-                D = p.D ? p.D[h] : 0.f;
+            Sums &sums = q.sums[((size_t)blockIdx.x * p.H + h) * p.S + (i & (p.S - 1))];
+            if ((i & (p.S - 1)) == 0) {  // another head: its gates (the last one's vectors are read: dx_full)
+                delta = n_delta, D = n_D;
                 float before, after, all;
-                around(tot, wr, &before, &after, &all);
-                u_r = ex2(g_f), e_r = ex2(before + g_f), tail = ex2(after + g_r), decay = ex2(all);
+                around(n_tot, wr, &before, &after, &all);
+                u_r = ex2(n_f), e_r = ex2(before + n_f), tail = ex2(after + n_r);
                 if (half == 0) {
-                    vec.gl[row] = g_f;
+                    vec.gl[row] = n_f;
                     vec.delta[row] = delta;
-                    const float t[4] = {tot.x, tot.y, tot.z, tot.w};
-                    float to = g_r;
+                    const float t[4] = {n_tot.x, n_tot.y, n_tot.z, n_tot.w};
+                    float to = n_r;
 #pragma unroll
                     for (int w = 1; w < 4; ++w)
                         if (w > wr) {
-                            vec.v[w][row] = ex2(to);
+                            vec.v[w - 1][row] = ex2(to);
                             to += t[w];
                         }
                 }
-                dgam = wsum = dD = 0.f;
             }
             // ---- rows of x and dY; e^gam dY for dC, dY.(C h)
             wait(x_full, i & 1);
-            wait(y_full, i & 1);
-            if (i > 0) wait(sy_free, (i - 1) & 1);
+            wait(&y_full[i & 1], (i >> 1) & 1);
+            const uint32_t yb = sb + (i & 1 ? kY1 : kY);
             uint4 xr[4];  // x, this half's 32 columns
             float ri = 0.f;
             if (ok) {
@@ -351,7 +374,7 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                 for (int j = 0; j < 4; ++j) {
                     const uint32_t at = piece(row, half * 4 + j);
                     xr[j] = live ? ld_shared_v4(sb + kX + at) : make_uint4(0u, 0u, 0u, 0u);
-                    yr[j] = live ? ld_shared_v4(sb + kY + at) : make_uint4(0u, 0u, 0u, 0u);
+                    yr[j] = live ? ld_shared_v4(yb + at) : make_uint4(0u, 0u, 0u, 0u);
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -367,10 +390,10 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                     st_shared_v4(sb + kSy + at, o[0], o[1], o[2], o[3]);
                     if (!live) {
                         st_shared_v4(sb + kX + at, 0u, 0u, 0u, 0u);
-                        st_shared_v4(sb + kY + at, 0u, 0u, 0u, 0u);
+                        st_shared_v4(yb + at, 0u, 0u, 0u, 0u);
                     }
                 }
-                dD += get(dd2).x + get(dd2).y;
+                sums.dD[half][row] = get(dd2).x + get(dd2).y;
                 wait(ch_full, i & 1);
                 tc_fence_after();
                 float v[32];
@@ -390,8 +413,8 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
             fence_proxy_async();
             tc_fence_before();
             mbar_arrive(r_free);
-            named_sync<kRowThreads>(1);  // the gate vectors are written, the last unit's sums are read
-            vec.rowi[half][row] = ri;
+            sums.rowi[half][row] = ri;
+            if ((i & (p.S - 1)) == 0) named_sync<kRowThreads>(1);  // the gate vectors are written
             // ---- Q is there and x read by it: scaled x in its place
             wait(q_full, i & 1);
             tc_fence_after();
@@ -435,7 +458,7 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                     F2 rs2 = f2(0.f, 0.f);
                     uint32_t o[8];
                     if (k < wr) {
-                        const float4 *ve = reinterpret_cast<const float4 *>(vec.v[wr] + 32 * k + 16 * half);
+                        const float4 *ve = reinterpret_cast<const float4 *>(vec.v[wr - 1] + 32 * k + 16 * half);
                         const F2 uu = f2(u_r, u_r);
 #pragma unroll
                         for (int j4 = 0; j4 < 4; ++j4) {
@@ -479,21 +502,22 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                                 rs2 = fma2(f2(w[b][2 * j], w[b][2 * j + 1]), d[jj], rs2);
                             }
                         }
-                        if (half == lane >> 4) vec.wdiag[row] = diag;
+                        if (half == lane >> 4) sums.wdiag[row] = diag;
                     }
                     st_shared_v4(at[0], o[0], o[1], o[2], o[3]);
                     st_shared_v4(at[1], o[4], o[5], o[6], o[7]);
                     const float2 rs = get(rs2);
-                    vec.rsum[half][k][row] = rs.x + rs.y;
+                    sums.rsum[k][half][row] = rs.x + rs.y;
                 }
                 if (2 * kp <= wr) {
                     const float cs = lane_sums(w[0], w[1], lane);
-                    vec.csum[wr][64 * kp + 32 * (lane >> 4) + 16 * half + (lane & 15)] = cs;
+                    sums.csum[wr][64 * kp + 32 * (lane >> 4) + 16 * half + (lane & 15)] = cs;
                 }
             }
             fence_proxy_async();
             tc_fence_before();
             mbar_arrive(p_ready);
+            fetch(i + 1);
             // ---- <h, g'> (this thread's 32 elements)
             float hg = 0.f;
             wait(g_full, i & 1);
@@ -514,8 +538,8 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
             }
             mbar_arrive(hg_read);
             hg = warp_sum(hg);
-            if (lane == 0) vec.red[0][warp] = hg;
-            // ---- dx, in the scaled dY's place
+            if (lane == 0) sums.hg[warp] = hg;
+            // ---- dx, in dY's place
             wait(cd_full, i & 1);
             wait(dx_full, i & 1);
             tc_fence_after();
@@ -525,7 +549,7 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                 tmem_ld32_nowait(tmem + lanes + kColR + 64 + 32 * half, br);
                 uint4 yr[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) yr[j] = ld_shared_v4(sb + kY + piece(row, half * 4 + j));
+                for (int j = 0; j < 4; ++j) yr[j] = ld_shared_v4(yb + piece(row, half * 4 + j));
                 tmem_landed(ar);
                 tmem_landed(br);
                 F2 s2 = f2(0.f, 0.f);
@@ -542,72 +566,17 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                         o[k] = pack_bf16(fma2(de, fma2(tt, bb, f2(ar[c], ar[c + 1])), mul2(dd, f2(bf_lo(y[k]), bf_hi(y[k])))));
                     }
                     if (full_chunk)
-                        st_shared_v4(sb + kSy + piece(row, half * 4 + j), o[0], o[1], o[2], o[3]);
+                        st_shared_v4(yb + piece(row, half * 4 + j), o[0], o[1], o[2], o[3]);
                     else if (live)
                         *reinterpret_cast<uint4 *>(q.dx + ((size_t)(t0 + row) * p.H + h) * p.P + p.col0(u) + half * 32 + 8 * j) =
                             make_uint4(o[0], o[1], o[2], o[3]);
                 }
                 const float2 s = get(s2);
-                vec.bt[half][row] = live ? tail * (s.x + s.y) : 0.f;
+                sums.bt[half][row] = live ? tail * (s.x + s.y) : 0.f;
             }
             fence_proxy_async();
             tc_fence_before();
-            mbar_arrive(dx_done);
-            named_sync<kRowThreads>(1);  // every row's and column's sums are written
-            if (half == 0) {
-                // strictly lower W: sums of this token's row left of its block, of its column below it, and
-                // of both inside it
-                float roff = 0.f, coff = 0.f;
-                for (int k = 0; k < wr; ++k) roff += vec.rsum[0][k][row] + vec.rsum[1][k][row];
-                for (int k = wr + 1; k < 4; ++k) coff += vec.csum[k][row];
-                const float rd = vec.rsum[0][wr][row] + vec.rsum[1][wr][row], cd = vec.csum[wr][row];
-                const float rw = vec.rowi[0][row] + vec.rowi[1][row];
-                const float bt = vec.bt[0][row] + vec.bt[1][row];
-                float suf = rw + roff + rd - delta * cd, pre = delta * (bt + coff);
-                const float pre_own = pre;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const float a = __shfl_down_sync(0xffffffffu, suf, o), b = __shfl_up_sync(0xffffffffu, pre, o);
-                    if (lane + o < 32) suf += a;
-                    if (lane >= o) pre += b;
-                }
-                const float t_ri = warp_sum(rw), t_bt = warp_sum(delta * bt);
-                const float r0 = warp_sum(wr > 0 ? vec.rsum[0][0][row] + vec.rsum[1][0][row] : 0.f);
-                const float r1 = warp_sum(wr > 1 ? vec.rsum[0][1][row] + vec.rsum[1][1][row] : 0.f);
-                if (lane == 0) vec.tot[wr][0] = t_ri, vec.tot[wr][1] = t_bt, vec.tot[wr][2] = r0, vec.tot[wr][3] = r1;
-                named_sync<128>(2);
-                float dg = suf + (pre - pre_own);
-                for (int k = 0; k < 4; ++k) {
-                    if (k > wr) dg += vec.tot[k][0];
-                    if (k < wr) dg += vec.tot[k][1];
-                }
-                // pairs of blocks around this one: rows below, columns left
-                if (wr == 1) dg += vec.tot[2][2] + vec.tot[3][2];
-                if (wr == 2) dg += vec.tot[3][2] + vec.tot[3][3];
-                float e = 0.f;
-                for (int k = 0; k < 8; ++k) e += vec.red[0][k];
-                dgam += dg + decay * e;
-                wsum += cd + coff + vec.wdiag[row] + bt;
-            }
-            if ((i & (p.S - 1)) == p.S - 1) {  // the head's last slice
-                float ddt = 0.f;
-                if (half == 0 && live) {
-                    ddt = fmaf(p.A[h], dgam, wsum);
-                    if (p.softplus) ddt /= 1.f + expf(-p.raw_dt(t0 + row, h));
-                    const size_t at = (size_t)(t0 + row) * p.H + h;
-                    if (p.dt_f32) ((float *)q.ddt)[at] = ddt;
-                    else ((__nv_bfloat16 *)q.ddt)[at] = __float2bfloat16_rn(ddt);
-                }
-                const float a = warp_sum(half == 0 && live ? delta * dgam : 0.f), b = warp_sum(ddt), d = warp_sum(dD);
-                named_sync<kRowThreads>(1);  // red is read
-                if (lane == 0) vec.red[0][warp] = a, vec.red[1][warp] = b, vec.red[2][warp] = d;
-                named_sync<kRowThreads>(1);
-                if (tid < 3) {
-                    float v = 0.f;
-                    for (int k = 0; k < 8; ++k) v += vec.red[tid][k];
-                    q.part[((size_t)blockIdx.x * 3 + tid) * p.H + h] = v;
-                }
-            }
+            mbar_arrive(&dx_done[i & 1]);
         }
         // ---- the summed masked Q, in P's place (its last product has completed: dx_full)
 #pragma unroll
@@ -661,6 +630,81 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
     }
 }
 
+// The gates' gradients of one chunk and head, a thread per token: dgam from the sums of crossing
+// pairs, ddt, and the chunk's parts [slots, 3, H] of dA, ddt_bias and dD.
+__global__ void __launch_bounds__(kC) scan_gate_grad_kernel(const Params p, const Sums *__restrict__ sums, void *ddt_out, float *__restrict__ part) {
+    const int row = threadIdx.x, wr = row >> 5, lane = row & 31, h = blockIdx.y;
+    __shared__ float tot[4][4];  // per row block: sums of rowi, delta bt, row sums left: of block 0, of block 1
+    __shared__ float red[3][4];
+    float *out = part + (size_t)blockIdx.x * 3 * p.H + h;
+    int n, local;
+    if (!p.m.slot(blockIdx.x, kC, &n, &local)) {  // an unused slot adds nothing
+        if (row < 3) out[row * p.H] = 0.f;
+        return;
+    }
+    const int t0 = p.m.begin(n) + local * kC;
+    const bool live = t0 + row < p.m.end(n);
+    const float delta = p.gates.at(blockIdx.x, p.H, h)[row];
+    float before, after, all;
+    around(p.gates.totals(blockIdx.x, p.H, h), wr, &before, &after, &all);
+    // strictly lower W: sums of this token's row left of its block, of its column below it, and of both
+    // inside it
+    float rs[4] = {}, coff = 0.f, cd = 0.f, rw = 0.f, bt = 0.f, wd = 0.f, dD = 0.f, hg = 0.f;
+    for (int k = 0; k < p.S; ++k) {
+        const Sums &s = sums[((size_t)blockIdx.x * p.H + h) * p.S + k];
+        rw += s.rowi[0][row] + s.rowi[1][row];
+        bt += s.bt[0][row] + s.bt[1][row];
+        dD += s.dD[0][row] + s.dD[1][row];
+        wd += s.wdiag[row];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            if (w <= wr) rs[w] += s.rsum[w][0][row] + s.rsum[w][1][row];
+            if (w == wr) cd += s.csum[w][row];
+            if (w > wr) coff += s.csum[w][row];
+        }
+        if (lane < 8) hg += s.hg[lane];
+    }
+    float roff = 0.f, rd = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        if (w < wr) roff += rs[w];
+        if (w == wr) rd = rs[w];
+    }
+    hg = warp_sum(hg);
+    float suf = rw + roff + rd - delta * cd, pre = delta * (bt + coff);
+    const float pre_own = pre;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float a = __shfl_down_sync(0xffffffffu, suf, o), b = __shfl_up_sync(0xffffffffu, pre, o);
+        if (lane + o < 32) suf += a;
+        if (lane >= o) pre += b;
+    }
+    const float t_ri = warp_sum(rw), t_bt = warp_sum(delta * bt), r0 = warp_sum(wr > 0 ? rs[0] : 0.f), r1 = warp_sum(wr > 1 ? rs[1] : 0.f);
+    if (lane == 0) tot[wr][0] = t_ri, tot[wr][1] = t_bt, tot[wr][2] = r0, tot[wr][3] = r1;
+    __syncthreads();
+    float dgam = suf + (pre - pre_own);
+    for (int k = 0; k < 4; ++k) {
+        if (k > wr) dgam += tot[k][0];
+        if (k < wr) dgam += tot[k][1];
+    }
+    // pairs of blocks around this one: rows below, columns left
+    if (wr == 1) dgam += tot[2][2] + tot[3][2];
+    if (wr == 2) dgam += tot[3][2] + tot[3][3];
+    dgam += ex2(all) * hg;
+    float ddt = 0.f;
+    if (live) {
+        ddt = fmaf(p.A[h], dgam, cd + coff + wd + bt);
+        if (p.softplus) ddt /= 1.f + expf(-p.raw_dt(t0 + row, h));
+        const size_t at = (size_t)(t0 + row) * p.H + h;
+        if (p.dt_f32) ((float *)ddt_out)[at] = ddt;
+        else ((__nv_bfloat16 *)ddt_out)[at] = __float2bfloat16_rn(ddt);
+    }
+    const float a = warp_sum(live ? delta * dgam : 0.f), b = warp_sum(ddt), d = warp_sum(dD);
+    if (lane == 0) red[0][wr] = a, red[1][wr] = b, red[2][wr] = d;
+    __syncthreads();
+    if (row < 3) out[row * p.H] = (red[row][0] + red[row][1]) + (red[row][2] + red[row][3]);
+}
+
 // dC, dB from the runs' fp32 parts, in a fixed order; 4 elements per thread.
 __global__ void __launch_bounds__(256) scan_join_kernel(const float *__restrict__ part, int runs, long long n, __nv_bfloat16 *dC, __nv_bfloat16 *dB) {
     const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
@@ -693,6 +737,8 @@ int runs_of(const ScanArgs &a) {
     return (U + r - 1) / r;
 }
 
+size_t sums_bytes(const ScanArgs &a) { return align_up((size_t)a.seq.slots(kC) * a.H * (a.P / kPT) * sizeof(Sums)); }
+
 template <int K>
 cudaError_t run(const ScanArgs &a, const Gates &gates, const Tiles &h, const Tiles &gr, char *ws) {
     GradP q{};
@@ -700,10 +746,10 @@ cudaError_t run(const ScanArgs &a, const Gates &gates, const Tiles &h, const Til
     q.run = units_per_cta(a), q.runs = runs_of(a);
     q.h_hi = h.hi, q.h_lo = h.lo, q.g_hi = gr.hi, q.g_lo = gr.lo;
     q.dx = (__nv_bfloat16 *)a.dx, q.dB = (__nv_bfloat16 *)a.dB, q.dC = (__nv_bfloat16 *)a.dC;
-    q.ddt = a.ddt;
     const int slots = a.seq.total ? a.seq.slots(kC) : 0;
-    q.part = (float *)ws;
-    q.part_bc = (float *)(ws + align_up((size_t)slots * 3 * a.H * 4));
+    float *part = (float *)ws;
+    q.sums = (Sums *)(ws + align_up((size_t)slots * 3 * a.H * 4));
+    q.part_bc = (float *)((char *)q.sums + sums_bytes(a));
     if (slots) {
         CUtensorMap mb, mc, mx, my, mdx;
         const long long dense = (long long)a.H * a.P;
@@ -718,6 +764,10 @@ cudaError_t run(const ScanArgs &a, const Gates &gates, const Tiles &h, const Til
             TimedLaunch t("scan_grad", a.stream);
             kernel<<<dim3(slots, a.G * q.runs), kThreads, kSmem, a.stream>>>(mb, mc, mx, my, mdx, q);
         }
+        {
+            TimedLaunch t("scan_gate_grad", a.stream);
+            scan_gate_grad_kernel<<<dim3(slots, a.H), kC, 0, a.stream>>>(q.p, q.sums, a.ddt, part);
+        }
         if (q.runs > 1) {
             TimedLaunch t("scan_join", a.stream);
             const long long n = (long long)a.seq.total * a.G * K;
@@ -725,7 +775,7 @@ cudaError_t run(const ScanArgs &a, const Gates &gates, const Tiles &h, const Til
         }
     }
     TimedLaunch t("scan_sum", a.stream);
-    return launch_scan_sum(q.part, slots, a);
+    return launch_scan_sum(part, slots, a);
 }
 
 }  // namespace
@@ -733,7 +783,7 @@ cudaError_t run(const ScanArgs &a, const Gates &gates, const Tiles &h, const Til
 size_t grad_bytes(const ScanArgs &a) {
     if (!a.seq.total) return 256;
     const int runs = runs_of(a);
-    return align_up((size_t)a.seq.slots(kC) * 3 * a.H * 4) + (runs > 1 ? align_up(2ull * runs * a.seq.total * a.G * a.K * 4) : 0);
+    return align_up((size_t)a.seq.slots(kC) * 3 * a.H * 4) + sums_bytes(a) + (runs > 1 ? align_up(2ull * runs * a.seq.total * a.G * a.K * 4) : 0);
 }
 
 cudaError_t launch_grad(const ScanArgs &a, const Gates &gates, const Tiles &h, const Tiles &g, char *ws) {
