@@ -40,6 +40,7 @@ constexpr int kCt = 0, kP = 32768, kX = 98304, kHt = 147456, kHs = 180224;
 struct Vec {
     float col[4][kC];  // [w][s]: e^{(start of row block w) - gam_s} delta_s left of block w, delta_s in it
     float gl[kC];      // log2 decay from the block's start
+    float row[4][kC];  // e^{gam_r}, then (LOCAL) also times f; e^{from the row block's start}; D
 };
 constexpr int kVec = 212992;
 constexpr int kBarsAt = kVec + 2 * sizeof(Vec);
@@ -190,6 +191,7 @@ scan_out_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant_
             const float *gt = p.gates.at(blockIdx.x, p.H, h);
             const float4 tot = p.gates.totals(blockIdx.x, p.H, h);
             const float t[4] = {tot.x, tot.y, tot.z, tot.w};
+            const float D = p.D ? p.D[h] : 0.f, f = LOCAL ? q.locals.before[(size_t)blockIdx.x * p.H + h] : 0.f;
             float gd[2], gf[2], gr[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -205,6 +207,12 @@ scan_out_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant_
                 const int wr = w2 * 2 + k, row = wr * 32 + lane;
                 vec.gl[row] = gf[k];
                 vec.col[wr][row] = gd[k];
+                float before, after, all;
+                around(tot, wr, &before, &after, &all);
+                vec.row[0][row] = ex2(before + gf[k]);
+                if (LOCAL) vec.row[1][row] = ex2(f + before + gf[k]);
+                vec.row[2][row] = ex2(gf[k]);
+                vec.row[3][row] = D;
                 float to = gr[k];
 #pragma unroll
                 for (int w = 1; w < 4; ++w)
@@ -222,31 +230,17 @@ scan_out_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant_
         const int wr = warp & 3, qd = warp >> 2, row = wr * 32 + lane;  // row block, column quarter
         const bool live = row < len;
         const uint32_t lanes = (uint32_t)(wr * 32) << 16;
-        float g_f, g_d, g_s = 0.f;
-        float4 g_tot;
         bool ok = true;
-        auto fetch = [&](int i) {
-            const int h = p.head(g, u_first + i);
-            g_f = p.gates.at(blockIdx.x, p.H, h)[kC + row];
-            g_tot = p.gates.totals(blockIdx.x, p.H, h);
-            g_d = p.D ? p.D[h] : 0.f;
-            if (LOCAL) g_s = q.locals.before[(size_t)blockIdx.x * p.H + h];
-        };
-        fetch(0);
         float e_next = 0.f, d_next = 0.f, s_next = 0.f;  // e^{gam_r}, D and e^{gam_r} f of the head masked last
         // unit i's P (where it begins a head), and leave for its product
         auto mask = [&](int i) {
             if ((i & (p.S - 1)) == 0) {
                 const int hb = (i >> p.sh) & 1;
                 Vec &vec = reinterpret_cast<Vec *>(smem + kVec)[hb];
-                float before, after, all;
-                around(g_tot, wr, &before, &after, &all);
-                e_next = ex2(before + g_f);
-                d_next = g_d;
-                if (LOCAL) s_next = ex2(g_s + before + g_f);
-                const float me = g_f;
-                if (i + p.S < units) fetch(i + p.S);
                 ok = __all_sync(0xffffffffu, ok && wait_bar(&v_full[hb], (i >> p.sh >> 1) & 1, abort_flag));
+                e_next = vec.row[0][row], d_next = vec.row[3][row];
+                if (LOCAL) s_next = vec.row[1][row];
+                const float me = vec.gl[row], u_r = vec.row[2][row];
                 const uint32_t at = sb + kP + hb * 32768;
                 // this warp's columns: 8 qd .. of every block of 32, so that a row block's warps share its
                 // diagonal block
@@ -255,7 +249,6 @@ scan_out_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant_
                 for (int k = 0; k < 4; ++k)
                     if (k <= wr && ok) tmem_ld8_nowait(tmem + lanes + kColS + 32 * k + 8 * qd, v[k]);
                 tmem_landed(v);
-                const float u_r = ex2(me);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const uint32_t to = at + (k >> 1) * 16384 + piece(row, (k & 1) * 4 + qd);
