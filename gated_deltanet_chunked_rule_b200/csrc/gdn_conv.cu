@@ -7,14 +7,22 @@
 //   dpre_t = dy_t (dy/dpre),   dx_t = sum_j weight_j dpre_{t+W-1-j},
 //   dweight_j = sum_t dpre_t x_{t-W+1+j},          dbias = sum_t dpre_t
 //
-// Memory-bound: forward reads x and writes y, backward reads x and dy and writes dx. A
-// warp owns 32 x 16 bytes of channels and a run of tokens; the last W-1 inputs stay in
-// registers, so that every row is read once per run (plus W-1 rows of overlap). Rows come in
-// batches of eight (four in the backward, with dy's) that are loaded together and worked off
-// channel by channel without a branch while they lie in one sequence; a batch that meets a
-// border goes row by row. The backward recomputes pre, and holds dpre of the last W-1 tokens. The weight's gradient sums in fp32: over a run in
-// registers, over a block's runs in shared memory, over blocks by a second kernel in a
-// fixed order.
+// A warp owns 32 x 16 bytes of channels (8 in the backward) and a run of tokens; the last W-1
+// inputs stay in registers, so that every row is read once per run (plus W-1 rows of overlap).
+// Rows come in batches of eight (four in the backward, with dy's) that are loaded together and
+// worked off, two channels per instruction, without a branch while they lie in one sequence; a
+// batch that meets a border goes row by row. The backward recomputes pre, and holds dpre of the
+// last W-1 tokens. The weight's gradient sums in fp32: over a run in registers, over a block's
+// runs in shared memory, over blocks by a second kernel in a fixed order. The runs are as long as
+// lets every block be resident at once.
+//
+// The bytes: forward reads x and writes y, backward reads x and dy and writes dx. What bounds it
+// is the work on them, 17 and 30 instructions per element, with 16 warps on an SM: 8192 tokens of
+// 8192 channels forward 60 us (42 by the copy rate), of 4352 channels backward 68 us (33). One
+// channel per instruction and runs of 32 tokens: backward 89 us. Tried and slower: the next batch
+// loaded ahead (81 us), two channels per thread and twice the warps (88 us).
+#include <algorithm>
+
 #include "gdn_host.cuh"
 #include "gdn_layer.cuh"
 
@@ -22,14 +30,14 @@ namespace gdn {
 namespace {
 
 constexpr int kWarps = 4;   // runs per block
-constexpr int kRunF = 32;   // tokens of a forward run
-constexpr int kRunB = 32;   // tokens of a backward run
+constexpr int kResident = 4;  // blocks of an SM
+constexpr int kMinRun = 8;  // tokens
 constexpr int kAhead = 8;   // rows loaded together
 constexpr int kAheadB = 4;  // (each of x and dy) in the backward
 
 struct ConvP {
     SeqMap m;
-    int C, runs;
+    int C, run, runs;  // tokens of a run
     bool silu;
     long long xs;
 };
@@ -39,6 +47,7 @@ struct ConvP {
 template <typename T, int VEC>
 struct Pack {
     static constexpr int kWords = VEC == 1 ? 1 : VEC * (int)sizeof(T) / 4, kPer = VEC / kWords;
+    static constexpr int kPairs = VEC == 1 ? 1 : VEC / 2;  // of channels, worked on together (one channel: beside a zero)
     uint32_t w[kWords];
     __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -64,12 +73,20 @@ struct Pack {
         if constexpr (kPer == 1) return __uint_as_float(w[k]);
         return __uint_as_float(e ? w[k] & 0xffff0000u : w[k] << 16);
     }
-    __device__ __forceinline__ void put(int k, const float (&v)[kPer]) {
-        if constexpr (kPer == 1) {
-            w[k] = __float_as_uint(v[0]);
+    __device__ __forceinline__ F2 pair(int m) const {
+        if constexpr (VEC == 1) return f2(w[0], 0u);
+        else if constexpr (kPer == 1) return f2(w[2 * m], w[2 * m + 1]);
+        else return f2(w[m] << 16, w[m] & 0xffff0000u);
+    }
+    __device__ __forceinline__ void put(int m, F2 v) {
+        const float2 a = gdn::get(v);
+        if constexpr (VEC == 1) {
+            w[0] = __float_as_uint(a.x);
+        } else if constexpr (kPer == 1) {
+            w[2 * m] = __float_as_uint(a.x), w[2 * m + 1] = __float_as_uint(a.y);
         } else {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v[0], v[1]);
-            w[k] = *reinterpret_cast<const uint32_t *>(&h);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(a.x, a.y);
+            w[m] = *reinterpret_cast<const uint32_t *>(&h);
         }
     }
 };
@@ -90,6 +107,10 @@ struct Taps {
         const int i = (k * P::kPer + e) * W + j;
         return w[i / VEC].get(i % VEC / P::kPer, i % P::kPer);
     }
+    __device__ __forceinline__ F2 pair(int m, int j) const {
+        if constexpr (VEC == 1) return f2(tap(0, 0, j), 0.f);
+        else return f2(tap(2 * m / P::kPer, 0, j), tap((2 * m + 1) / P::kPer, 1 % P::kPer, j));
+    }
 };
 
 // Input row i of sequence n counted from its first state row: the state's rows, then x.
@@ -108,33 +129,29 @@ __device__ __forceinline__ void forward_rows(const Taps<T, VEC, W> &t, bool silu
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) next[i] = U + i >= W - 1 ? r[U + i - (W - 1) < 0 ? 0 : U + i - (W - 1)] : hist[U + i < W - 1 ? U + i : 0];
 #pragma unroll
-    for (int k = 0; k < P::kWords; ++k) {
-        float out[U][P::kPer];
+    for (int m = 0; m < P::kPairs; ++m) {
+        F2 x[W - 1 + U], w[W];
 #pragma unroll
-        for (int e = 0; e < P::kPer; ++e) {
-            float x[W - 1 + U];
+        for (int i = 0; i < W - 1; ++i) x[i] = hist[i].pair(m);
 #pragma unroll
-            for (int i = 0; i < W - 1; ++i) x[i] = hist[i].get(k, e);
+        for (int u = 0; u < U; ++u) x[W - 1 + u] = r[u].pair(m);
 #pragma unroll
-            for (int u = 0; u < U; ++u) x[W - 1 + u] = r[u].get(k, e);
-            const float b = t.b.get(k, e);
+        for (int j = 0; j < W; ++j) w[j] = t.pair(m, j);
+        const F2 b = t.b.pair(m);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float a = b;
+        for (int u = 0; u < U; ++u) {
+            F2 a = b;
 #pragma unroll
-                for (int j = 0; j < W; ++j) a = fmaf(t.tap(k, e, j), x[u + j], a);
-                out[u][e] = silu ? a * sigmoid<sizeof(T) == 2>(a) : a;
-            }
+            for (int j = 0; j < W; ++j) a = fma2(w[j], x[u + j], a);
+            r[u].put(m, silu ? mul2(a, sigmoid<sizeof(T) == 2>(a)) : a);
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u) r[u].put(k, out[u]);
     }
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) hist[i] = next[i];
 }
 
 template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(32 * kWarps, 4)
+__global__ void __launch_bounds__(32 * kWarps, kResident)
 conv_fwd_kernel(ConvP p, const T *__restrict__ x, const T *__restrict__ weight, const T *__restrict__ bias,
                 const T *__restrict__ state, T *__restrict__ y, T *__restrict__ final_state, unsigned *status) {
     using P = Pack<T, VEC>;
@@ -155,7 +172,7 @@ conv_fwd_kernel(ConvP p, const T *__restrict__ x, const T *__restrict__ weight, 
         }
         return;
     }
-    const int t0 = run * kRunF, t1 = min(t0 + kRunF, p.m.total);
+    const int t0 = run * p.run, t1 = min((long long)t0 + p.run, (long long)p.m.total);
     int n = p.m.owner(t0), s = p.m.begin(n), e = p.m.end(n);
     P hist[W - 1];
 #pragma unroll
@@ -192,58 +209,56 @@ conv_fwd_kernel(ConvP p, const T *__restrict__ x, const T *__restrict__ weight, 
 // dpre of the W-1 tokens before.
 template <typename T, int VEC, int W, int U, bool ACC>
 __device__ __forceinline__ void backward_rows(const Taps<T, VEC, W> &t, bool silu, Pack<T, VEC> (&r)[U], const Pack<T, VEC> (&dy)[U],
-                                              const Pack<T, VEC> &add, Pack<T, VEC> (&hist)[W - 1], float (&dh)[W - 1][VEC],
-                                              float (&dw)[W][VEC], float (&db)[VEC]) {
+                                              const Pack<T, VEC> &add, Pack<T, VEC> (&hist)[W - 1],
+                                              F2 (&dh)[W - 1][Pack<T, VEC>::kPairs], F2 (&dw)[W][Pack<T, VEC>::kPairs],
+                                              F2 (&db)[Pack<T, VEC>::kPairs]) {
     using P = Pack<T, VEC>;
     P next[W - 1];
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) next[i] = U + i >= W - 1 ? r[U + i - (W - 1) < 0 ? 0 : U + i - (W - 1)] : hist[U + i < W - 1 ? U + i : 0];
+    const F2 one = f2(1.f, 1.f), minus = f2(-1.f, -1.f);
 #pragma unroll
-    for (int k = 0; k < P::kWords; ++k) {
-        float out[U][P::kPer];
+    for (int m = 0; m < P::kPairs; ++m) {
+        F2 x[W - 1 + U], d[W - 1 + U], w[W];
 #pragma unroll
-        for (int e = 0; e < P::kPer; ++e) {
-            const int q = k * P::kPer + e;
-            float x[W - 1 + U], d[W - 1 + U];
+        for (int i = 0; i < W - 1; ++i) x[i] = hist[i].pair(m), d[i] = dh[i][m];
 #pragma unroll
-            for (int i = 0; i < W - 1; ++i) x[i] = hist[i].get(k, e), d[i] = dh[i][q];
+        for (int j = 0; j < W; ++j) w[j] = t.pair(m, j);
+        const F2 b = t.b.pair(m);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                x[W - 1 + u] = r[u].get(k, e);
-                float g = dy[u].get(k, e);
-                if (silu) {
-                    float a = t.b.get(k, e);
+        for (int u = 0; u < U; ++u) {
+            x[W - 1 + u] = r[u].pair(m);
+            F2 g = dy[u].pair(m);
+            if (silu) {
+                F2 a = b;
 #pragma unroll
-                    for (int j = 0; j < W; ++j) a = fmaf(t.tap(k, e, j), x[u + j], a);
-                    const float s = sigmoid<sizeof(T) == 2>(a);
-                    g *= fmaf(a, s - s * s, s);
-                }
-                d[W - 1 + u] = g;
-                if (ACC) {
-                    db[q] += g;
-#pragma unroll
-                    for (int j = 0; j < W; ++j) dw[j][q] = fmaf(g, x[u + j], dw[j][q]);
-                }
+                for (int j = 0; j < W; ++j) a = fma2(w[j], x[u + j], a);
+                const F2 s = sigmoid<sizeof(T) == 2>(a);
+                g = mul2(g, fma2(mul2(a, s), fma2(s, minus, one), s));
             }
+            d[W - 1 + u] = g;
+            if (ACC) {
+                db[m] = add2(db[m], g);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float a = U == 1 ? add.get(k, e) : 0.f;
-#pragma unroll
-                for (int j = 0; j < W; ++j) a = fmaf(t.tap(k, e, j), d[u + W - 1 - j], a);
-                out[u][e] = a;
+                for (int j = 0; j < W; ++j) dw[j][m] = fma2(g, x[u + j], dw[j][m]);
             }
-#pragma unroll
-            for (int i = 0; i < W - 1; ++i) dh[i][q] = d[U + i];
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) r[u].put(k, out[u]);
+        for (int u = 0; u < U; ++u) {
+            F2 a = U == 1 ? add.pair(m) : f2(0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < W; ++j) a = fma2(w[j], d[u + W - 1 - j], a);
+            r[u].put(m, a);
+        }
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) dh[i][m] = d[U + i];
     }
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) hist[i] = next[i];
 }
 
 template <typename T, int VEC, int W, int UB>
-__global__ void __launch_bounds__(32 * kWarps, VEC == 8 ? 3 : VEC * sizeof(T) == 16 ? 4 : 5)
+__global__ void __launch_bounds__(32 * kWarps, kResident)
 conv_bwd_kernel(ConvP p, const T *__restrict__ x, const T *__restrict__ weight, const T *__restrict__ bias,
                 const T *__restrict__ state, const T *__restrict__ dy, const T *__restrict__ dfinal, T *__restrict__ dx,
                 float *__restrict__ part, unsigned *status) {
@@ -254,15 +269,15 @@ conv_bwd_kernel(ConvP p, const T *__restrict__ x, const T *__restrict__ weight, 
     if (blockIdx.x == 0 && blockIdx.y == 0) check_cu(p.m, status, threadIdx.x, blockDim.x);
     const int c = (blockIdx.y * 32 + lane) * VEC;
     const int run = blockIdx.x * kWarps + warp;
-    const int t0 = run * kRunB, t1 = min(t0 + kRunB, p.m.total);
-    float dw[W][VEC], db[VEC], dh[W - 1][VEC];
+    const int t0 = run < p.runs ? run * p.run : 0, t1 = run < p.runs ? min((long long)t0 + p.run, (long long)p.m.total) : 0;
+    F2 dw[W][P::kPairs], db[P::kPairs], dh[W - 1][P::kPairs];
 #pragma unroll
-    for (int q = 0; q < VEC; ++q) {
-        db[q] = 0.f;
+    for (int m = 0; m < P::kPairs; ++m) {
+        db[m] = f2(0.f, 0.f);
 #pragma unroll
-        for (int j = 0; j < W; ++j) dw[j][q] = 0.f;
+        for (int j = 0; j < W; ++j) dw[j][m] = f2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < W - 1; ++i) dh[i][q] = 0.f;
+        for (int i = 0; i < W - 1; ++i) dh[i][m] = f2(0.f, 0.f);
     }
     if (c < p.C && t0 < t1) {
         int n = p.m.owner(t0), s = p.m.begin(n), e = p.m.end(n);
@@ -288,7 +303,7 @@ conv_bwd_kernel(ConvP p, const T *__restrict__ x, const T *__restrict__ weight, 
 #pragma unroll
             for (int i = 0; i < W - 1; ++i) {
                 none[0].zero(), zero[0].zero();
-                float keep[W][VEC], kb[VEC];
+                F2 keep[W][P::kPairs], kb[P::kPairs];
                 backward_rows<T, VEC, W, 1, false>(taps, false, none, zero, final_part(t - (W - 1) + i), hist, dh, keep, kb);
                 emit(t - (W - 1) + i, none[0]);
             }
@@ -307,7 +322,7 @@ conv_bwd_kernel(ConvP p, const T *__restrict__ x, const T *__restrict__ weight, 
                 if (t < t1) {
                     backward_rows<T, VEC, W, U, true>(taps, p.silu, r, d, r[0], hist, dh, dw, db);
                 } else {
-                    float keep[W][VEC], kb[VEC];
+                    F2 keep[W][P::kPairs], kb[P::kPairs];
                     backward_rows<T, VEC, W, U, false>(taps, p.silu, r, d, r[0], hist, dh, keep, kb);
                 }
 #pragma unroll
@@ -335,7 +350,7 @@ conv_bwd_kernel(ConvP p, const T *__restrict__ x, const T *__restrict__ weight, 
             if (t < t1) {
                 backward_rows<T, VEC, W, 1, true>(taps, p.silu, r, d, final_part(t - (W - 1)), hist, dh, dw, db);
             } else {
-                float keep[W][VEC], kb[VEC];
+                F2 keep[W][P::kPairs], kb[P::kPairs];
                 backward_rows<T, VEC, W, 1, false>(taps, p.silu, r, d, final_part(t - (W - 1)), hist, dh, keep, kb);
             }
             emit(t - (W - 1), r[0]);
@@ -344,10 +359,13 @@ conv_bwd_kernel(ConvP p, const T *__restrict__ x, const T *__restrict__ weight, 
         if (!done) flush(t);
     }
 #pragma unroll
-    for (int q = 0; q < VEC; ++q) {
+    for (int m = 0; m < P::kPairs; ++m) {
 #pragma unroll
-        for (int j = 0; j < W; ++j) red[warp][j * VEC + q][lane] = dw[j][q];
-        red[warp][W * VEC + q][lane] = db[q];
+        for (int j = 0; j <= W; ++j) {
+            const float2 v = get(j < W ? dw[j < W ? j : 0][m] : db[m]);
+            red[warp][j * VEC + 2 * m][lane] = v.x;
+            if (VEC > 1) red[warp][j * VEC + 2 * m + 1][lane] = v.y;
+        }
     }
     __syncthreads();
     for (int i = threadIdx.x; i < (W + 1) * VEC * 32; i += blockDim.x) {
@@ -443,22 +461,30 @@ conv_update_kernel(ConvP p, const T *__restrict__ x, const T *__restrict__ weigh
     for (int i = 0; i < W - 1; ++i) hist[i].store(st + (size_t)i * p.C);
 }
 
+// Blocks along the tokens (without the final states'): as many as run beside each other, with
+// runs of one length, or one wave more would stand half empty.
+int token_blocks(int total, unsigned column_blocks) {
+    return std::max(1, std::min((total + kMinRun * kWarps - 1) / (kMinRun * kWarps), (int)(kResident * sm_count() / column_blocks)));
+}
+
 enum Pass { kFwd, kBwd, kUpdate };
 
 template <typename T, int VEC, int W>
 cudaError_t run_pass(const ConvArgs &a, Pass pass) {
-    ConvP p{a.seq, a.C, 0, a.silu, a.x_stride};
+    ConvP p{a.seq, a.C, 0, 0, a.silu, a.x_stride};
     const T *x = (const T *)a.x, *w = (const T *)a.weight, *b = (const T *)a.bias, *st = (const T *)a.state;
     const unsigned cb = (unsigned)((a.C + 32 * VEC - 1) / (32 * VEC));
+    const int share = token_blocks(a.seq.total, cb) * kWarps;
+    p.run = std::max(kMinRun, ((a.seq.total + share - 1) / share + 7) / 8 * 8);
+    p.runs = (a.seq.total + p.run - 1) / p.run;
     if (pass == kFwd) {
-        p.runs = (a.seq.total + kRunF - 1) / kRunF;
         const long long runs = (long long)p.runs + (a.final_state ? a.seq.N : 0);
         if (runs == 0) return cudaSuccess;
         conv_fwd_kernel<T, VEC, W><<<dim3((unsigned)((runs + kWarps - 1) / kWarps), cb), 32 * kWarps, 0, a.stream>>>(
             p, x, w, b, st, (T *)a.y, (T *)a.final_state, a.status);
     } else if (pass == kBwd) {
         const T *dy = (const T *)a.dy, *df = (const T *)a.dfinal;
-        const int blocks = (a.seq.total + kRunB * kWarps - 1) / (kRunB * kWarps);
+        const int blocks = (p.runs + kWarps - 1) / kWarps;
         if (blocks) {
             TimedLaunch tl("conv_bwd", a.stream);
             conv_bwd_kernel<T, VEC, W, kAheadB><<<dim3(blocks, cb), 32 * kWarps, 0, a.stream>>>(p, x, w, b, st, dy, df, (T *)a.dx, a.part,
@@ -502,7 +528,7 @@ cudaError_t dispatch(const ConvArgs &a, Pass pass) {
 }  // namespace
 
 size_t conv_part_bytes(int total, int C, int W) {
-    const size_t blocks = ((size_t)total + kRunB * kWarps - 1) / (kRunB * kWarps);
+    const size_t blocks = total ? token_blocks(total, (C + 255) / 256) : 0;  // of the widest column blocks: the most
     return blocks * (W + 1) * C * sizeof(float);
 }
 

@@ -70,11 +70,63 @@ __device__ __forceinline__ void check_cu(const SeqMap &m, unsigned *status, int 
     if (bad) set_status(status, GDN_ERR_DEVICE_ARG);
 }
 
+// Two fp32 operations per instruction (sm_100a), on register pairs.
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ F2 f2(uint32_t a, uint32_t b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float2 get(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+
 // kFast: single-instruction exponentials (relative error below 2^-18 for |x| < 16), enough
 // where the results are rounded to bf16; the library's expf otherwise.
 template <bool kFast>
 __device__ __forceinline__ float sigmoid(float x) {
     return kFast ? __fdividef(1.f, 1.f + __expf(-x)) : 1.f / (1.f + expf(-x));
+}
+
+template <bool kFast>
+__device__ __forceinline__ F2 sigmoid(F2 x) {
+    if constexpr (!kFast) {
+        const float2 v = get(x);
+        return f2(sigmoid<false>(v.x), sigmoid<false>(v.y));
+    }
+    const float log2e = 1.4426950408889634f;
+    const float2 t = get(mul2(x, f2(-log2e, -log2e)));
+    float a, b;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(t.y));
+    const float2 d = get(add2(f2(a, b), f2(1.f, 1.f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(d.y));
+    return f2(a, b);
 }
 
 // VEC consecutive elements as fp32, by one 16-byte access (or one element).
