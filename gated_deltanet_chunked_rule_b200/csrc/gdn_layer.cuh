@@ -164,6 +164,17 @@ __device__ __forceinline__ void store_vec(T *p, const float (&v)[VEC]) {
     }
 }
 
+template <typename T, int PAIRS>
+__device__ __forceinline__ void store_pairs(T *p, const F2 (&v)[PAIRS]) {
+    float f[2 * PAIRS];
+#pragma unroll
+    for (int m = 0; m < PAIRS; ++m) {
+        const float2 a = get(v[m]);
+        f[2 * m] = a.x, f[2 * m + 1] = a.y;
+    }
+    store_vec<T, 2 * PAIRS>(p, f);
+}
+
 // --------------------------------------------------------------- convolution
 struct ConvArgs {
     SeqMap seq;

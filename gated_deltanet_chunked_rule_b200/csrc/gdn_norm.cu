@@ -26,10 +26,10 @@ template <typename T, int VEC>
 struct alignas(16) Raw {
     uint4 v;
     __device__ __forceinline__ void load(const T *p) { v = *reinterpret_cast<const uint4 *>(p); }
-    __device__ __forceinline__ float get(int i) const {
+    __device__ __forceinline__ F2 pair(int m) const {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
-        return __uint_as_float((i & 1) ? (w[i >> 1] & 0xffff0000u) : (w[i >> 1] << 16));
+        if constexpr (sizeof(T) == 4) return f2(w[2 * m], w[2 * m + 1]);
+        return f2(w[m] << 16, w[m] & 0xffff0000u);
     }
 };
 
@@ -69,6 +69,27 @@ __device__ __forceinline__ float load_w(const void *w, int wf32, int i) {
     return wf32 ? ((const float *)w)[i] : __bfloat162float(((const __nv_bfloat16 *)w)[i]);
 }
 
+// VEC weights from element i on, which lie in one row of them (zeros behind it).
+template <int VEC>
+__device__ __forceinline__ void load_weights(const void *w, int wf32, int i, bool in, F2 (&v)[VEC / 2]) {
+#pragma unroll
+    for (int m = 0; m < VEC / 2; ++m) v[m] = f2(0.f, 0.f);
+    if (!in || !w) return;
+    if (wf32) {
+#pragma unroll
+        for (int m = 0; m < VEC / 4; ++m) {
+            const float4 a = reinterpret_cast<const float4 *>((const float *)w + i)[m];
+            v[2 * m] = f2(a.x, a.y), v[2 * m + 1] = f2(a.z, a.w);
+        }
+    } else {
+#pragma unroll
+        for (int m = 0; m < VEC / 2; ++m) {
+            const uint32_t a = reinterpret_cast<const uint32_t *>((const __nv_bfloat16 *)w + i)[m];
+            v[m] = f2(a << 16, a & 0xffff0000u);
+        }
+    }
+}
+
 // GATE: 0 none, 1 before the normalisation, 2 after it
 template <typename T, int TPR, int NV, int GATE, bool CENTER>
 __global__ void __launch_bounds__(kThreads)
@@ -78,15 +99,14 @@ norm_fwd_kernel(NormP p, const T *__restrict__ x, const void *__restrict__ weigh
     constexpr bool kFast = sizeof(T) == 2;
     __shared__ float buf[2][1][kThreads / 32];
     const int g = threadIdx.x / TPR, l = threadIdx.x % TPR, nv = p.D / VEC;
-    float w[NV][VEC], b[NV][VEC];
+    constexpr int PAIRS = VEC / 2;
+    F2 w[NV][PAIRS], b[NV][PAIRS];
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const int v = i * TPR + l;
-            w[i][e] = v < nv ? load_w(weight, wf32, v * VEC + e) : 0.f;
-            b[i][e] = v < nv && bias ? load_w(bias, wf32, v * VEC + e) : 0.f;
-        }
+    for (int i = 0; i < NV; ++i) {
+        const int v = i * TPR + l;
+        load_weights<VEC>(weight, wf32, v * VEC, v < nv, w[i]);
+        load_weights<VEC>(bias, wf32, v * VEC, v < nv, b[i]);
+    }
     int phase = 0;
     Raw<T, VEC> q[NV], z[NV];
     auto fetch = [&](long long r) {
@@ -105,38 +125,39 @@ norm_fwd_kernel(NormP p, const T *__restrict__ x, const void *__restrict__ weigh
     for (long long r0 = (long long)blockIdx.x * kGroups; r0 < p.R; r0 += stride) {
         const long long r = r0 + g;
         const bool live = r < p.R;
-        float u[NV][VEC];
+        F2 u[NV][PAIRS], sum = f2(0.f, 0.f), sq = f2(0.f, 0.f);
         Raw<T, VEC> zc[NV];
-        float s[1] = {0.f};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             zc[i] = z[i];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                u[i][e] = q[i].get(e);
+            for (int m = 0; m < PAIRS; ++m) {
+                u[i][m] = q[i].pair(m);
                 if (GATE == 1) {
-                    const float zz = z[i].get(e);
-                    u[i][e] *= zz * sigmoid<kFast>(zz);
+                    const F2 zz = z[i].pair(m);
+                    u[i][m] = mul2(u[i][m], mul2(zz, sigmoid<kFast>(zz)));
                 }
-                s[0] += u[i][e];
+                if (CENTER) sum = add2(sum, u[i][m]);
             }
         }
         fetch(r + stride);
-        float mean = 0.f;
+        float s[1], mean = 0.f;
         if (CENTER) {
+            s[0] = get(sum).x + get(sum).y;
             row_sum<TPR, 1>(s, buf, phase);
             mean = s[0] * p.inv_d;
         }
-        s[0] = 0.f;
+        const F2 minus = f2(-mean, -mean);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const bool in = i * TPR + l < nv;
+            if (i * TPR + l >= nv) continue;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                u[i][e] -= mean;
-                if (in) s[0] = fmaf(u[i][e], u[i][e], s[0]);
+            for (int m = 0; m < PAIRS; ++m) {
+                if (CENTER) u[i][m] = add2(u[i][m], minus);
+                sq = fma2(u[i][m], u[i][m], sq);
             }
         }
+        s[0] = get(sq).x + get(sq).y;
         row_sum<TPR, 1>(s, buf, phase);
         const float rstd = rsqrtf(fmaf(s[0], p.inv_d, p.eps));
         if (!live) continue;
@@ -144,20 +165,21 @@ norm_fwd_kernel(NormP p, const T *__restrict__ x, const void *__restrict__ weigh
             stats[2 * r] = mean;
             stats[2 * r + 1] = rstd;
         }
+        const F2 rs = f2(rstd, rstd);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int v = i * TPR + l;
             if (v >= nv) continue;
-            float o[VEC];
+            F2 o[PAIRS];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                o[e] = fmaf(u[i][e] * rstd, w[i][e], b[i][e]);
+            for (int m = 0; m < PAIRS; ++m) {
+                o[m] = fma2(mul2(u[i][m], rs), w[i][m], b[i][m]);
                 if (GATE == 2) {
-                    const float zz = zc[i].get(e);
-                    o[e] *= zz * sigmoid<kFast>(zz);
+                    const F2 zz = zc[i].pair(m);
+                    o[m] = mul2(o[m], mul2(zz, sigmoid<kFast>(zz)));
                 }
             }
-            store_vec<T, VEC>(y + r * p.D + v * VEC, o);
+            store_pairs<T, PAIRS>(y + r * p.D + v * VEC, o);
         }
     }
 }
@@ -169,19 +191,20 @@ norm_bwd_kernel(NormP p, const T *__restrict__ x, const void *__restrict__ weigh
                 T *__restrict__ dgate, float *__restrict__ part) {
     constexpr int VEC = 16 / sizeof(T), kGroups = kThreads / TPR;
     constexpr bool kFast = sizeof(T) == 2;
-    __shared__ float buf[2][2][kThreads / 32];
+    __shared__ float buf[2][CENTER ? 2 : 1][kThreads / 32];
     __shared__ float sum[kGroups > 1 ? 2 * TPR * NV * VEC : 1];
     const int g = threadIdx.x / TPR, l = threadIdx.x % TPR, nv = p.D / VEC;
-    float w[NV][VEC], b[GATE == 2 ? NV : 1][VEC], dw[NV][VEC], db[NV][VEC];
+    constexpr int PAIRS = VEC / 2;
+    const F2 zero = f2(0.f, 0.f), one = f2(1.f, 1.f), minus = f2(-1.f, -1.f);
+    F2 w[NV][PAIRS], b[GATE == 2 ? NV : 1][PAIRS], dw[NV][PAIRS], db[NV][PAIRS];
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+        const int v = i * TPR + l;
+        load_weights<VEC>(weight, wf32, v * VEC, v < nv, w[i]);
+        if (GATE == 2) load_weights<VEC>(bias, wf32, v * VEC, v < nv, b[GATE == 2 ? i : 0]);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const int v = i * TPR + l;
-            w[i][e] = v < nv ? load_w(weight, wf32, v * VEC + e) : 0.f;
-            if (GATE == 2) b[i][e] = v < nv && bias ? load_w(bias, wf32, v * VEC + e) : 0.f;
-            dw[i][e] = db[i][e] = 0.f;
-        }
+        for (int m = 0; m < PAIRS; ++m) dw[i][m] = db[i][m] = zero;
+    }
     int phase = 0;
     Raw<T, VEC> q[NV], z[NV], d[NV];
     float mean = 0.f, rstd = 0.f;
@@ -207,66 +230,72 @@ norm_bwd_kernel(NormP p, const T *__restrict__ x, const void *__restrict__ weigh
         const long long r = r0 + g;
         const bool live = r < p.R;
         if (!kKeep) fetch(r);
-        const float mu = mean, rs = rstd;
-        float s[2] = {0.f, 0.f};
+        const F2 mu = f2(-mean, -mean), rs = f2(rstd, rstd);
+        F2 s0 = zero, s1 = zero;
         // n; dn; gate first: silu(z), x silu'(z)
-        float kn[kKeep ? NV : 1][VEC], kd[kKeep ? NV : 1][VEC], ka[kKeep && GATE == 1 ? NV : 1][VEC], kb[kKeep && GATE == 1 ? NV : 1][VEC];
+        F2 kn[kKeep ? NV : 1][PAIRS], kd[kKeep ? NV : 1][PAIRS], ka[kKeep && GATE == 1 ? NV : 1][PAIRS], kb[kKeep && GATE == 1 ? NV : 1][PAIRS];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int v = i * TPR + l;
             if (v >= nv) continue;
-            float og[VEC];
+            F2 og[PAIRS];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float xe = q[i].get(e), de = d[i].get(e);
-                float u = xe, dl = de, dsilu = 0.f;
+            for (int m = 0; m < PAIRS; ++m) {
+                const F2 xe = q[i].pair(m), de = d[i].pair(m);
+                F2 u = xe, dl = de, dsilu = zero;
                 if (GATE) {
-                    const float zz = z[i].get(e), sg = sigmoid<kFast>(zz), si = zz * sg;
-                    dsilu = fmaf(si, 1.f - sg, sg);
-                    if (GATE == 1) u *= si;
-                    else dl *= si;
-                    if (kKeep && GATE == 1) ka[i][e] = si, kb[i][e] = xe * dsilu;
+                    const F2 zz = z[i].pair(m), sg = sigmoid<kFast>(zz), si = mul2(zz, sg);
+                    dsilu = fma2(si, fma2(sg, minus, one), sg);
+                    if (GATE == 1) u = mul2(u, si);
+                    else dl = mul2(dl, si);
+                    if (kKeep && GATE == 1) ka[i][m] = si, kb[i][m] = mul2(xe, dsilu);
                 }
-                const float n = (u - mu) * rs, dn = dl * w[i][e];
-                dw[i][e] = fmaf(dl, n, dw[i][e]);
-                db[i][e] += dl;
-                s[0] = fmaf(dn, n, s[0]);
-                s[1] += dn;
-                if (kKeep) kn[i][e] = n, kd[i][e] = dn;
-                if (GATE == 2) og[e] = dsilu * de * fmaf(n, w[i][e], b[GATE == 2 ? i : 0][e]);
+                const F2 n = mul2(CENTER ? add2(u, mu) : u, rs), dn = mul2(dl, w[i][m]);
+                dw[i][m] = fma2(dl, n, dw[i][m]);
+                db[i][m] = add2(db[i][m], dl);
+                s0 = fma2(dn, n, s0);
+                if (CENTER) s1 = add2(s1, dn);
+                if (kKeep) kn[i][m] = n, kd[i][m] = dn;
+                if (GATE == 2) og[m] = mul2(mul2(dsilu, de), fma2(n, w[i][m], b[GATE == 2 ? i : 0][m]));
             }
-            if (GATE == 2 && live) store_vec<T, VEC>(dgate + r * p.D + v * VEC, og);
+            if (GATE == 2 && live) store_pairs<T, PAIRS>(dgate + r * p.D + v * VEC, og);
         }
         if (kKeep) fetch(r + stride);
-        row_sum<TPR, 2>(s, buf, phase);
+        float s[CENTER ? 2 : 1];
+        s[0] = get(s0).x + get(s0).y;
+        if (CENTER) s[CENTER ? 1 : 0] = get(s1).x + get(s1).y;
+        row_sum<TPR, CENTER ? 2 : 1>(s, buf, phase);
         if (!live) continue;
-        const float m0 = s[0] * p.inv_d, m1 = CENTER ? s[1] * p.inv_d : 0.f;
+        const float a0 = -s[0] * p.inv_d, a1 = CENTER ? -s[CENTER ? 1 : 0] * p.inv_d : 0.f;
+        const F2 m0 = f2(a0, a0), m1 = f2(a1, a1);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int v = i * TPR + l;
             if (v >= nv) continue;
-            float o[VEC], og[VEC];
+            F2 o[PAIRS], og[PAIRS];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                float n, dn, a = 1.f, bb = 0.f;
+            for (int m = 0; m < PAIRS; ++m) {
+                F2 n, dn, a = one, bb = zero;
                 if (kKeep) {
-                    n = kn[i][e], dn = kd[i][e];
-                    if (GATE == 1) a = ka[i][e], bb = kb[i][e];
+                    n = kn[i][m], dn = kd[i][m];
+                    if (GATE == 1) a = ka[i][m], bb = kb[i][m];
                 } else {
-                    float u = q[i].get(e), dl = d[i].get(e);
+                    F2 u = q[i].pair(m), dl = d[i].pair(m);
                     if (GATE) {
-                        const float zz = z[i].get(e), sg = sigmoid<kFast>(zz), si = zz * sg;
-                        if (GATE == 1) bb = u * fmaf(si, 1.f - sg, sg), a = si, u *= si;
-                        else dl *= si;
+                        const F2 zz = z[i].pair(m), sg = sigmoid<kFast>(zz), si = mul2(zz, sg);
+                        if (GATE == 1) bb = mul2(u, fma2(si, fma2(sg, minus, one), sg)), a = si, u = mul2(u, si);
+                        else dl = mul2(dl, si);
                     }
-                    n = (u - mu) * rs, dn = dl * w[i][e];
+                    n = mul2(CENTER ? add2(u, mu) : u, rs), dn = mul2(dl, w[i][m]);
                 }
-                const float du = rs * (dn - n * m0 - m1);
-                o[e] = GATE == 1 ? du * a : du;
-                if (GATE == 1) og[e] = du * bb;
+                F2 du = fma2(n, m0, dn);
+                if (CENTER) du = add2(du, m1);
+                du = mul2(du, rs);
+                o[m] = GATE == 1 ? mul2(du, a) : du;
+                if (GATE == 1) og[m] = mul2(du, bb);
             }
-            store_vec<T, VEC>(dx + r * p.D + v * VEC, o);
-            if (GATE == 1) store_vec<T, VEC>(dgate + r * p.D + v * VEC, og);
+            store_pairs<T, PAIRS>(dx + r * p.D + v * VEC, o);
+            if (GATE == 1) store_pairs<T, PAIRS>(dgate + r * p.D + v * VEC, og);
         }
     }
     // the block's sums of dweight, dbias
@@ -277,9 +306,10 @@ norm_bwd_kernel(NormP p, const T *__restrict__ x, const void *__restrict__ weigh
             const int v = i * TPR + l;
             if (v >= nv) continue;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                out[v * VEC + e] = dw[i][e];
-                out[p.D + v * VEC + e] = db[i][e];
+            for (int m = 0; m < PAIRS; m += 2) {
+                const float2 a = get(dw[i][m]), b = get(dw[i][m + 1]), c = get(db[i][m]), d = get(db[i][m + 1]);
+                *reinterpret_cast<float4 *>(out + v * VEC + 2 * m) = make_float4(a.x, a.y, b.x, b.y);
+                *reinterpret_cast<float4 *>(out + p.D + v * VEC + 2 * m) = make_float4(c.x, c.y, d.x, d.y);
             }
         }
     } else {
@@ -291,8 +321,9 @@ norm_bwd_kernel(NormP p, const T *__restrict__ x, const void *__restrict__ weigh
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     const int at = (i * VEC + e) * TPR + l;
-                    sum[at] = (k ? sum[at] : 0.f) + dw[i][e];
-                    sum[TPR * NV * VEC + at] = (k ? sum[TPR * NV * VEC + at] : 0.f) + db[i][e];
+                    const float2 a = get(dw[i][e / 2]), b = get(db[i][e / 2]);
+                    sum[at] = (k ? sum[at] : 0.f) + (e & 1 ? a.y : a.x);
+                    sum[TPR * NV * VEC + at] = (k ? sum[TPR * NV * VEC + at] : 0.f) + (e & 1 ? b.y : b.x);
                 }
         }
         __syncthreads();
