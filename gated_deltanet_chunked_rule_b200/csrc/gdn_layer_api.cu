@@ -25,6 +25,14 @@ bool all_aligned16(std::initializer_list<const void *> ps) {
     return true;
 }
 
+// Whether an output is one of the call's inputs: other blocks may still read them.
+bool over_input(std::initializer_list<const void *> outs, std::initializer_list<const void *> ins) {
+    for (const void *o : outs)
+        for (const void *i : ins)
+            if (o && o == i) return true;
+    return false;
+}
+
 // The sequences of a problem; GDN_OK or why they are refused.
 int make_seq(int B, int T, int num_seqs, const int32_t *cu, SeqMap *m) {
     if (B < 1 || T < 0 || num_seqs < 0) return GDN_ERR_INVALID_ARG;
@@ -203,8 +211,8 @@ int gdn_conv_fwd(const gdn_conv_problem *p, const void *x, const void *weight, c
     const int rc = conv_args(p, &a);
     if (rc != GDN_OK) return rc;
     if (!weight || (a.seq.total && (!x || !y))) return GDN_ERR_INVALID_ARG;
-    if (final_state && final_state == initial_state) return GDN_ERR_INVALID_ARG;
     if (!all_aligned16({x, weight, bias, initial_state, y, final_state})) return GDN_ERR_INVALID_ARG;
+    if (over_input({y, final_state}, {x, weight, bias, initial_state})) return GDN_ERR_INVALID_ARG;
     a.x = x, a.weight = weight, a.bias = bias, a.state = initial_state, a.y = y, a.final_state = final_state;
     a.stream = (cudaStream_t)stream;
     if (!(a.status = status_ptr())) return GDN_ERR_CUDA;
@@ -221,6 +229,7 @@ int gdn_conv_bwd(const gdn_conv_problem *p, const void *x, const void *weight, c
     if (!weight || !dweight || (a.seq.total && (!x || !dy || !dx))) return GDN_ERR_INVALID_ARG;
     if (!all_aligned16({x, weight, bias, initial_state, dy, dfinal, dx, dweight, dbias, dinitial_state})) return GDN_ERR_INVALID_ARG;
     if (!good_ws(workspace, workspace_bytes, conv_part_bytes(a.seq.total, a.C, a.W))) return GDN_ERR_WORKSPACE;
+    if (over_input({dx, dweight, dbias, dinitial_state}, {x, weight, bias, initial_state, dy, dfinal})) return GDN_ERR_INVALID_ARG;
     a.x = x, a.weight = weight, a.bias = bias, a.state = initial_state, a.dy = dy, a.dfinal = dfinal;
     a.dx = dx, a.dweight = dweight, a.dbias = dbias, a.dstate = dinitial_state, a.part = (float *)workspace;
     a.stream = (cudaStream_t)stream;
@@ -279,6 +288,7 @@ int gdn_scan_fwd(const gdn_scan_problem *p, const void *x, const void *dt, const
     if (a.seq.total && !y) return GDN_ERR_INVALID_ARG;
     if (!all_aligned16({y, final_state}) || ((uintptr_t)saved & 255u)) return GDN_ERR_INVALID_ARG;
     if (!good_ws(workspace, workspace_bytes, gdn_scan_fwd_workspace_size(p))) return GDN_ERR_WORKSPACE;
+    if (over_input({y, final_state}, {x, dt, A, B, C, D, dt_bias, h0})) return GDN_ERR_INVALID_ARG;
     a.y = y, a.final_state = final_state, a.saved = saved, a.ws = workspace;
     if (!(a.status = status_ptr())) return GDN_ERR_CUDA;
     if (scan_on_tensor_cores(a)) return finish(scan_fwd_tc(a));
@@ -309,6 +319,7 @@ int gdn_scan_bwd(const gdn_scan_problem *p, const void *x, const void *dt, const
     if (!dA || (a.seq.total && (!dy || !dx || !ddt || !dB || !dC))) return GDN_ERR_INVALID_ARG;
     if (!all_aligned16({dy, dht, dx, ddt, dA, dB, dC, dD, ddt_bias, dh0}) || ((uintptr_t)saved & 255u)) return GDN_ERR_INVALID_ARG;
     if (!good_ws(workspace, workspace_bytes, gdn_scan_bwd_workspace_size(p))) return GDN_ERR_WORKSPACE;
+    if (over_input({dx, ddt, dA, dB, dC, dD, ddt_bias, dh0}, {x, dt, A, B, C, D, dt_bias, h0, saved, dy, dht})) return GDN_ERR_INVALID_ARG;
     a.saved = const_cast<void *>(saved), a.dy = dy, a.dht = dht, a.dx = dx, a.ddt = ddt, a.dA = dA, a.dB = dB, a.dC = dC, a.dD = dD;
     a.ddt_bias = ddt_bias, a.dh0 = dh0, a.ws = workspace;
     if (!(a.status = status_ptr())) return GDN_ERR_CUDA;
@@ -330,6 +341,7 @@ int gdn_norm_fwd(const gdn_norm_problem *p, const void *x, const void *weight, c
     if (rc != GDN_OK) return rc;
     if (!weight || (a.R && (!x || !y))) return GDN_ERR_INVALID_ARG;
     if (!all_aligned16({x, weight, bias, gate, y, stats})) return GDN_ERR_INVALID_ARG;
+    if (over_input({y, stats}, {x, weight, bias, gate})) return GDN_ERR_INVALID_ARG;
     a.x = x, a.weight = weight, a.bias = bias, a.gate = gate, a.y = y, a.stats = stats, a.stream = (cudaStream_t)stream;
     TimedLaunch t("norm_fwd", a.stream);
     return finish(launch_norm_fwd(a));
@@ -344,6 +356,7 @@ int gdn_norm_bwd(const gdn_norm_problem *p, const void *x, const void *weight, c
     if (!weight || !dweight || (a.R && (!x || !dy || !stats || !dx || (gate && !dgate)))) return GDN_ERR_INVALID_ARG;
     if (!all_aligned16({x, weight, bias, gate, dy, stats, dx, dweight, dbias, dgate})) return GDN_ERR_INVALID_ARG;
     if (!good_ws(workspace, workspace_bytes, norm_part_bytes(a))) return GDN_ERR_WORKSPACE;
+    if (over_input({dx, dweight, dbias, dgate}, {x, weight, bias, gate, dy, stats})) return GDN_ERR_INVALID_ARG;
     a.x = x, a.weight = weight, a.bias = bias, a.gate = gate, a.dy = dy, a.stats = const_cast<float *>(stats);
     a.dx = dx, a.dweight = dweight, a.dbias = dbias, a.dgate = dgate, a.part = (float *)workspace, a.stream = (cudaStream_t)stream;
     TimedLaunch t("norm_bwd", a.stream);

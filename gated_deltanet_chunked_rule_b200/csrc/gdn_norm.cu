@@ -497,8 +497,8 @@ bool in_registers(const NormArgs &a) {
 }
 
 // Blocks that walk the rows: as many as run at once, at most one per row group (and at most eight
-// per SM: a backward's partial sums are one row per block).
-constexpr int kMostPerSm = 8;
+// per SM, four of a block per row: a backward's partial sums are one row per block).
+int most_per_sm(int tpr) { return tpr > 32 ? 4 : 8; }
 
 int walk_blocks(long long groups, int per_sm) {
     const long long most = (long long)sm_count() * per_sm;
@@ -506,10 +506,10 @@ int walk_blocks(long long groups, int per_sm) {
 }
 
 template <typename Kernel>
-int resident(Kernel kernel) {
+int resident(Kernel kernel, int most) {
     int n = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, 0) != cudaSuccess || n < 1) n = 1;
-    return n < kMostPerSm ? n : kMostPerSm;
+    return n < most ? n : most;
 }
 
 template <typename T, int TPR, int NV, int GATE, bool CENTER>
@@ -519,12 +519,12 @@ cudaError_t run(const NormArgs &a, bool bwd) {
     const int wf32 = a.wdtype == GDN_DTYPE_F32;
     if (!bwd) {
         auto kernel = norm_fwd_kernel<T, TPR, NV, GATE, CENTER>;
-        static const int per_sm = resident(kernel);  // the kernel's own, the same on every such device
+        static const int per_sm = resident(kernel, most_per_sm(TPR));  // the kernel's own, the same on every such device
         kernel<<<walk_blocks(groups, per_sm), kThreads, 0, a.stream>>>(
             p, (const T *)a.x, a.weight, a.bias, wf32, (const T *)a.gate, (T *)a.y, a.stats);
     } else {
         auto kernel = norm_bwd_kernel<T, TPR, NV, GATE, CENTER>;
-        static const int per_sm = resident(kernel);
+        static const int per_sm = resident(kernel, most_per_sm(TPR));
         const int blocks = walk_blocks(groups, per_sm);
         kernel<<<blocks, kThreads, 0, a.stream>>>(
             p, (const T *)a.x, a.weight, a.bias, wf32, (const T *)a.gate, (const T *)a.dy, a.stats, (T *)a.dx, (T *)a.dgate, a.part);
@@ -594,7 +594,8 @@ cudaError_t dispatch(const NormArgs &a, bool bwd) {
 }  // namespace
 
 size_t norm_part_bytes(const NormArgs &a) {
-    const int blocks = in_registers(a) ? sm_count() * kMostPerSm : any_dw_blocks(a);
+    const int wide = a.D / (a.dtype == GDN_DTYPE_BF16 ? 8 : 4) > 128;  // a block per row (by_width)
+    const int blocks = in_registers(a) ? walk_blocks(a.R, most_per_sm(wide ? kThreads : 32)) : any_dw_blocks(a);
     return (size_t)blocks * 2 * a.D * sizeof(float);
 }
 

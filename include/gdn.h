@@ -193,7 +193,8 @@ int gdn_recurrent_fwd(const gdn_problem *p, const void *q, const void *k, const 
  * inconsistent one never leads out of the tensors and is recorded as
  * GDN_ERR_DEVICE_ARG in the status word; the results are then unspecified.
  * Packed sequences are independent, also for non-finite values. Results do not
- * change from run to run. The FlashQLA pages have no counterpart to these.
+ * change from run to run. An output must not be one of the call's inputs (or
+ * overlap one), except for the states that are said to be updated in place. The FlashQLA pages have no counterpart to these.
  * ------------------------------------------------------------------------- */
 
 /* Short causal convolution, depthwise: per channel and sequence

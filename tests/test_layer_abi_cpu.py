@@ -190,3 +190,44 @@ def test_packed_offsets():
     for c, b in ((torch.tensor([0]), 1), (torch.tensor([[0, 1]]), 1), (torch.tensor([0.0, 1.0]), 1), (torch.tensor([0, 1]), 2)):
         with pytest.raises(ValueError):
             ops._packed(c, b, cpu)
+
+
+def test_outputs_over_inputs_refused(L):
+    """Each output given one of the inputs' buffers, everything else distinct."""
+    def q(i):
+        return ctypes.c_void_p((1 << 20) + (i << 12))
+
+    ws = q(40)
+    p = ctypes.byref(conv())
+    for out in range(2):
+        for i in range(4):
+            o = [q(10), q(11)]
+            o[out] = q(i)
+            assert L.gdn_conv_fwd(p, q(0), q(1), q(2), q(3), *o, None) == INV
+    for out in range(4):
+        for i in range(6):
+            o = [q(10 + k) for k in range(4)]
+            o[out] = q(i)
+            assert L.gdn_conv_bwd(p, *(q(k) for k in range(6)), *o, ws, BIG, None) == INV
+    p = ctypes.byref(scan())
+    for out in range(2):
+        for i in range(8):
+            o = [q(10), q(11)]
+            o[out] = q(i)
+            assert L.gdn_scan_fwd(p, *(q(k) for k in range(8)), *o, None, ws, BIG, None) == INV
+    for out in range(8):
+        for i in range(11):
+            o = [q(20 + k) for k in range(8)]
+            o[out] = q(i)
+            assert L.gdn_scan_bwd(p, *(q(k) for k in range(11)), *o, ws, BIG, None) == INV
+    p = ctypes.byref(norm())
+    for out in range(2):
+        for i in range(4):
+            o = [q(10), q(11)]
+            o[out] = q(i)
+            assert L.gdn_norm_fwd(p, *(q(k) for k in range(4)), *o, None) == INV
+    for out in range(4):
+        for i in range(6):
+            o = [q(20 + k) for k in range(4)]
+            o[out] = q(i)
+            assert L.gdn_norm_bwd(p, *(q(k) for k in range(6)), *o, ws, BIG, None) == INV
