@@ -259,12 +259,23 @@ __global__ void __launch_bounds__(256) scan_segments_kernel(ScanP p, int element
     const size_t slot0 = p.m.slot0(n, p.seg.tokens);
     auto slot = [&](int i) { return slot0 + (REV ? segs - 1 - i : i); };
     auto at = [&](int i) { return p.seg.state + (slot(i) * p.H + h) * elements + e; };
-    float cur = from ? from[((size_t)n * p.H + h) * elements + e] : 0.f, end = *at(0);
-    for (int i = 0; i + 1 < segs; ++i) {
-        const float v = end;
-        if (i + 2 < segs) end = *at(i + 1);  // before its place is taken
-        cur = fmaf(expf(p.seg.decay[slot(i) * p.H + h]), cur, v);
-        *at(i + 1) = cur;
+    float cur = from ? from[((size_t)n * p.H + h) * elements + e] : 0.f, next = *at(0);
+    constexpr int kBatch = 8;  // ends loaded together, each before its place is taken
+    for (int i = 0; i + 1 < segs; i += kBatch) {
+        float end[kBatch + 1], decay[kBatch];
+        end[0] = next;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            end[k + 1] = i + k + 2 < segs ? *at(i + k + 1) : 0.f;
+            decay[k] = i + k + 1 < segs ? p.seg.decay[slot(i + k) * p.H + h] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            if (i + k + 1 >= segs) break;
+            cur = fmaf(expf(decay[k]), cur, end[k]);
+            *at(i + k + 1) = cur;
+        }
+        next = end[kBatch];
     }
 }
 
@@ -429,37 +440,55 @@ scan_gather_kernel(ScanP p, const Tdt *__restrict__ dt, const float *__restrict_
     }
 }
 
-// Per tile of 16 tokens and head (a thread per head): the gradients of the log decay and
+// Per tile of 16 tokens and head (16 lanes, one per token): the gradients of the log decay and
 // dt, and this tile's parts [slots, 3, H] of dA, ddt_bias and dD.
+constexpr int kGateHeads = 8;  // per block
 template <typename Tdt>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(kGateHeads * kKeep)
 scan_gates_kernel(ScanP p, const Tdt *__restrict__ dt, Dots dots, const float *__restrict__ chunk_q, int S,
                   Tdt *__restrict__ ddt, float *__restrict__ part) {
-    const int h = blockIdx.y * blockDim.x + threadIdx.x, slot = blockIdx.x;
-    if (h >= p.H) return;
+    static_assert(kKeep == 16, "half a warp per tile");
+    const int i = threadIdx.x % kKeep, h = blockIdx.y * kGateHeads + threadIdx.x / kKeep, slot = blockIdx.x;
     int n, local;
     float dA = 0.f, dbias = 0.f, dD = 0.f;
-    if (p.m.slot(slot, kKeep, &n, &local)) {
-        const int t0 = p.m.begin(n) + local * kKeep, len = min(kKeep, p.m.end(n) - t0);
+    if (p.m.slot(slot, kKeep, &n, &local) && h < p.H) {
+        const int t0 = p.m.begin(n) + local * kKeep, t = t0 + i;
+        const bool live = t < p.m.end(n);
         const float A = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.f;
-        float carry = 0.f;
-        for (int k = 0; k < S; ++k) carry += chunk_q[((size_t)slot * p.H + h) * S + k];
-        for (int t = t0 + len - 1; t >= t0; --t) {
-            const size_t at = (size_t)t * p.H + h;
-            const float raw = to_f32(dt[t * p.dts + h]) + bias, d = delta_of(raw, p.softplus);
-            float rv = 0.f, vv = 0.f, wv = 0.f;
+        const size_t at = (size_t)t * p.H + h;
+        float raw = 0.f, d = 0.f, rv = 0.f, vv = 0.f, wv = 0.f, q = 0.f;
+        for (int k = 0; k < S; ++k) q += chunk_q[((size_t)slot * p.H + h) * S + k];
+        if (live) {
+            raw = to_f32(dt[t * p.dts + h]) + bias, d = delta_of(raw, p.softplus);
             for (int k = 0; k < S; ++k) {
                 rv += *dots(kR, at * S + k), vv += *dots(kV, at * S + k), wv += *dots(kWt, at * S + k);
                 dD += *dots(kXd, at * S + k);
             }
-            carry += rv - d * vv;
-            dA = fmaf(d, carry, dA);
+        }
+        // a token's log decay: what later tokens of the tile leave, and the tile's end
+        float carry = rv - d * vv;
+        const unsigned half = 0xffffu << (threadIdx.x & 16);
+#pragma unroll
+        for (int o = 1; o < kKeep; o <<= 1) {
+            const float v = __shfl_down_sync(half, carry, o, kKeep);
+            if (i + o < kKeep) carry += v;
+        }
+        carry += q;
+        if (live) {
+            dA = d * carry;
             float g = fmaf(A, carry, wv);
             if (p.softplus) g /= 1.f + expf(-raw);
             ddt[at] = from_f32<Tdt>(g);
-            dbias += g;
+            dbias = g;
+        }
+#pragma unroll
+        for (int o = kKeep / 2; o > 0; o >>= 1) {
+            dA += __shfl_xor_sync(half, dA, o, kKeep);
+            dbias += __shfl_xor_sync(half, dbias, o, kKeep);
+            dD += __shfl_xor_sync(half, dD, o, kKeep);
         }
     }
+    if (i || h >= p.H) return;
     part[((size_t)slot * 3 + 0) * p.H + h] = dA;
     part[((size_t)slot * 3 + 1) * p.H + h] = dbias;
     part[((size_t)slot * 3 + 2) * p.H + h] = dD;
@@ -588,7 +617,7 @@ cudaError_t backward(const ScanArgs &a) {
     if (a.seq.total)
         scan_gather_kernel<Tin, Tdt, K><<<a.seq.total, K, 0, a.stream>>>(p, dt, dc, db, (Tin *)a.dB, (Tin *)a.dC);
     if (slots)
-        scan_gates_kernel<Tdt><<<dim3(slots, (a.H + 127) / 128), 128, 0, a.stream>>>(p, dt, dots, q, a.P / kCols, (Tdt *)a.ddt, part);
+        scan_gates_kernel<Tdt><<<dim3(slots, (a.H + kGateHeads - 1) / kGateHeads), kGateHeads * kKeep, 0, a.stream>>>(p, dt, dots, q, a.P / kCols, (Tdt *)a.ddt, part);
     return launch_scan_sum(part, slots, a);
 }
 
