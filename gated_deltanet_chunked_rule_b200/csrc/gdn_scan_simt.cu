@@ -514,13 +514,14 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 // Tokens of a segment; 0: whole sequences. Four CTAs of these kernels run on an SM; where there are
 // fewer than two per SM a sequence is cut into about as many segments as would fill them, of at
-// least four tiles (a packed batch, of unknown lengths, by its total).
+// least two tiles (a packed batch, of unknown lengths, by its total). 1000 tokens of 4 heads, K = P =
+// 64: forward and backward 30 + 90 us with two tiles, 34 + 108 with three, 40 + 125 with four.
 int segment_tokens(const ScanArgs &a) {
     const long long ctas = (long long)(a.seq.cu ? 1 : a.seq.N) * a.H * (a.P / kCols);
     const int tokens = a.seq.cu ? a.seq.total : a.seq.T;
     if (ctas >= 2 * sm_count() || tokens < 8 * kTile) return 0;
     const long long want = (4ll * sm_count() + ctas - 1) / ctas, per = (tokens + want - 1) / want;
-    return (int)((per < 4 * kTile ? 4 * kTile : per) + kTile - 1) / kTile * kTile;
+    return (int)((per < 2 * kTile ? 2 * kTile : per) + kTile - 1) / kTile * kTile;
 }
 
 size_t segments_bytes(const ScanArgs &a) {
