@@ -12,7 +12,13 @@
 // unit (a thread per row and column quarter) and mask the next head's P before they take up
 // this unit's products, so that the tensor core's latency is behind the mask: P, the
 // accumulators and h have two buffers, x three. Warp 16 issues the products, warp 17 loads and
-// stores, warps 18 and 19 prepare the mask's factors a head ahead. Two units side by side in eight warps each, without that overlap, took 4.7 us.
+// stores, warps 18 and 19 prepare the heads' row and column factors a head ahead. Two units side
+// by side in eight warps each, without that overlap, took 4.7 us; a unit takes 1.65 us now.
+// 8192 tokens, 64 heads: 57 us, 128 CTAs; 32768 packed tokens, 32 heads in 4 groups: 151 us. Bound by
+// the row warps: their schedulers issue in 62 % of the cycles and wait for tensor memory and shared
+// memory in the rest (a unit's products and tiles need 0.8 us of the shared memory's bandwidth). With the
+// row warps forming their own row factors 64 us; packed pairs of fp32 in the mask, whose operands
+// have to be moved together first, 71 us.
 //
 // The mask's exponentials: for a column left of the row's block of 32 tokens
 // e^{gam_r - gam_s} delta_s factors at the block's start, into one factor per row and one per

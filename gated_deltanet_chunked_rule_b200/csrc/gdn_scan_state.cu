@@ -9,8 +9,9 @@
 // accumulator columns) of a group: warps 0-7 hold unit 0's state in fp32 registers (a thread
 // per row of K and 32 columns), warps 8-15 unit 1's, warp 16 loads the tiles by TMA (two
 // stages), warp 17 issues the products. Bound by the sixteen warps' conversions (about 430
-// instructions per chunk each) and the 24 products of 64 cycles; with eight warps of 64
-// columns each the latencies showed and a chunk took 3.6 us instead.
+// instructions per chunk each), the 24 products of 64 cycles and the 400 KB that both move
+// through shared memory (1.6 us of a chunk's 2.7); with eight warps of 64 columns each the
+// latencies showed and a chunk took 3.6 us instead. 8192 tokens, 64 heads: 47 us in one pass.
 //
 // The fp32 state keeps fp32 precision although the tensor core takes bf16: B is bf16 as it
 // is, and Xs is cut into three bf16 terms that hold its 24 bits exactly (8 + 8 + 8, by
