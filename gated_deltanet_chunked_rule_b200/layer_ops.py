@@ -27,6 +27,8 @@ from . import _binding as _b
 from .api import _DTYPES
 
 _F32 = torch.float32
+_Tensor = torch.Tensor
+_empty_like = torch.empty_like
 
 
 def _call(dev, name, *args):
@@ -58,7 +60,7 @@ def _p(t):
 def _check(dev, *want):
     """Every tensor the library reads or writes: (name, tensor or None, shape, dtype)."""
     for name, t, shape, dtype in want:
-        if t is None:
+        if t is None or (t.__class__ is _Tensor and t.dtype is dtype and t.device == dev and t.shape == shape):
             continue
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
@@ -68,6 +70,11 @@ def _check(dev, *want):
             raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
         if t.shape != shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _empty(like):
+    """Contiguous, of like's shape (empty_like keeps a slice's strides, and takes half as long)."""
+    return _empty_like(like) if like.is_contiguous() else like.new_empty(like.shape)
 
 
 def _cuda(x, name="x"):
@@ -151,7 +158,7 @@ def causal_conv1d_fwd(x, weight, bias=None, activation=None, initial_state=None,
     dev, x, weight, bias, P, cu, state = _conv(x, weight, bias, activation, cu_seqlens)
     _check(dev, ("initial_state", initial_state, state, x.dtype))
     initial_state = _dense(initial_state)
-    y = x.new_empty(x.shape)
+    y = _empty(x)
     fin = x.new_empty(state) if output_final_state else None
     _call(dev, "gdn_conv_fwd", byref(P), x.data_ptr(), _p(weight), _p(bias), _p(initial_state), y.data_ptr(), _p(fin))
     return y, fin
@@ -163,7 +170,7 @@ def causal_conv1d_bwd(x, weight, bias, dy, dfinal=None, activation=None, initial
     _check(dev, ("initial_state", initial_state, state, x.dtype), ("dy", dy, x.shape, x.dtype),
            ("dfinal", dfinal, state, x.dtype))
     initial_state, dy, dfinal = _dense(initial_state), _dense(dy), _dense(dfinal)
-    dx = x.new_empty(x.shape)
+    dx = _empty(x)
     dw = torch.empty_like(weight)
     db = torch.empty_like(bias) if bias is not None else None
     ds = torch.empty_like(initial_state) if initial_state is not None else None
@@ -182,7 +189,7 @@ def causal_conv1d_update(x, conv_state, weight, bias=None, activation=None):
     if conv_state is None:
         raise ValueError("conv_state is required")
     _in_place("conv_state", conv_state)
-    y = x.new_empty(x.shape)
+    y = _empty(x)
     _call(dev, "gdn_conv_update", byref(P), x.data_ptr(), _p(weight), _p(bias), conv_state.data_ptr(), y.data_ptr())
     return y
 
@@ -243,9 +250,6 @@ class _Scan:
         return (byref(self.P), self.x.data_ptr(), self.dt.data_ptr(), self.A.data_ptr(), self.B.data_ptr(), self.C.data_ptr(),
                 _p(self.D), _p(self.dt_bias), _p(self.h0))
 
-    def empty(self, like):
-        return like.new_empty(like.shape)
-
     def bytes(self, n):
         return self.x.new_empty(n, dtype=torch.uint8)
 
@@ -259,7 +263,7 @@ def chunk_selective_scan_fwd(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus=F
     dtype), A, D, dt_bias [H] fp32, B and C [B, T, G, K] (H a multiple of G), states
     [N, H, K, V] fp32. Returns (y, final_state or None, saved or None)."""
     s = _Scan(x, dt, A, B, C, D, dt_bias, dt_softplus, initial_state, cu_seqlens)
-    y = s.empty(x)
+    y = _empty(x)
     fin = s.states() if output_final_state else None
     saved = s.bytes(_size(s.dev, "gdn_scan_saved_size", s.P)) if save_for_backward else None
     n = _size(s.dev, "gdn_scan_fwd_workspace_size", s.P)
@@ -275,9 +279,9 @@ def chunk_selective_scan_bwd(x, dt, A, B, C, D, dt_bias, dt_softplus, saved, dy,
     s = _Scan(x, dt, A, B, C, D, dt_bias, dt_softplus, initial_state, cu_seqlens)
     _check(s.dev, ("dy", dy, x.shape, x.dtype), ("dht", dht, s.state, _F32))
     dy, dht = _dense(dy), _dense(dht)
-    dx, ddt, dB, dC, dA = s.empty(x), s.empty(dt), s.empty(B), s.empty(C), s.empty(A)
-    dD = s.empty(D) if D is not None else None
-    db = s.empty(dt_bias) if dt_bias is not None else None
+    dx, ddt, dB, dC, dA = _empty(x), _empty(dt), _empty(B), _empty(C), _empty(A)
+    dD = _empty(D) if D is not None else None
+    db = _empty(dt_bias) if dt_bias is not None else None
     dh0 = s.states()
     if saved is not None:
         _check(s.dev, ("saved", saved, saved.shape, torch.uint8))
@@ -303,7 +307,7 @@ def recurrent_selective_scan(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus=F
         final_state = s.states()
     else:
         _in_place("final_state", final_state)
-    y = s.empty(x)
+    y = _empty(x)
     _call(s.dev, "gdn_scan_step", *s.inputs(), y.data_ptr(), final_state.data_ptr())
     return y, final_state
 
