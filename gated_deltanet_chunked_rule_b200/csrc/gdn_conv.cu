@@ -262,6 +262,7 @@ __global__ void __launch_bounds__(32 * kWarps, kResident)
 conv_bwd_kernel(ConvP p, const T *__restrict__ x, const T *__restrict__ weight, const T *__restrict__ bias,
                 const T *__restrict__ state, const T *__restrict__ dy, const T *__restrict__ dfinal, T *__restrict__ dx,
                 float *__restrict__ part, unsigned *status) {
+    let_next_start();
     using P = Pack<T, VEC>;
     constexpr int U = UB;
     __shared__ float red[kWarps][(W + 1) * VEC][32];
@@ -383,6 +384,7 @@ conv_bwd_kernel(ConvP p, const T *__restrict__ x, const T *__restrict__ weight, 
 // value, each over every eighth block.
 template <typename T>
 __global__ void __launch_bounds__(256) conv_dw_kernel(const float *__restrict__ part, int blocks, int C, int W, T *dweight, T *dbias) {
+    wait_for_previous();
     __shared__ float red[8][33];
     const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane, j = blockIdx.y;
@@ -491,7 +493,9 @@ cudaError_t run_pass(const ConvArgs &a, Pass pass) {
                                                                                       a.status);
         }
         TimedLaunch tl("conv_bwd_sums", a.stream);
-        conv_dw_kernel<T><<<dim3((a.C + 31) / 32, W + 1), 256, 0, a.stream>>>(a.part, blocks, a.C, W, (T *)a.dweight, (T *)a.dbias);
+        const cudaError_t e = launch(blocks > 0, conv_dw_kernel<T>, dim3((a.C + 31) / 32, W + 1), dim3(256), 0, a.stream, a.part, blocks, a.C, W,
+                                     (T *)a.dweight, (T *)a.dbias);
+        if (e != cudaSuccess) return e;
         if (a.dstate)
             conv_dstate_kernel<T, W><<<dim3(a.seq.N, (a.C + 127) / 128), 128, 0, a.stream>>>(p, x, w, b, st, dy, df, (T *)a.dstate);
     } else {

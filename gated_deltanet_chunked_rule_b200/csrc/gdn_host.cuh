@@ -35,4 +35,18 @@ inline int sm_count() {
     return sms;
 }
 
+// Launches a kernel; `follows`: the launch before it on the stream is a kernel of the same call, and
+// this one calls wait_for_previous before it reads what that one wrote, or writes what it reads. It
+// may then come up while that one ends.
+template <typename... Want, typename... Have>
+cudaError_t launch(bool follows, void (*kernel)(Want...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, Have &&...args) {
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid, c.blockDim = block, c.dynamicSmemBytes = smem, c.stream = stream;
+    c.attrs = &early, c.numAttrs = follows ? 1 : 0;
+    return cudaLaunchKernelEx(&c, kernel, static_cast<Want>(args)...);
+}
+
 }  // namespace gdn

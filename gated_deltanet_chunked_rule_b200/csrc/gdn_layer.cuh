@@ -7,6 +7,12 @@
 
 namespace gdn {
 
+// The kernel after this one may come up once every block of this one has started ...
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;"); }
+// ... and waits here, in every block, until this one has ended and its writes are there (launched
+// the usual way it has waited already).
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Sequences on the flattened token axis: B rows of T tokens, or N packed ones whose
 // offsets stand in cu (device, [N + 1]). A kernel clamps what it reads from cu to
 // [0, total], so an inconsistent copy never leads out of the tensors; one block of

@@ -120,6 +120,7 @@ scan_tc::StateArgs state_pass(const ScanArgs &a, const scan_tc::Gates &gates, bo
     s.a = &a;
     s.gates = gates;
     s.reverse = reverse;
+    s.after_gates = !reverse;
     s.chunks_per_seg = scan_tc::chunks_per_segment(a);
     if (s.chunks_per_seg) {
         const size_t slots = a.seq.slots(s.chunks_per_seg * scan_tc::kC);

@@ -195,6 +195,7 @@ __global__ void __launch_bounds__(kThreads, NV == 1 ? 3 : NV == 2 ? 2 : 1)
 norm_bwd_kernel(NormP p, const T *__restrict__ x, const void *__restrict__ weight, const void *__restrict__ bias, int wf32,
                 const T *__restrict__ gate, const T *__restrict__ dy, const float *__restrict__ stats, T *__restrict__ dx,
                 T *__restrict__ dgate, float *__restrict__ part) {
+    let_next_start();
     constexpr int VEC = 16 / sizeof(T), kGroups = kThreads / TPR;
     constexpr bool kFast = sizeof(T) == 2;
     __shared__ float buf[2][CENTER ? 2 : 1][kThreads / 32];
@@ -343,6 +344,7 @@ norm_bwd_kernel(NormP p, const T *__restrict__ x, const void *__restrict__ weigh
 
 // dweight, dbias [D] from the blocks' parts, in a fixed order.
 __global__ void __launch_bounds__(1024) norm_dw_kernel(const float *__restrict__ part, int blocks, int D, int wf32, void *dweight, void *dbias) {
+    wait_for_previous();
     __shared__ float red[32][33];
     const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
@@ -459,6 +461,7 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads)
 norm_dw_any_kernel(NormP p, const T *__restrict__ x, const T *__restrict__ gate, int GATE, const T *__restrict__ dy,
                    const float *__restrict__ stats, float *__restrict__ part) {
+    let_next_start();
     __shared__ float red[2][8][33];
     const int lane = threadIdx.x & 31, wr = threadIdx.x >> 5;
     const int c = blockIdx.y * 32 + lane;
@@ -512,6 +515,11 @@ int resident(Kernel kernel, int most) {
     return n < most ? n : most;
 }
 
+cudaError_t sum_parts(const NormArgs &a, int blocks) {
+    return launch(blocks > 0, norm_dw_kernel, dim3((a.D + 31) / 32, a.dbias ? 2 : 1), dim3(1024), 0, a.stream, a.part, blocks, a.D,
+                  (int)(a.wdtype == GDN_DTYPE_F32), a.dweight, a.dbias);
+}
+
 template <typename T, int TPR, int NV, int GATE, bool CENTER>
 cudaError_t run(const NormArgs &a, bool bwd) {
     const NormP p = params(a);
@@ -528,7 +536,7 @@ cudaError_t run(const NormArgs &a, bool bwd) {
         const int blocks = walk_blocks(groups, per_sm);
         kernel<<<blocks, kThreads, 0, a.stream>>>(
             p, (const T *)a.x, a.weight, a.bias, wf32, (const T *)a.gate, (const T *)a.dy, a.stats, (T *)a.dx, (T *)a.dgate, a.part);
-        norm_dw_kernel<<<dim3((a.D + 31) / 32, a.dbias ? 2 : 1), 1024, 0, a.stream>>>(a.part, blocks, a.D, wf32, a.dweight, a.dbias);
+        return sum_parts(a, blocks);
     }
     return cudaGetLastError();
 }
@@ -582,8 +590,7 @@ cudaError_t run_any(const NormArgs &a, bool bwd) {
     const int blocks = any_dw_blocks(a);
     norm_dw_any_kernel<T><<<dim3(blocks, (a.D + 31) / 32), kThreads, 0, a.stream>>>(p, (const T *)a.x, (const T *)a.gate, gate,
                                                                                   (const T *)a.dy, a.stats, a.part);
-    norm_dw_kernel<<<dim3((a.D + 31) / 32, a.dbias ? 2 : 1), 1024, 0, a.stream>>>(a.part, blocks, a.D, wf32, a.dweight, a.dbias);
-    return cudaGetLastError();
+    return sum_parts(a, blocks);
 }
 
 cudaError_t dispatch(const NormArgs &a, bool bwd) {
@@ -603,9 +610,7 @@ cudaError_t launch_norm_fwd(const NormArgs &a) { return a.R ? dispatch(a, false)
 
 cudaError_t launch_norm_bwd(const NormArgs &a) {
     if (a.R) return dispatch(a, true);
-    const int wf32 = a.wdtype == GDN_DTYPE_F32;  // no rows: the sums are zero
-    norm_dw_kernel<<<dim3((a.D + 31) / 32, a.dbias ? 2 : 1), 1024, 0, a.stream>>>(a.part, 0, a.D, wf32, a.dweight, a.dbias);
-    return cudaGetLastError();
+    return sum_parts(a, 0);  // no rows: the sums are zero
 }
 
 }  // namespace gdn

@@ -46,6 +46,7 @@ using namespace gdn::warp;
 
 // Gates of every chunk slot: a warp per head.
 __global__ void __launch_bounds__(256) scan_gates_tc_kernel(Params p) {
+    let_next_start();
     const int lane = threadIdx.x & 31, h = blockIdx.y * 8 + (threadIdx.x >> 5);
     if (blockIdx.x == 0 && blockIdx.y == 0) check_cu(p.m, p.status, threadIdx.x, blockDim.x);
     int n, local;
@@ -113,6 +114,7 @@ __device__ __forceinline__ size_t product_at(size_t slot, size_t units, size_t u
 template <int K, bool REVERSE>
 __global__ void __launch_bounds__(kThreads, 1)
 scan_state_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_x, const StateP q) {
+    let_next_start();
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align_smem_1024(smem_raw);
     const uint32_t sb = smem_u32(smem);
@@ -135,6 +137,7 @@ scan_state_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constan
     const int h = mine ? p.head(g, u) : 0;
     const size_t user = (((size_t)n * p.H + h) * K + row) * p.P + (mine ? p.col0(u) : 0) + c0;  // in the user's states
     if (!used) {  // an empty sequence keeps its state
+        wait_for_previous();
         if (local == 0 && s_len == 0 && (q.pass == kWalk || q.pass == kLocal) && q.last && real)
             for (int i = 0; i < kHalf; ++i) q.last[user + i] = q.first ? q.first[user + i] : 0.f;
         return;
@@ -142,7 +145,10 @@ scan_state_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constan
     const int seg_begin = s_begin + local * q.seg_tokens, seg_len = min(q.seg_tokens, s_begin + s_len - seg_begin);
     const bool at_first = REVERSE ? seg_begin + seg_len == s_begin + s_len : local == 0;
     const bool at_last = REVERSE ? local == 0 : seg_begin + seg_len == s_begin + s_len;
-    if (q.pass == kEnds && at_last) return;  // nothing follows it
+    if (q.pass == kEnds && at_last) {  // nothing follows it
+        wait_for_previous();
+        return;
+    }
     const int chunks = (seg_len + kC - 1) / kC;
 
     if (tid == 0) {
@@ -159,6 +165,7 @@ scan_state_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constan
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    wait_for_previous();
     const uint32_t tmem = *tmem_slot;
     auto chunk_at = [&](int i) { return REVERSE ? chunks - 1 - i : i; };
     auto fail = [&]() {
@@ -389,6 +396,7 @@ template <int K>
 __global__ void __launch_bounds__(256)
 scan_starts_kernel(Params p, int seg_tokens, const float *__restrict__ seg, const float *__restrict__ seg_gam,
                    __nv_bfloat16 *__restrict__ starts, float *__restrict__ last) {
+    let_next_start();
     const int n = blockIdx.x, unit = blockIdx.y, e = blockIdx.z * 256 + threadIdx.x, row = e % K, c8 = e / K;
     const int len = p.m.end(n) - p.m.begin(n), segs = (len + seg_tokens - 1) / seg_tokens;
     if (segs == 0) return;
@@ -493,42 +501,36 @@ cudaError_t run(const StateArgs &s) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const dim3 grid(slots, a.G * pairs);
+    bool early = s.after_gates && !s.products;
+    auto pass = [&](const char *name, Pass which) {
+        TimedLaunch t(name, a.stream);
+        q.pass = which;
+        const cudaError_t rc = launch(early, kernel, grid, dim3(kThreads), kSmem, a.stream, mb, mx, q);
+        early = false;
+        return rc;
+    };
     if (s.products) {
-        {
-            TimedLaunch t(REVERSE ? "scan_products_bwd" : "scan_products", a.stream);
-            q.pass = kProducts;
-            kernel<<<grid, kThreads, kSmem, a.stream>>>(mb, mx, q);
-        }
+        if ((e = pass(REVERSE ? "scan_products_bwd" : "scan_products", kProducts)) != cudaSuccess) return e;
         TimedLaunch t(REVERSE ? "scan_chunks_bwd" : "scan_chunks", a.stream);
         scan_chunks_kernel<K, REVERSE><<<dim3(a.seq.N, a.G * q.p.U, K * kPT / 2048), 256, 0, a.stream>>>(q.p, s.seg, s.first, s.last, s.tiles);
         return cudaGetLastError();
     }
     if (s.starts) {
-        {
-            TimedLaunch t("scan_state_local", a.stream);
-            q.pass = kLocal;
-            q.before = s.before;
-            kernel<<<grid, kThreads, kSmem, a.stream>>>(mb, mx, q);
-        }
+        q.before = s.before;
+        if ((e = pass("scan_state_local", kLocal)) != cudaSuccess) return e;
         TimedLaunch t("scan_starts", a.stream);
         scan_starts_kernel<K><<<dim3(a.seq.N, a.G * q.p.U, K * kPT / 2048), 256, 0, a.stream>>>(q.p, q.seg_tokens, s.seg, s.seg_gam, s.starts,
                                                                                             s.last);
         return cudaGetLastError();
     }
     if (split) {
-        q.pass = kEnds;
-        {
-            TimedLaunch t(REVERSE ? "scan_seg_bwd" : "scan_seg", a.stream);
-            kernel<<<grid, kThreads, kSmem, a.stream>>>(mb, mx, q);
-        }
-        q.pass = kWalk;
+        if ((e = pass(REVERSE ? "scan_seg_bwd" : "scan_seg", kEnds)) != cudaSuccess) return e;
         TimedLaunch t("scan_compose", a.stream);
         scan_compose_kernel<K, REVERSE><<<dim3(a.seq.N, a.G * q.p.U, K * kPT / 1024), 256, 0, a.stream>>>(q.p, q.seg_tokens, s.first, s.seg,
                                                                                                      s.seg_gam);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    TimedLaunch t(REVERSE ? "scan_state_bwd" : "scan_state", a.stream);
-    kernel<<<grid, kThreads, kSmem, a.stream>>>(mb, mx, q);
-    return cudaGetLastError();
+    return pass(REVERSE ? "scan_state_bwd" : "scan_state", kWalk);
 }
 
 }  // namespace

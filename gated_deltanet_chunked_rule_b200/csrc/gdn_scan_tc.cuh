@@ -177,6 +177,7 @@ struct StateArgs {
     const ScanArgs *a;
     Gates gates;
     bool reverse;
+    bool after_gates;    // the launch before is launch_gates'
     int chunks_per_seg;  // 0: whole sequences
     bool products;       // the segments write their chunks' products (by_products)
     float *seg;          // those: [chunk slots, units, 64 K]; otherwise [segment slots, units, K, 64]
