@@ -95,6 +95,13 @@ def test_many_packed_sequences(gdn):
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_long_runs(gdn, dtype):
+    # so many channels that a warp's run spans tens of tokens, with sequences' borders inside
+    lens = [500, 1, 0, 2, 37, 300, 3, 0, 163, 8, 486]
+    check(gdn, make(lens, 8192, 4, DT[dtype], 12), lens, True)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_empty_batch(gdn, dtype):
     v = make([0, 0], 24, 4, DT[dtype], 9)
     check(gdn, v, [0, 0], True)  # final = initial, dstate = dfinal, dweight = 0

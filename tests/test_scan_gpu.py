@@ -275,6 +275,28 @@ def test_autograd_repeat_and_other_stream(gdn, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("H,lens", [(2, [2100]), (2, [700, 0, 1400]), (192, [130])])
+def test_calls_in_a_row(gdn, dtype, H, lens):
+    # nothing between the calls, whose kernels come up early and whose workspaces are the same memory:
+    # each call's results are those of the call by itself
+    both = [make(lens, H, 1, 64, 64, DT[dtype], seed=s) for s in (31, 32)]
+
+    def call(v):
+        y, fin, _ = gdn.chunk_selective_scan_fwd(*args(v), True, v["h0"], True, v["cu"])
+        return y, fin
+
+    alone = []
+    for v in both:
+        alone.append(call(v))
+        torch.cuda.synchronize()
+    got = [call(both[i % 2]) for i in range(24)]
+    torch.cuda.synchronize()
+    assert gdn.device_status() == 0
+    for i, (y, fin) in enumerate(got):
+        assert torch.equal(y, alone[i % 2][0]) and torch.equal(fin, alone[i % 2][1]), i
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_captured_graph(gdn, dtype):
     v = make([150, 90], 4, 2, 128, 64, DT[dtype], seed=17)
     want = train(gdn, v)
