@@ -167,143 +167,143 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                        idC = idesc_bf16(128, K, false, true), idB = idesc_bf16(128, K, true, true);
 
     if (warp >= 8) {
-    reg_dec<kAuxRegs>();
-    if (warp == 8) {  // products on the work region
-        if (lane == 0) {
-            uint32_t b = cols(sb + kB), c = cols(sb + kCt), y = cols(sb + kY), x = cols(sb + kX), yr = rows(sb + kY),
-                     pm = rows(sb + kPm), h0 = state_rows(sb + kH), h1 = state_rows(sb + kH + kTile),
-                           g0 = state_rows(sb + kG), g1 = state_rows(sb + kG + kTile);
-            bool ok = wait_bar(cb_full, 0, abort_flag) && wait_bar(cb_ready, 0, abort_flag);
-            tc_fence_after();
-            if (ok) {
-#pragma unroll
-                for (int k = 0; k < K / 16; ++k) mma<kTokenHi, kTokenHi>(tmem + kColS, c + cstep(k), b + cstep(k), idQ, k > 0);
-            }
-            for (int i = 0; i < units && ok; ++i) {
-                // or the sums below are all formed ahead, in more registers than there are
-                asm volatile("" : "+r"(b), "+r"(c), "+r"(y), "+r"(x), "+r"(yr), "+r"(pm), "+r"(h0), "+r"(h1), "+r"(g0), "+r"(g1));
-                const uint32_t y2 = (i & 1) * ((kY1 - kY) >> 4);
-                // C h
-                if (i > 0) ok = wait_bar(&dx_done[(i - 1) & 1], ((i - 1) >> 1) & 1, abort_flag);  // the work region is read
-                ok = ok && wait_bar(h_full, i & 1, abort_flag);
-                if (!ok) break;
+        reg_dec<kAuxRegs>();
+        if (warp == 8) {  // products on the work region
+            if (lane == 0) {
+                uint32_t b = cols(sb + kB), c = cols(sb + kCt), y = cols(sb + kY), x = cols(sb + kX), yr = rows(sb + kY),
+                         pm = rows(sb + kPm), h0 = state_rows(sb + kH), h1 = state_rows(sb + kH + kTile),
+                               g0 = state_rows(sb + kG), g1 = state_rows(sb + kG + kTile);
+                bool ok = wait_bar(cb_full, 0, abort_flag) && wait_bar(cb_ready, 0, abort_flag);
                 tc_fence_after();
+                if (ok) {
 #pragma unroll
-                for (int k = 0; k < K / 16; ++k) {
-                    mma<kTokenHi, kStateRowsHi<K>>(tmem + kColR, c + cstep(k), h0 + srstep(k), idH, k > 0);
-                    mma<kTokenHi, kStateRowsHi<K>>(tmem + kColR, c + cstep(k), h1 + srstep(k), idH, true);
+                    for (int k = 0; k < K / 16; ++k) mma<kTokenHi, kTokenHi>(tmem + kColS, c + cstep(k), b + cstep(k), idQ, k > 0);
                 }
-                mma_commit(ch_full);
-                // Q = dY X^T
-                ok = wait_bar(x_full, i & 1, abort_flag) && wait_bar(&y_full[i & 1], (i >> 1) & 1, abort_flag) && wait_bar(r_free, i & 1, abort_flag);
-                if (!ok) break;
-                tc_fence_after();
+                for (int i = 0; i < units && ok; ++i) {
+                    // or the sums below are all formed ahead, in more registers than there are
+                    asm volatile("" : "+r"(b), "+r"(c), "+r"(y), "+r"(x), "+r"(yr), "+r"(pm), "+r"(h0), "+r"(h1), "+r"(g0), "+r"(g1));
+                    const uint32_t y2 = (i & 1) * ((kY1 - kY) >> 4);
+                    // C h
+                    if (i > 0) ok = wait_bar(&dx_done[(i - 1) & 1], ((i - 1) >> 1) & 1, abort_flag);  // the work region is read
+                    ok = ok && wait_bar(h_full, i & 1, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < 4; ++k) mma<kTokenHi, kTokenHi>(tmem + kColR, y + y2 + cstep(k), x + cstep(k), idQ, k > 0);
-                mma_commit(q_full);
-                // (L o S)^T dY and B g'
-                ok = wait_bar(g_full, i & 1, abort_flag) && wait_bar(p_ready, i & 1, abort_flag);
-                if (!ok) break;
-                tc_fence_after();
+                    for (int k = 0; k < K / 16; ++k) {
+                        mma<kTokenHi, kStateRowsHi<K>>(tmem + kColR, c + cstep(k), h0 + srstep(k), idH, k > 0);
+                        mma<kTokenHi, kStateRowsHi<K>>(tmem + kColR, c + cstep(k), h1 + srstep(k), idH, true);
+                    }
+                    mma_commit(ch_full);
+                    // Q = dY X^T
+                    ok = wait_bar(x_full, i & 1, abort_flag) && wait_bar(&y_full[i & 1], (i >> 1) & 1, abort_flag) && wait_bar(r_free, i & 1, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < 8; ++k) mma<kTokenHi, kTokenHi>(tmem + kColR, pm + rstep(k), yr + y2 + rstep(k), idX, k > 0);
+                    for (int k = 0; k < 4; ++k) mma<kTokenHi, kTokenHi>(tmem + kColR, y + y2 + cstep(k), x + cstep(k), idQ, k > 0);
+                    mma_commit(q_full);
+                    // (L o S)^T dY and B g'
+                    ok = wait_bar(g_full, i & 1, abort_flag) && wait_bar(p_ready, i & 1, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < K / 16; ++k) {
-                    mma<kTokenHi, kStateRowsHi<K>>(tmem + kColR + 64, b + cstep(k), g0 + srstep(k), idH, k > 0);
-                    mma<kTokenHi, kStateRowsHi<K>>(tmem + kColR + 64, b + cstep(k), g1 + srstep(k), idH, true);
+                    for (int k = 0; k < 8; ++k) mma<kTokenHi, kTokenHi>(tmem + kColR, pm + rstep(k), yr + y2 + rstep(k), idX, k > 0);
+#pragma unroll
+                    for (int k = 0; k < K / 16; ++k) {
+                        mma<kTokenHi, kStateRowsHi<K>>(tmem + kColR + 64, b + cstep(k), g0 + srstep(k), idH, k > 0);
+                        mma<kTokenHi, kStateRowsHi<K>>(tmem + kColR + 64, b + cstep(k), g1 + srstep(k), idH, true);
+                    }
+                    mma_commit(dx_full);
                 }
-                mma_commit(dx_full);
+                if (!ok) fail();
             }
-            if (!ok) fail();
-        }
-    } else if (warp == 9) {  // dC and dB
-        if (lane == 0) {
-            const uint32_t sy = cols(sb + kSy), x = cols(sb + kX), h0 = state_cols<K>(sb + kH), h1 = state_cols<K>(sb + kH + kTile),
-                           g0 = state_cols<K>(sb + kG), g1 = state_cols<K>(sb + kG + kTile);
-            bool ok = true;
-            for (int i = 0; i < units && ok; ++i) {
-                // dC += (e^gam dY) h^T, dB += (delta e^{gam_C - gam} X) g'^T
-                ok = wait_bar(h_full, i & 1, abort_flag) && wait_bar(g_full, i & 1, abort_flag) && wait_bar(s_ready, i & 1, abort_flag);
-                if (!ok) break;
-                tc_fence_after();
+        } else if (warp == 9) {  // dC and dB
+            if (lane == 0) {
+                const uint32_t sy = cols(sb + kSy), x = cols(sb + kX), h0 = state_cols<K>(sb + kH), h1 = state_cols<K>(sb + kH + kTile),
+                               g0 = state_cols<K>(sb + kG), g1 = state_cols<K>(sb + kG + kTile);
+                bool ok = true;
+                for (int i = 0; i < units && ok; ++i) {
+                    // dC += (e^gam dY) h^T, dB += (delta e^{gam_C - gam} X) g'^T
+                    ok = wait_bar(h_full, i & 1, abort_flag) && wait_bar(g_full, i & 1, abort_flag) && wait_bar(s_ready, i & 1, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    mma<kTokenHi, kStateColsHi>(tmem + kColC, sy + cstep(k), h0 + scstep<K>(k), idO, i + k > 0);
-                    mma<kTokenHi, kStateColsHi>(tmem + kColB, x + cstep(k), g0 + scstep<K>(k), idO, i + k > 0);
-                    mma<kTokenHi, kStateColsHi>(tmem + kColC, sy + cstep(k), h1 + scstep<K>(k), idO, true);
-                    mma<kTokenHi, kStateColsHi>(tmem + kColB, x + cstep(k), g1 + scstep<K>(k), idO, true);
+                    for (int k = 0; k < 4; ++k) {
+                        mma<kTokenHi, kStateColsHi>(tmem + kColC, sy + cstep(k), h0 + scstep<K>(k), idO, i + k > 0);
+                        mma<kTokenHi, kStateColsHi>(tmem + kColB, x + cstep(k), g0 + scstep<K>(k), idO, i + k > 0);
+                        mma<kTokenHi, kStateColsHi>(tmem + kColC, sy + cstep(k), h1 + scstep<K>(k), idO, true);
+                        mma<kTokenHi, kStateColsHi>(tmem + kColB, x + cstep(k), g1 + scstep<K>(k), idO, true);
+                    }
+                    mma_commit(cd_full);
                 }
-                mma_commit(cd_full);
-            }
-            ok = ok && wait_bar(m_ready, 0, abort_flag);
-            if (ok) {
-                tc_fence_after();
-                const uint32_t mc = cols(sb + kPm), mr = rows(sb + kPm), b = rows(sb + kB), c = rows(sb + kCt);
+                ok = ok && wait_bar(m_ready, 0, abort_flag);
+                if (ok) {
+                    tc_fence_after();
+                    const uint32_t mc = cols(sb + kPm), mr = rows(sb + kPm), b = rows(sb + kB), c = rows(sb + kCt);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    mma<kTokenHi, kTokenHi>(tmem + kColC, mc + cstep(k), b + rstep(k), idC, true);
-                    mma<kTokenHi, kTokenHi>(tmem + kColB, mr + rstep(k), c + rstep(k), idB, true);
+                    for (int k = 0; k < 8; ++k) {
+                        mma<kTokenHi, kTokenHi>(tmem + kColC, mc + cstep(k), b + rstep(k), idC, true);
+                        mma<kTokenHi, kTokenHi>(tmem + kColB, mr + rstep(k), c + rstep(k), idB, true);
+                    }
+                    mma_commit(end_full);
                 }
-                mma_commit(end_full);
+                if (!ok) fail();
             }
-            if (!ok) fail();
-        }
-    } else if (warp == 10) {  // copies
-        if (lane == 0) {
-            auto tile_at = [&](int i) { return (((size_t)blockIdx.x * p.G + g) * p.U + u_first + i) * (K * kPT); };
-            auto load_pair = [&](int at, uint64_t *bar, const __nv_bfloat16 *hi, const __nv_bfloat16 *lo, int i) {
-                mbar_arrive_expect_tx(bar, 2 * kTile);
-                bulk_load(smem + at, hi + tile_at(i), kTile, bar);
-                bulk_load(smem + at + kTile, lo + tile_at(i), kTile, bar);
-            };
-            auto load_rows = [&](int at, uint64_t *bar, const CUtensorMap *map, int i) {
-                const int u = u_first + i;
-                mbar_arrive_expect_tx(bar, 16384);
-                tma_load_3d(smem + at, map, bar, p.col0(u), p.head(g, u), t0);
-            };
-            mbar_arrive_expect_tx(cb_full, 2 * (K / 64) * 16384);
-            for (int j = 0; j < K / 64; ++j) {
-                tma_load_3d(smem + kCt + j * 16384, &tm_c, cb_full, 64 * j, g, t0);
-                tma_load_3d(smem + kB + j * 16384, &tm_b, cb_full, 64 * j, g, t0);
-            }
-            int hs = 1, gs = 1, xs = 1, ys = 1;  // loads issued
-            load_pair(kH, h_full, q.h_hi, q.h_lo, 0);
-            load_rows(kX, x_full, &tm_x, 0);
-            load_rows(kY, &y_full[0], &tm_dy, 0);
-            if (units > 1) load_rows(kY1, &y_full[1], &tm_dy, 1), ++ys;
-            load_pair(kG, g_full, q.g_hi, q.g_lo, 0);
-            bool ok = true;
-            for (int i = 0; i < units && ok; ++i) {
-                const bool more = i + 1 < units;
-                ok = wait_bar(cd_full, i & 1, abort_flag);
-                if (ok && more) load_rows(kX, x_full, &tm_x, i + 1), ++xs;
-                ok = ok && wait_bar(hg_read, i & 1, abort_flag);
-                if (ok && more) load_pair(kH, h_full, q.h_hi, q.h_lo, i + 1), ++hs;
-                ok = ok && wait_bar(dx_full, i & 1, abort_flag);
-                if (ok && more) load_pair(kG, g_full, q.g_hi, q.g_lo, i + 1), ++gs;
-                ok = ok && wait_bar(&dx_done[i & 1], (i >> 1) & 1, abort_flag);
-                if (!ok) break;
-                const int y = i & 1 ? kY1 : kY;
-                if (full_chunk) {  // dx stands in dY's tile
+        } else if (warp == 10) {  // copies
+            if (lane == 0) {
+                auto tile_at = [&](int i) { return (((size_t)blockIdx.x * p.G + g) * p.U + u_first + i) * (K * kPT); };
+                auto load_pair = [&](int at, uint64_t *bar, const __nv_bfloat16 *hi, const __nv_bfloat16 *lo, int i) {
+                    mbar_arrive_expect_tx(bar, 2 * kTile);
+                    bulk_load(smem + at, hi + tile_at(i), kTile, bar);
+                    bulk_load(smem + at + kTile, lo + tile_at(i), kTile, bar);
+                };
+                auto load_rows = [&](int at, uint64_t *bar, const CUtensorMap *map, int i) {
                     const int u = u_first + i;
-                    tma_store_3d(&tm_dx, sb + y, p.col0(u), p.head(g, u), t0);
-                    bulk_commit();
-                    bulk_wait_read<0>();
+                    mbar_arrive_expect_tx(bar, 16384);
+                    tma_load_3d(smem + at, map, bar, p.col0(u), p.head(g, u), t0);
+                };
+                mbar_arrive_expect_tx(cb_full, 2 * (K / 64) * 16384);
+                for (int j = 0; j < K / 64; ++j) {
+                    tma_load_3d(smem + kCt + j * 16384, &tm_c, cb_full, 64 * j, g, t0);
+                    tma_load_3d(smem + kB + j * 16384, &tm_b, cb_full, 64 * j, g, t0);
                 }
-                if (i + 2 < units) load_rows(y, &y_full[i & 1], &tm_dy, i + 2), ++ys;
+                int hs = 1, gs = 1, xs = 1, ys = 1;  // loads issued
+                load_pair(kH, h_full, q.h_hi, q.h_lo, 0);
+                load_rows(kX, x_full, &tm_x, 0);
+                load_rows(kY, &y_full[0], &tm_dy, 0);
+                if (units > 1) load_rows(kY1, &y_full[1], &tm_dy, 1), ++ys;
+                load_pair(kG, g_full, q.g_hi, q.g_lo, 0);
+                bool ok = true;
+                for (int i = 0; i < units && ok; ++i) {
+                    const bool more = i + 1 < units;
+                    ok = wait_bar(cd_full, i & 1, abort_flag);
+                    if (ok && more) load_rows(kX, x_full, &tm_x, i + 1), ++xs;
+                    ok = ok && wait_bar(hg_read, i & 1, abort_flag);
+                    if (ok && more) load_pair(kH, h_full, q.h_hi, q.h_lo, i + 1), ++hs;
+                    ok = ok && wait_bar(dx_full, i & 1, abort_flag);
+                    if (ok && more) load_pair(kG, g_full, q.g_hi, q.g_lo, i + 1), ++gs;
+                    ok = ok && wait_bar(&dx_done[i & 1], (i >> 1) & 1, abort_flag);
+                    if (!ok) break;
+                    const int y = i & 1 ? kY1 : kY;
+                    if (full_chunk) {  // dx stands in dY's tile
+                        const int u = u_first + i;
+                        tma_store_3d(&tm_dx, sb + y, p.col0(u), p.head(g, u), t0);
+                        bulk_commit();
+                        bulk_wait_read<0>();
+                    }
+                    if (i + 2 < units) load_rows(y, &y_full[i & 1], &tm_dy, i + 2), ++ys;
+                }
+                if (!ok) fail();
+                // no copy outlives the CTA
+                bool done = drain(cb_full, 0);
+                done = drain(h_full, (hs - 1) & 1) && done;
+                done = drain(g_full, (gs - 1) & 1) && done;
+                done = drain(x_full, (xs - 1) & 1) && done;
+                done = drain(&y_full[0], ((ys + 1) / 2 - 1) & 1) && done;
+                if (ys > 1) done = drain(&y_full[1], (ys / 2 - 1) & 1) && done;
+                if (!done) fail();
+                bulk_wait_all();
             }
-            if (!ok) fail();
-            // no copy outlives the CTA
-            bool done = drain(cb_full, 0);
-            done = drain(h_full, (hs - 1) & 1) && done;
-            done = drain(g_full, (gs - 1) & 1) && done;
-            done = drain(x_full, (xs - 1) & 1) && done;
-            done = drain(&y_full[0], ((ys + 1) / 2 - 1) & 1) && done;
-            if (ys > 1) done = drain(&y_full[1], (ys / 2 - 1) & 1) && done;
-            if (!done) fail();
-            bulk_wait_all();
         }
-    }
     } else {
         reg_inc<kRowRegs>();
         const int wr = warp & 3, half = warp >> 2, row = wr * 32 + lane;  // row block, column half

@@ -111,130 +111,130 @@ scan_out_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant_
     };
 
     if (warp >= 16) {
-    reg_dec<kAuxRegs>();
-    if (warp == 16) {  // products
-        if (lane == 0) {
-            bool ok = wait_bar(cb_full, 0, abort_flag);
-            tc_fence_after();
-            const uint32_t c = cols(sb + kCt);
-            if (ok) {
-                constexpr uint32_t id = idesc_bf16(128, 128, false, false);
-                const uint32_t b = cols(sb + kP);
-#pragma unroll
-                for (int k = 0; k < K / 16; ++k) mma<kTokenHi, kTokenHi>(tmem + kColS, c + cstep(k), b + cstep(k), id, k > 0);
-                mma_commit(s_full);
-            }
-            constexpr uint32_t id = idesc_bf16(128, 64, false, true);
-            for (int i = 0; i < units && ok; ++i) {
-                const uint32_t d = tmem + kColY + (i & 1) * kYCols, h = state_rows(sb + kHt + (i & 1) * 16384);
-                if (i > 1) ok = wait_bar(&y_done[(i - 2) % 3], ((i - 2) / 3) & 1, abort_flag);  // its accumulators are read
-                ok = ok && wait_bar(&h_full[i & 1], (i >> 1) & 1, abort_flag);
-                if (!ok) break;
+        reg_dec<kAuxRegs>();
+        if (warp == 16) {  // products
+            if (lane == 0) {
+                bool ok = wait_bar(cb_full, 0, abort_flag);
                 tc_fence_after();
+                const uint32_t c = cols(sb + kCt);
+                if (ok) {
+                    constexpr uint32_t id = idesc_bf16(128, 128, false, false);
+                    const uint32_t b = cols(sb + kP);
 #pragma unroll
-                for (int k = 0; k < K / 16; ++k) mma<kTokenHi, kStateRowsHi<K>>(d + 64, c + cstep(k), h + srstep(k), id, k > 0);
-                if (LOCAL) {
-                    const uint32_t hs = state_rows(sb + kHs + (i & 1) * 16384);
-#pragma unroll
-                    for (int k = 0; k < K / 16; ++k) mma<kTokenHi, kStateRowsHi<K>>(d + 128, c + cstep(k), hs + srstep(k), id, k > 0);
+                    for (int k = 0; k < K / 16; ++k) mma<kTokenHi, kTokenHi>(tmem + kColS, c + cstep(k), b + cstep(k), id, k > 0);
+                    mma_commit(s_full);
                 }
-                ok = wait_bar(&x_full[i % 3], (i / 3) & 1, abort_flag) && wait_bar(&p_ready[i & 1], (i >> 1) & 1, abort_flag);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t pm = cols(sb + kP + ((i >> p.sh) & 1) * 32768), x = rows(sb + kX + i % 3 * 16384);
+                constexpr uint32_t id = idesc_bf16(128, 64, false, true);
+                for (int i = 0; i < units && ok; ++i) {
+                    const uint32_t d = tmem + kColY + (i & 1) * kYCols, h = state_rows(sb + kHt + (i & 1) * 16384);
+                    if (i > 1) ok = wait_bar(&y_done[(i - 2) % 3], ((i - 2) / 3) & 1, abort_flag);  // its accumulators are read
+                    ok = ok && wait_bar(&h_full[i & 1], (i >> 1) & 1, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < 8; ++k) mma<kTokenHi, kTokenHi>(d, pm + cstep(k), x + rstep(k), id, k > 0);
-                mma_commit(&y_full[i & 1]);
-            }
-            if (!ok) fail();
-        }
-    } else if (warp == 17) {  // copies
-        if (lane == 0) {
-            auto load_x = [&](int i) {
-                const int u = u_first + i;
-                mbar_arrive_expect_tx(&x_full[i % 3], 16384);
-                tma_load_3d(smem + kX + i % 3 * 16384, &tm_x, &x_full[i % 3], p.col0(u), p.head(g, u), t0);
-            };
-            auto load_h = [&](int i) {
-                mbar_arrive_expect_tx(&h_full[i & 1], (LOCAL ? 2 : 1) * K * kPT * 2);
-                if (LOCAL)
-                    bulk_load(smem + kHs + (i & 1) * 16384, q.locals.starts + ((seg_slot * p.G + g) * p.U + u_first + i) * (K * kPT), K * kPT * 2,
-                              &h_full[i & 1]);
-                bulk_load(smem + kHt + (i & 1) * 16384, q.tiles + (((size_t)blockIdx.x * p.G + g) * p.U + u_first + i) * (K * kPT),
-                          K * kPT * 2, &h_full[i & 1]);
-            };
-            mbar_arrive_expect_tx(cb_full, 2 * (K / 64) * 16384);
-            for (int j = 0; j < K / 64; ++j) {
-                tma_load_3d(smem + kCt + j * 16384, &tm_c, cb_full, 64 * j, g, t0);
-                tma_load_3d(smem + kP + j * 16384, &tm_b, cb_full, 64 * j, g, t0);
-            }
-            int xs = 0, hs = 0;  // loads issued
-            while (xs < min(units, 3)) load_x(xs++);
-            while (hs < min(units, 2)) load_h(hs++);
-            bool ok = true;
-            for (int i = 0; i < units && ok; ++i) {
-                ok = wait_bar(&y_full[i & 1], (i >> 1) & 1, abort_flag);
-                if (ok && hs < units) load_h(hs++);  // the products have read h
-                ok = ok && wait_bar(&y_done[i % 3], (i / 3) & 1, abort_flag);  // y stands in x's tile (or is written)
-                if (!ok) break;
-                if (full_chunk) {
-                    const int u = u_first + i;
-                    tma_store_3d(&tm_y, sb + kX + i % 3 * 16384, p.col0(u), p.head(g, u), t0);
-                    bulk_commit();
-                    bulk_wait_read<0>();
-                }
-                if (xs < units) load_x(xs++);
-            }
-            if (!ok) fail();
-            // no copy outlives the CTA
-            bool done = drain(cb_full, 0);
-            for (int k = max(0, xs - 3); k < xs; ++k) done = drain(&x_full[k % 3], (k / 3) & 1) && done;
-            for (int k = max(0, hs - 2); k < hs; ++k) done = drain(&h_full[k & 1], (k >> 1) & 1) && done;
-            if (!done) fail();
-            bulk_wait_all();
-        }
-    } else {  // warps 18, 19: the heads' column factors, a head ahead of the mask
-        const int w2 = warp - 18;
-        bool ok = true;
-        for (int i = 0; i < units; i += p.S) {
-            const int hb = (i >> p.sh) & 1, h = p.head(g, u_first + i);
-            const float *gt = p.gates.at(blockIdx.x, p.H, h);
-            const float4 tot = p.gates.totals(blockIdx.x, p.H, h);
-            const float t[4] = {tot.x, tot.y, tot.z, tot.w};
-            const float D = p.D ? p.D[h] : 0.f, f = LOCAL ? q.locals.before[(size_t)blockIdx.x * p.H + h] : 0.f;
-            float gd[2], gf[2], gr[2];
+                    for (int k = 0; k < K / 16; ++k) mma<kTokenHi, kStateRowsHi<K>>(d + 64, c + cstep(k), h + srstep(k), id, k > 0);
+                    if (LOCAL) {
+                        const uint32_t hs = state_rows(sb + kHs + (i & 1) * 16384);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int row = (w2 * 2 + k) * 32 + lane;
-                gd[k] = gt[row], gf[k] = gt[kC + row], gr[k] = gt[2 * kC + row];
-            }
-            // the factors of two heads before are read
-            const int j = i >> p.sh;
-            if (j >= 2) ok = __all_sync(0xffffffffu, ok && wait_bar(&v_free[hb], ((j - 2) >> 1) & 1, abort_flag));
-            Vec &vec = reinterpret_cast<Vec *>(smem + kVec)[hb];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int wr = w2 * 2 + k, row = wr * 32 + lane;
-                vec.gl[row] = gf[k];
-                vec.col[wr][row] = gd[k];
-                float before, after, all;
-                around(tot, wr, &before, &after, &all);
-                vec.row[0][row] = ex2(before + gf[k]);
-                if (LOCAL) vec.row[1][row] = ex2(f + before + gf[k]);
-                vec.row[2][row] = ex2(gf[k]);
-                vec.row[3][row] = D;
-                float to = gr[k];
-#pragma unroll
-                for (int w = 1; w < 4; ++w)
-                    if (w > wr) {
-                        vec.col[w][row] = ex2(to) * gd[k];
-                        to += t[w];
+                        for (int k = 0; k < K / 16; ++k) mma<kTokenHi, kStateRowsHi<K>>(d + 128, c + cstep(k), hs + srstep(k), id, k > 0);
                     }
+                    ok = wait_bar(&x_full[i % 3], (i / 3) & 1, abort_flag) && wait_bar(&p_ready[i & 1], (i >> 1) & 1, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t pm = cols(sb + kP + ((i >> p.sh) & 1) * 32768), x = rows(sb + kX + i % 3 * 16384);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) mma<kTokenHi, kTokenHi>(d, pm + cstep(k), x + rstep(k), id, k > 0);
+                    mma_commit(&y_full[i & 1]);
+                }
+                if (!ok) fail();
             }
-            mbar_arrive(&v_full[hb]);
+        } else if (warp == 17) {  // copies
+            if (lane == 0) {
+                auto load_x = [&](int i) {
+                    const int u = u_first + i;
+                    mbar_arrive_expect_tx(&x_full[i % 3], 16384);
+                    tma_load_3d(smem + kX + i % 3 * 16384, &tm_x, &x_full[i % 3], p.col0(u), p.head(g, u), t0);
+                };
+                auto load_h = [&](int i) {
+                    mbar_arrive_expect_tx(&h_full[i & 1], (LOCAL ? 2 : 1) * K * kPT * 2);
+                    if (LOCAL)
+                        bulk_load(smem + kHs + (i & 1) * 16384, q.locals.starts + ((seg_slot * p.G + g) * p.U + u_first + i) * (K * kPT), K * kPT * 2,
+                                  &h_full[i & 1]);
+                    bulk_load(smem + kHt + (i & 1) * 16384, q.tiles + (((size_t)blockIdx.x * p.G + g) * p.U + u_first + i) * (K * kPT),
+                              K * kPT * 2, &h_full[i & 1]);
+                };
+                mbar_arrive_expect_tx(cb_full, 2 * (K / 64) * 16384);
+                for (int j = 0; j < K / 64; ++j) {
+                    tma_load_3d(smem + kCt + j * 16384, &tm_c, cb_full, 64 * j, g, t0);
+                    tma_load_3d(smem + kP + j * 16384, &tm_b, cb_full, 64 * j, g, t0);
+                }
+                int xs = 0, hs = 0;  // loads issued
+                while (xs < min(units, 3)) load_x(xs++);
+                while (hs < min(units, 2)) load_h(hs++);
+                bool ok = true;
+                for (int i = 0; i < units && ok; ++i) {
+                    ok = wait_bar(&y_full[i & 1], (i >> 1) & 1, abort_flag);
+                    if (ok && hs < units) load_h(hs++);  // the products have read h
+                    ok = ok && wait_bar(&y_done[i % 3], (i / 3) & 1, abort_flag);  // y stands in x's tile (or is written)
+                    if (!ok) break;
+                    if (full_chunk) {
+                        const int u = u_first + i;
+                        tma_store_3d(&tm_y, sb + kX + i % 3 * 16384, p.col0(u), p.head(g, u), t0);
+                        bulk_commit();
+                        bulk_wait_read<0>();
+                    }
+                    if (xs < units) load_x(xs++);
+                }
+                if (!ok) fail();
+                // no copy outlives the CTA
+                bool done = drain(cb_full, 0);
+                for (int k = max(0, xs - 3); k < xs; ++k) done = drain(&x_full[k % 3], (k / 3) & 1) && done;
+                for (int k = max(0, hs - 2); k < hs; ++k) done = drain(&h_full[k & 1], (k >> 1) & 1) && done;
+                if (!done) fail();
+                bulk_wait_all();
+            }
+        } else {  // warps 18, 19: the heads' column factors, a head ahead of the mask
+            const int w2 = warp - 18;
+            bool ok = true;
+            for (int i = 0; i < units; i += p.S) {
+                const int hb = (i >> p.sh) & 1, h = p.head(g, u_first + i);
+                const float *gt = p.gates.at(blockIdx.x, p.H, h);
+                const float4 tot = p.gates.totals(blockIdx.x, p.H, h);
+                const float t[4] = {tot.x, tot.y, tot.z, tot.w};
+                const float D = p.D ? p.D[h] : 0.f, f = LOCAL ? q.locals.before[(size_t)blockIdx.x * p.H + h] : 0.f;
+                float gd[2], gf[2], gr[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int row = (w2 * 2 + k) * 32 + lane;
+                    gd[k] = gt[row], gf[k] = gt[kC + row], gr[k] = gt[2 * kC + row];
+                }
+                // the factors of two heads before are read
+                const int j = i >> p.sh;
+                if (j >= 2) ok = __all_sync(0xffffffffu, ok && wait_bar(&v_free[hb], ((j - 2) >> 1) & 1, abort_flag));
+                Vec &vec = reinterpret_cast<Vec *>(smem + kVec)[hb];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int wr = w2 * 2 + k, row = wr * 32 + lane;
+                    vec.gl[row] = gf[k];
+                    vec.col[wr][row] = gd[k];
+                    float before, after, all;
+                    around(tot, wr, &before, &after, &all);
+                    vec.row[0][row] = ex2(before + gf[k]);
+                    if (LOCAL) vec.row[1][row] = ex2(f + before + gf[k]);
+                    vec.row[2][row] = ex2(gf[k]);
+                    vec.row[3][row] = D;
+                    float to = gr[k];
+#pragma unroll
+                    for (int w = 1; w < 4; ++w)
+                        if (w > wr) {
+                            vec.col[w][row] = ex2(to) * gd[k];
+                            to += t[w];
+                        }
+                }
+                mbar_arrive(&v_full[hb]);
+            }
+            if (!ok) fail();
         }
-        if (!ok) fail();
-    }
     } else {
         reg_inc<kRowRegs>();
         const int wr = warp & 3, qd = warp >> 2, row = wr * 32 + lane;  // row block, column quarter

@@ -174,51 +174,51 @@ scan_state_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constan
     };
 
     if (warp >= 16) {  // (the register split stands inside the roles: what follows a join keeps the smaller share)
-    reg_dec<kAuxRegs>();
-    if (warp == 16) {
-        if (lane == 0) {
-            const int nx = u0 + 1 < p.U ? 2 : 1;
-            bool ok = true;
-            int i = 0;
-            for (; i < chunks && ok; ++i) {
-                const int st = i & 1, t0 = seg_begin + chunk_at(i) * kC;
-                if (i >= 2) ok = wait_bar(&empty[st], ((i >> 1) - 1) & 1, abort_flag);
-                if (!ok) break;
-                uint8_t *dst = smem + st * kStage;
-                mbar_arrive_expect_tx(&full[st], (K / 64 + nx) * 16384);
-                for (int j = 0; j < K / 64; ++j) tma_load_3d(dst + j * 16384, &tm_b, &full[st], 64 * j, g, t0);
-                for (int j = 0; j < nx; ++j)
-                    tma_load_3d(dst + 32768 + j * 16384, &tm_x, &full[st], p.col0(u0 + j), p.head(g, u0 + j), t0);
-            }
-            if (!ok) fail();
-            // no copy outlives the CTA: the last two stages issued are waited for
-            for (int k = max(0, i - 2); k < i; ++k)
-                if (!drain(&full[k & 1], (k >> 1) & 1)) fail();
-        }
-    } else if (warp == 17) {
-        if (lane == 0) {
-            const uint32_t id = idesc_bf16(128, 128, true, true);
-            bool ok = true;
-            for (int i = 0; i < chunks && ok; ++i) {
-                ok = wait_bar(xs_ready, i & 1, abort_flag);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t st = sb + (i & 1) * kStage, d = tmem + (i & 1) * 128;
-                const uint32_t a = rows(st), hi = rows(st + 32768), md = rows(sb + kMid), lo = rows(sb + kMid + 32768);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    mma<kTokenHi, kTokenHi>(d, a + rstep(k), md + rstep(k), id, k > 0);
-                    mma<kTokenHi, kTokenHi>(d, a + rstep(k), lo + rstep(k), id, true);
+        reg_dec<kAuxRegs>();
+        if (warp == 16) {
+            if (lane == 0) {
+                const int nx = u0 + 1 < p.U ? 2 : 1;
+                bool ok = true;
+                int i = 0;
+                for (; i < chunks && ok; ++i) {
+                    const int st = i & 1, t0 = seg_begin + chunk_at(i) * kC;
+                    if (i >= 2) ok = wait_bar(&empty[st], ((i >> 1) - 1) & 1, abort_flag);
+                    if (!ok) break;
+                    uint8_t *dst = smem + st * kStage;
+                    mbar_arrive_expect_tx(&full[st], (K / 64 + nx) * 16384);
+                    for (int j = 0; j < K / 64; ++j) tma_load_3d(dst + j * 16384, &tm_b, &full[st], 64 * j, g, t0);
+                    for (int j = 0; j < nx; ++j)
+                        tma_load_3d(dst + 32768 + j * 16384, &tm_x, &full[st], p.col0(u0 + j), p.head(g, u0 + j), t0);
                 }
-                mma_commit(ml_free);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) mma<kTokenHi, kTokenHi>(d, a + rstep(k), hi + rstep(k), id, true);
-                mma_commit(&dfull[i & 1]);
-                mma_commit(&empty[i & 1]);
+                if (!ok) fail();
+                // no copy outlives the CTA: the last two stages issued are waited for
+                for (int k = max(0, i - 2); k < i; ++k)
+                    if (!drain(&full[k & 1], (k >> 1) & 1)) fail();
             }
-            if (!ok) fail();
+        } else if (warp == 17) {
+            if (lane == 0) {
+                const uint32_t id = idesc_bf16(128, 128, true, true);
+                bool ok = true;
+                for (int i = 0; i < chunks && ok; ++i) {
+                    ok = wait_bar(xs_ready, i & 1, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t st = sb + (i & 1) * kStage, d = tmem + (i & 1) * 128;
+                    const uint32_t a = rows(st), hi = rows(st + 32768), md = rows(sb + kMid), lo = rows(sb + kMid + 32768);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        mma<kTokenHi, kTokenHi>(d, a + rstep(k), md + rstep(k), id, k > 0);
+                        mma<kTokenHi, kTokenHi>(d, a + rstep(k), lo + rstep(k), id, true);
+                    }
+                    mma_commit(ml_free);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) mma<kTokenHi, kTokenHi>(d, a + rstep(k), hi + rstep(k), id, true);
+                    mma_commit(&dfull[i & 1]);
+                    mma_commit(&empty[i & 1]);
+                }
+                if (!ok) fail();
+            }
         }
-    }
     } else {
         reg_inc<kRowRegs>();
         float st[kHalf];  // this thread's part of the state
