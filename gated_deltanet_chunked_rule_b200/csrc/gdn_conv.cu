@@ -291,8 +291,8 @@ conv_bwd_kernel(ConvP p, const T *__restrict__ x, const T *__restrict__ weight, 
         auto final_part = [&](int t) {
             P f;
             f.zero();
-            if (dfinal && t >= max(t0, s) && t < t1 && t >= e - (W - 1))
-                f.load(dfinal + ((size_t)n * (W - 1) + (W - 1 - (e - t))) * p.C + c);
+            const long long k = kept_row(n, e, t, W - 1);
+            if (dfinal && t >= max(t0, s) && t < t1 && k >= 0) f.load(dfinal + (size_t)k * p.C + c);
             return f;
         };
         auto emit = [&](int t, const P &v) {  // token t is finished, if it is of this sequence and run

@@ -21,11 +21,11 @@ struct SeqMap {
     const int *cu;  // nullptr: no packing
     int N, T, total;
 
-    __device__ __forceinline__ int begin(int n) const {
+    __host__ __device__ __forceinline__ int begin(int n) const {
         if (!cu) return n * T;
         return min(max(cu[n], 0), total);
     }
-    __device__ __forceinline__ int end(int n) const {
+    __host__ __device__ __forceinline__ int end(int n) const {
         if (!cu) return (n + 1) * T;
         return max(begin(n), min(max(cu[n + 1], 0), total));
     }
@@ -200,6 +200,12 @@ size_t conv_part_bytes(int total, int C, int W);
 cudaError_t launch_conv_fwd(const ConvArgs &a);
 cudaError_t launch_conv_bwd(const ConvArgs &a);
 cudaError_t launch_conv_update(const ConvArgs &a);  // state in place, seq without packing
+
+// Row of the states [N, w1, C] that holds token t of sequence n, which ends at e: one of the last w1
+// before e, or -1. (Where the offsets end early, the last sequence is walked on behind its e.)
+__host__ __device__ __forceinline__ long long kept_row(int n, int e, int t, int w1) {
+    return t < e && t >= e - w1 ? (long long)n * w1 + w1 - (e - t) : -1;
+}
 
 // ----------------------------------------------------------------- layer norm
 struct NormArgs {
