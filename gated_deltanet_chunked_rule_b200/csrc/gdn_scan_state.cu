@@ -127,6 +127,8 @@ scan_state_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constan
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 8);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
+    // the backward's first kernel where the forward's gates are kept; warps 18 and 19 have no other work
+    if (REVERSE && blockIdx.x == 0 && blockIdx.y == 0 && warp >= 18) check_cu(p.m, p.status, tid - 18 * 32, 64);
     int n, local;
     const bool used = p.m.slot(blockIdx.x, q.seg_tokens, &n, &local);
     const int s_begin = p.m.begin(n), s_len = p.m.end(n) - s_begin;

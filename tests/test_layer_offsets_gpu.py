@@ -56,3 +56,35 @@ def test_convolution_padded_at_its_end(gdn, dtype, C, W, T, cu):
     base = 2.0 ** -18 if dtype == "bf16" else 0
     for name, got, ops in (("dx", dx[0], 16), ("dweight", dw, T), ("dbias", db, T), ("dstate", ds, 16)):
         R.close(name, got, ref[name], mass[name], base + (16 + ops) * 2.0 ** -24)
+
+
+def scan_inputs(T, N, dtype, seed):
+    g = torch.Generator().manual_seed(seed)
+
+    def r(*s, dt=dtype):
+        return torch.randn(s, generator=g).to(dt).cuda()
+
+    f = torch.float32
+    a = (r(1, T, 2, 64), r(1, T, 2), -r(2, dt=f).abs() - 0.1, r(1, T, 1, 128), r(1, T, 1, 128), r(2, dt=f), r(2, dt=f), True)
+    return a, r(N, 2, 128, 64, dt=f), r(1, T, 2, 64), r(N, 2, 128, 64, dt=f)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("keep", [True, False])
+@pytest.mark.parametrize("T,good", [(171, (0, 100, 171)), (1400, (0, 100, 1400))])
+def test_scan_gradients_report_offsets(gdn, dtype, keep, T, good):
+    # each call by itself: a forward on good offsets says nothing for the backward, whose offsets went bad
+    # after it (whole sequences, and sequences in segments)
+    a, h0, dy, dht = scan_inputs(T, 2, DT[dtype], T)
+    _, _, saved = gdn.chunk_selective_scan_fwd(*a, h0, True, offsets(*good), save_for_backward=keep)
+    want = gdn.chunk_selective_scan_bwd(*a, saved, dy, dht, h0, offsets(*good))
+    assert gdn.device_status() == 0
+    for cu in ((0, T + 9, T), (0, 100, T - 11), (0, -5, T), (3, 100, T)):
+        gdn.chunk_selective_scan_bwd(*a, saved, dy, dht, h0, offsets(*cu))
+        assert gdn.device_status() == BAD, cu
+        gdn.chunk_selective_scan_fwd(*a, h0, True, offsets(*cu))
+        assert gdn.device_status() == BAD, cu
+    again = gdn.chunk_selective_scan_bwd(*a, saved, dy, dht, h0, offsets(*good))
+    assert gdn.device_status() == 0
+    for p, q in zip(again, want):
+        assert torch.equal(p, q)
