@@ -463,6 +463,9 @@ conv_update_kernel(ConvP p, const T *__restrict__ x, const T *__restrict__ weigh
     for (int i = 0; i < W - 1; ++i) hist[i].store(st + (size_t)i * p.C);
 }
 
+// Of a call without tokens: the offsets' check alone.
+__global__ void __launch_bounds__(128) conv_offsets_kernel(SeqMap m, unsigned *status) { check_cu(m, status, threadIdx.x, 128); }
+
 // Blocks along the tokens (without the final states'): as many as run beside each other, with
 // runs of one length, or one wave more would stand half empty.
 int token_blocks(int total, unsigned column_blocks) {
@@ -479,9 +482,10 @@ cudaError_t run_pass(const ConvArgs &a, Pass pass) {
     const int share = token_blocks(a.seq.total, cb) * kWarps;
     p.run = std::max(kMinRun, ((a.seq.total + share - 1) / share + 7) / 8 * 8);
     p.runs = (a.seq.total + p.run - 1) / p.run;
+    if (a.seq.total == 0 && a.seq.cu) conv_offsets_kernel<<<1, 128, 0, a.stream>>>(a.seq, a.status);
     if (pass == kFwd) {
         const long long runs = (long long)p.runs + (a.final_state ? a.seq.N : 0);
-        if (runs == 0) return cudaSuccess;
+        if (runs == 0) return cudaGetLastError();
         conv_fwd_kernel<T, VEC, W><<<dim3((unsigned)((runs + kWarps - 1) / kWarps), cb), 32 * kWarps, 0, a.stream>>>(
             p, x, w, b, st, (T *)a.y, (T *)a.final_state, a.status);
     } else if (pass == kBwd) {

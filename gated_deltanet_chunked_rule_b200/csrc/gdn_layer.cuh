@@ -16,7 +16,7 @@ __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontr
 // Sequences on the flattened token axis: B rows of T tokens, or N packed ones whose
 // offsets stand in cu (device, [N + 1]). A kernel clamps what it reads from cu to
 // [0, total], so an inconsistent copy never leads out of the tensors; one block of
-// each call's first kernel checks it and records GDN_ERR_DEVICE_ARG.
+// each call's first kernel that walks the sequences checks it and records GDN_ERR_DEVICE_ARG.
 struct SeqMap {
     const int *cu;  // nullptr: no packing
     int N, T, total;

@@ -88,3 +88,20 @@ def test_scan_gradients_report_offsets(gdn, dtype, keep, T, good):
     assert gdn.device_status() == 0
     for p, q in zip(again, want):
         assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_no_tokens_report_offsets(gdn, dtype):
+    x, w = torch.empty(1, 0, 40, dtype=DT[dtype], device="cuda"), torch.zeros(40, 4, dtype=DT[dtype], device="cuda")
+    a, h0, dy, dht = scan_inputs(0, 2, DT[dtype], 1)
+    for cu, status in ((offsets(0, 5, 0), BAD), (offsets(0, 0, 0), 0)):
+        for final in (True, False):
+            gdn.causal_conv1d_fwd(x, w, None, None, None, final, cu)
+            assert gdn.device_status() == status
+        gdn.causal_conv1d_bwd(x, w, None, x, None, None, None, cu)
+        assert gdn.device_status() == status
+        _, _, saved = gdn.chunk_selective_scan_fwd(*a, h0, True, cu, save_for_backward=True)
+        assert gdn.device_status() == status
+        for kept in (saved, None):
+            gdn.chunk_selective_scan_bwd(*a, kept, dy, dht, h0, cu)
+            assert gdn.device_status() == status
