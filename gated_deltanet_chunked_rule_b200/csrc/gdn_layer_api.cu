@@ -245,6 +245,7 @@ int gdn_conv_update(const gdn_conv_problem *p, const void *x, const void *weight
     if (rc != GDN_OK) return rc;
     if (p->num_seqs || !weight || !state || (a.seq.total && (!x || !y))) return GDN_ERR_INVALID_ARG;
     if (!all_aligned16({x, weight, bias, state, y})) return GDN_ERR_INVALID_ARG;
+    if (over_input({y}, {x, weight, bias, state}) || over_input({state}, {x, weight, bias})) return GDN_ERR_INVALID_ARG;
     a.x = x, a.weight = weight, a.bias = bias, a.state = state, a.y = y;
     a.stream = (cudaStream_t)stream;
     TimedLaunch t("conv_update", a.stream);
@@ -304,6 +305,8 @@ int gdn_scan_step(const gdn_scan_problem *p, const void *x, const void *dt, cons
     if (rc != GDN_OK) return rc;
     if (a.seq.total && !y) return GDN_ERR_INVALID_ARG;
     if (!all_aligned16({y, final_state})) return GDN_ERR_INVALID_ARG;
+    if (over_input({y}, {x, dt, A, B, C, D, dt_bias, h0, final_state}) || over_input({final_state}, {x, dt, A, B, C, D, dt_bias}))
+        return GDN_ERR_INVALID_ARG;  // (h0 may be updated in place)
     a.y = y, a.final_state = final_state;
     if (!(a.status = status_ptr())) return GDN_ERR_CUDA;
     TimedLaunch t("scan_step", a.stream);
