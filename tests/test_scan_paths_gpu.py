@@ -1,0 +1,146 @@
+"""The scan's CUDA-core path for both types, judged by the stretches of tokens that it sums over; long
+sequences; and calls in a row.
+
+Tolerances as in test_scan_gpu.py: of the terms' mass, every fp32 operation in sequence, (T + 512 + 17 * 128)
+2^-24, and a sum over T tokens T 2^-24 more. The CUDA-core kernels round nothing to bf16 but the results, for
+bf16 tensors too, and start the sum behind the gates' gradients anew every 16 tokens: the masses are those of
+16 tokens."""
+import pytest
+import torch
+
+import layer_ref as R
+import test_scan_gpu as S
+
+pytestmark = pytest.mark.gpu
+DT = S.DT
+
+
+@pytest.fixture(scope="module")
+def gdn():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from gated_deltanet_chunked_rule_b200 import build
+    build.build()
+    import gated_deltanet_chunked_rule_b200 as g
+    return g
+
+
+def verify(v, lens, softplus, got):
+    ref, mass = S.reference(v, lens, softplus, keep=16)
+    base = (max(lens, default=0) + 512 + 17 * 128) * 2.0 ** -24
+    for k, t in got.items():
+        if t is not None:
+            R.close(k, t.reshape(ref[k].shape), ref[k], mass[k], base + (sum(lens) * 2.0 ** -24 if k in ("dA", "dD", "ddt_bias") else 0))
+
+
+FORMS = [("fp32", "fp32"), ("bf16", "fp32"), ("bf16", "bf16")]
+
+
+@pytest.mark.parametrize("dtype,dt_dtype", FORMS)
+@pytest.mark.parametrize("K,P", [(64, 64), (128, 64), (64, 128)])
+@pytest.mark.parametrize("lens", [[1], [16, 17], [0, 5, 0, 130, 1, 0], [300], [700]])
+def test_on_cuda_cores(gdn, monkeypatch, dtype, dt_dtype, K, P, lens):
+    monkeypatch.setenv("GDN_IMPL", "simt")
+    v = S.make(lens, 4, 2, K, P, DT[dtype], DT[dt_dtype], seed=K + sum(lens))
+    got = S.train(gdn, v)
+    verify(v, lens, True, got)
+    again = S.train(gdn, v, save=False)
+    for k in got:
+        assert torch.equal(got[k], again[k]), k
+
+
+@pytest.mark.parametrize("dtype,dt_dtype", FORMS)
+@pytest.mark.parametrize("form", ["bare", "D", "bias", "h0", "linear"])
+def test_forms_on_cuda_cores(gdn, monkeypatch, dtype, dt_dtype, form):
+    monkeypatch.setenv("GDN_IMPL", "simt")
+    v = S.make([200, 70], 2, 1, 128, 64, DT[dtype], DT[dt_dtype], 7, D=form == "D", bias=form in ("bias", "linear"), h0=form == "h0",
+               slices=True)
+    if form == "linear":
+        v["dt"] = (v["dt"] * 0.05).to(v["dt"].dtype)
+        v["dt_bias"] = v["dt_bias"].abs() * 0 + 0.3
+    verify(v, [200, 70], form != "linear", S.train(gdn, v, form != "linear"))
+
+
+def test_kept_states_are_those_of_the_path(gdn, monkeypatch):
+    # what one path kept is nothing to the other: refused where too short, recomputed where not needed
+    v = S.make([150], 2, 1, 64, 64, torch.bfloat16, seed=3)
+    a, rest = (*S.args(v), True), (v["dy"], v["dht"], v["h0"], v["cu"])
+    _, _, tc = gdn.chunk_selective_scan_fwd(*a, v["h0"], True, v["cu"], save_for_backward=True)
+    monkeypatch.setenv("GDN_IMPL", "simt")
+    _, _, simt = gdn.chunk_selective_scan_fwd(*a, v["h0"], True, v["cu"], save_for_backward=True)
+    assert simt.numel() == 0
+    for p, q in zip(gdn.chunk_selective_scan_bwd(*a, tc, *rest), gdn.chunk_selective_scan_bwd(*a, simt, *rest)):
+        assert torch.equal(p, q)
+    monkeypatch.delenv("GDN_IMPL")
+    with pytest.raises(ValueError, match="saved holds"):
+        gdn.chunk_selective_scan_bwd(*a, simt, *rest)
+
+
+def chunked(v, lens):
+    """The scan in 64 bits on the GPU in chunks of 64 tokens, the state carried from chunk to chunk."""
+    x, dt, A, B, C, D, bias = (t.double() if t is not None else None for t in S.args(v))
+    H, G = x.shape[2], B.shape[2]
+    h = v["h0"].double()[0]
+    raw = dt[0] + bias
+    delta = torch.clamp(raw, min=0) + torch.log1p(torch.exp(-raw.abs()))
+    mask = torch.ones(64, 64, dtype=torch.bool, device="cuda").tril()
+    ys = []
+    for t in range(0, lens[0], 64):
+        xs, dl = x[0, t:t + 64], delta[t:t + 64]
+        bs, cs = (w[0, t:t + 64].repeat_interleave(H // G, 1) for w in (B, C))
+        n = xs.shape[0]
+        gam = torch.cumsum(dl * A, 0).t()
+        L = torch.exp((gam[:, :, None] - gam[:, None]).masked_fill(~mask[:n, :n], -float("inf")))
+        w = xs * dl[..., None]
+        y = torch.einsum("hqs,shp->qhp", torch.einsum("qhk,shk->hqs", cs, bs) * L, w)
+        y = y + torch.einsum("qhk,hkp->qhp", cs, h) * torch.exp(gam).t()[..., None] + D[:, None] * xs
+        h = torch.exp(gam[:, -1])[:, None, None] * h + torch.einsum("shk,shp->hkp", bs * torch.exp(gam[:, -1:] - gam).t()[..., None], w)
+        ys.append(y)
+    return torch.cat(ys)[None], h[None]
+
+
+@pytest.mark.parametrize("dtype,T,H,split", [("bf16", 8229, 3, ""), ("bf16", 8229, 3, "segments"), ("bf16", 65536, 8, ""),
+                                             ("fp32", 8229, 2, "")])
+def test_long_sequences(gdn, monkeypatch, dtype, T, H, split):
+    """Of norms. bf16 results: half a step, 2^-8, for the rounding of the result and of one operand in each of its
+    two terms. fp32 results: the operations in sequence, whose roundings are independent, sqrt(T + 512 + 17 * 128)
+    2^-24, and 2^-16 for two-part operands; the gates' gradients pass through four such results (kept states, exit
+    gradients, their product, the sum)."""
+    if split:
+        monkeypatch.setenv("GDN_SCAN_SPLIT", split)
+    v = S.make([T], H, 1, 128, 64, DT[dtype], torch.float32, seed=T + H, slow=True)
+    got = S.train(gdn, v)
+    names = ("x", "dt", "A", "B", "C", "D", "dt_bias", "h0")
+    leaves = {k: v[k].double().requires_grad_() for k in names}
+    y, fin = chunked({**v, **leaves}, [T])
+    want = dict(zip(("dx", "ddt", "dA", "dB", "dC", "dD", "ddt_bias", "dh0"),
+                    torch.autograd.grad([y, fin], [leaves[k] for k in names], [v["dy"].double(), v["dht"].double()])))
+    want |= {"y": y.detach(), "final": fin.detach()}
+    fp32 = (T + 512 + 17 * 128) ** 0.5 * 2.0 ** -24 + (2.0 ** -16 if dtype == "bf16" else 0)
+    for k, t in got.items():
+        tol = 3 * 2.0 ** -8 if t.dtype == torch.bfloat16 else 4 * fp32
+        off = ((t.double() - want[k]).norm() / want[k].norm()).item()
+        print(k, f"{off:.2e} of {tol:.2e}")
+        assert off <= tol, (k, off, tol)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("H,lens", [(2, [2100]), (2, [700, 0, 1400]), (96, [130])])
+def test_backward_calls_in_a_row(gdn, dtype, H, lens):
+    # forward and backward after one another with no wait between, on the same memory
+    both = [S.make(lens, H, 1, 64, 64, DT[dtype], seed=s) for s in (41, 42)]
+
+    def call(v, save):
+        _, _, saved = gdn.chunk_selective_scan_fwd(*S.args(v), True, v["h0"], True, v["cu"], save_for_backward=save)
+        return gdn.chunk_selective_scan_bwd(*S.args(v), True, saved, v["dy"], v["dht"], v["h0"], v["cu"])
+
+    alone = []
+    for v in both:
+        alone.append(call(v, True))
+        torch.cuda.synchronize()
+    got = [call(both[i % 2], i % 3 > 0) for i in range(12)]
+    torch.cuda.synchronize()
+    assert gdn.device_status() == 0
+    for i, g in enumerate(got):
+        for p, q in zip(g, alone[i % 2]):
+            assert torch.equal(p, q), i
