@@ -474,8 +474,8 @@ int token_blocks(int total, unsigned column_blocks) {
 
 enum Pass { kFwd, kBwd, kUpdate };
 
-template <typename T, int VEC, int W>
-cudaError_t run_pass(const ConvArgs &a, Pass pass) {
+template <typename T, int VEC, int W, Pass PASS>
+cudaError_t run_pass(const ConvArgs &a) {
     ConvP p{a.seq, a.C, 0, 0, a.silu, a.x_stride};
     const T *x = (const T *)a.x, *w = (const T *)a.weight, *b = (const T *)a.bias, *st = (const T *)a.state;
     const unsigned cb = (unsigned)((a.C + 32 * VEC - 1) / (32 * VEC));
@@ -483,12 +483,12 @@ cudaError_t run_pass(const ConvArgs &a, Pass pass) {
     p.run = std::max(kMinRun, ((a.seq.total + share - 1) / share + 7) / 8 * 8);
     p.runs = (a.seq.total + p.run - 1) / p.run;
     if (a.seq.total == 0 && a.seq.cu) conv_offsets_kernel<<<1, 128, 0, a.stream>>>(a.seq, a.status);
-    if (pass == kFwd) {
+    if constexpr (PASS == kFwd) {
         const long long runs = (long long)p.runs + (a.final_state ? a.seq.N : 0);
         if (runs == 0) return cudaGetLastError();
         conv_fwd_kernel<T, VEC, W><<<dim3((unsigned)((runs + kWarps - 1) / kWarps), cb), 32 * kWarps, 0, a.stream>>>(
             p, x, w, b, st, (T *)a.y, (T *)a.final_state, a.status);
-    } else if (pass == kBwd) {
+    } else if constexpr (PASS == kBwd) {
         const T *dy = (const T *)a.dy, *df = (const T *)a.dfinal;
         const int blocks = (p.runs + kWarps - 1) / kWarps;
         if (blocks) {
@@ -515,22 +515,23 @@ bool vectorized(const ConvArgs &a) {
     return a.C % el == 0 && a.x_stride % el == 0;
 }
 
-template <typename T, int VEC>
-cudaError_t by_taps(const ConvArgs &a, Pass pass) {
+template <typename T, int VEC, Pass PASS>
+cudaError_t by_taps(const ConvArgs &a) {
     switch (a.W) {
-        case 2: return run_pass<T, VEC, 2>(a, pass);
-        case 3: return run_pass<T, VEC, 3>(a, pass);
-        case 4: return run_pass<T, VEC, 4>(a, pass);
+        case 2: return run_pass<T, VEC, 2, PASS>(a);
+        case 3: return run_pass<T, VEC, 3, PASS>(a);
+        case 4: return run_pass<T, VEC, 4, PASS>(a);
     }
     return cudaErrorInvalidValue;
 }
 
-cudaError_t dispatch(const ConvArgs &a, Pass pass) {
+template <Pass PASS>
+cudaError_t dispatch(const ConvArgs &a) {
     const bool v = vectorized(a);
     // the backward holds ten registers per channel: four channels per thread let twice as many warps run
-    if (a.dtype == GDN_DTYPE_BF16)
-        return !v ? by_taps<__nv_bfloat16, 1>(a, pass) : pass == kBwd ? by_taps<__nv_bfloat16, 4>(a, pass) : by_taps<__nv_bfloat16, 8>(a, pass);
-    return v ? by_taps<float, 4>(a, pass) : by_taps<float, 1>(a, pass);
+    constexpr int kBf16 = PASS == kBwd ? 4 : 8;
+    if (a.dtype == GDN_DTYPE_BF16) return v ? by_taps<__nv_bfloat16, kBf16, PASS>(a) : by_taps<__nv_bfloat16, 1, PASS>(a);
+    return v ? by_taps<float, 4, PASS>(a) : by_taps<float, 1, PASS>(a);
 }
 
 }  // namespace
@@ -540,8 +541,8 @@ size_t conv_part_bytes(int total, int C, int W) {
     return blocks * (W + 1) * C * sizeof(float);
 }
 
-cudaError_t launch_conv_fwd(const ConvArgs &a) { return dispatch(a, kFwd); }
-cudaError_t launch_conv_bwd(const ConvArgs &a) { return dispatch(a, kBwd); }
-cudaError_t launch_conv_update(const ConvArgs &a) { return dispatch(a, kUpdate); }
+cudaError_t launch_conv_fwd(const ConvArgs &a) { return dispatch<kFwd>(a); }
+cudaError_t launch_conv_bwd(const ConvArgs &a) { return dispatch<kBwd>(a); }
+cudaError_t launch_conv_update(const ConvArgs &a) { return dispatch<kUpdate>(a); }
 
 }  // namespace gdn

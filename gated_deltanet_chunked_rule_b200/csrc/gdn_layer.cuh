@@ -135,29 +135,10 @@ __device__ __forceinline__ F2 sigmoid(F2 x) {
     return f2(a, b);
 }
 
-// VEC consecutive elements as fp32, by one 16-byte access (or one element).
-template <typename T, int VEC>
-__device__ __forceinline__ void load_vec(const T *p, float (&v)[VEC]) {
-    if constexpr (VEC == 1) {
-        v[0] = to_f32(*p);
-    } else if constexpr (sizeof(T) == 4) {
-        const float4 f = *reinterpret_cast<const float4 *>(p);
-        v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
-    } else {
-        const uint4 u = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-    }
-}
+// VEC consecutive fp32 values as elements, by one 16-byte access.
 template <typename T, int VEC>
 __device__ __forceinline__ void store_vec(T *p, const float (&v)[VEC]) {
-    if constexpr (VEC == 1) {
-        *p = from_f32<T>(v[0]);
-    } else if constexpr (sizeof(T) == 4) {
+    if constexpr (sizeof(T) == 4) {
         *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
     } else {
         uint32_t w[4];
