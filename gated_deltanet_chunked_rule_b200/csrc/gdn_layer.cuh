@@ -211,6 +211,7 @@ struct ScanArgs {
     SeqMap seq;
     int G, H, K, P, dtype, dt_dtype;
     bool softplus;
+    bool tensor_cores, products;  // the call's path, and how its state passes join segments: decided once per call
     long long xs, bs, cs, dts;  // elements between tokens of x, B, C, dt
     const void *x, *dt, *B, *C;
     const float *A, *D, *dt_bias, *h0;  // D, dt_bias, h0 nullable

@@ -59,6 +59,11 @@ int conv_args(const gdn_conv_problem *p, ConvArgs *a) {
     return GDN_OK;
 }
 
+bool env_is(const char *name, const char *value) {
+    const char *e = getenv(name);
+    return e && strcmp(e, value) == 0;
+}
+
 int scan_args(const gdn_scan_problem *p, ScanArgs *a) {
     if (!p) return GDN_ERR_INVALID_ARG;
     memset(a, 0, sizeof(*a));
@@ -76,6 +81,10 @@ int scan_args(const gdn_scan_problem *p, ScanArgs *a) {
     a->G = p->Hq, a->H = p->Hv, a->K = p->K, a->P = p->V;
     a->dtype = p->dtype, a->dt_dtype = p->dt_dtype, a->softplus = p->dt_softplus != 0;
     a->xs = p->x_stride, a->bs = p->b_stride, a->cs = p->c_stride, a->dts = p->dt_stride;
+    // bf16 prompts take the tensor-core kernels; fp32 ones, and all under GDN_IMPL=simt, the CUDA cores. The
+    // two switches (see gdn.h) are read here and nowhere else, so that a call and its kernels agree.
+    a->tensor_cores = a->dtype == GDN_DTYPE_BF16 && !env_is("GDN_IMPL", "simt");
+    a->products = a->tensor_cores && !env_is("GDN_SCAN_SPLIT", "segments") && scan_tc::products_fit(*a);
     return GDN_OK;
 }
 
@@ -89,12 +98,6 @@ int norm_args(const gdn_norm_problem *p, NormArgs *a) {
     a->R = p->rows, a->D = p->D, a->dtype = p->dtype, a->wdtype = p->weight_dtype, a->eps = p->eps;
     a->center = p->center != 0, a->gate_first = p->gate_first != 0;
     return GDN_OK;
-}
-
-// bf16 prompts take the tensor-core kernels; fp32 ones, and all under GDN_IMPL=simt, the CUDA cores.
-bool scan_on_tensor_cores(const ScanArgs &a) {
-    const char *e = getenv("GDN_IMPL");
-    return a.dtype == GDN_DTYPE_BF16 && !(e && strcmp(e, "simt") == 0);
 }
 
 // What the forward keeps: the gates, and every chunk's entry state, hi then lo.
@@ -125,7 +128,7 @@ scan_tc::StateArgs state_pass(const ScanArgs &a, const scan_tc::Gates &gates, bo
     if (s.chunks_per_seg) {
         const size_t slots = a.seq.slots(s.chunks_per_seg * scan_tc::kC);
         s.seg = (float *)seg;
-        s.products = scan_tc::by_products(a);
+        s.products = a.products;
         s.seg_gam = (float *)(seg + align_up(slots * a.H * a.P * a.K * sizeof(float)));
     }
     s.first = reverse ? a.dht : a.h0;
@@ -189,6 +192,9 @@ cudaError_t scan_bwd_tc(const ScanArgs &a) {
     if ((e = scan_tc::launch_states(s)) != cudaSuccess) return e;
     return scan_tc::launch_grad(a, gates, h, g, ws + L.grad);
 }
+
+size_t scan_fwd_bytes(const ScanArgs &a) { return a.tensor_cores ? scan_fwd_layout(a).total : scan_simt_fwd_bytes(a); }
+size_t scan_bwd_bytes(const ScanArgs &a) { return a.tensor_cores ? scan_bwd_layout(a).total : align_up(scan_simt_bwd_bytes(a)); }
 
 int finish(cudaError_t e) { return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA; }
 
@@ -255,19 +261,17 @@ int gdn_conv_update(const gdn_conv_problem *p, const void *x, const void *weight
 // ------------------------------------------------------------------------ scan
 size_t gdn_scan_saved_size(const gdn_scan_problem *p) {
     ScanArgs a;
-    return scan_args(p, &a) == GDN_OK && scan_on_tensor_cores(a) ? scan_saved_bytes(a) : 0;
+    return scan_args(p, &a) == GDN_OK && a.tensor_cores ? scan_saved_bytes(a) : 0;
 }
 
 size_t gdn_scan_fwd_workspace_size(const gdn_scan_problem *p) {
     ScanArgs a;
-    if (scan_args(p, &a) != GDN_OK) return 0;
-    return scan_on_tensor_cores(a) ? scan_fwd_layout(a).total : scan_simt_fwd_bytes(a);
+    return scan_args(p, &a) == GDN_OK ? scan_fwd_bytes(a) : 0;
 }
 
 size_t gdn_scan_bwd_workspace_size(const gdn_scan_problem *p) {
     ScanArgs a;
-    if (scan_args(p, &a) != GDN_OK) return 0;
-    return scan_on_tensor_cores(a) ? scan_bwd_layout(a).total : align_up(scan_simt_bwd_bytes(a));
+    return scan_args(p, &a) == GDN_OK ? scan_bwd_bytes(a) : 0;
 }
 
 static int scan_inputs(const gdn_scan_problem *p, ScanArgs *a, const void *x, const void *dt, const float *A, const void *B,
@@ -289,11 +293,11 @@ int gdn_scan_fwd(const gdn_scan_problem *p, const void *x, const void *dt, const
     if (rc != GDN_OK) return rc;
     if (a.seq.total && !y) return GDN_ERR_INVALID_ARG;
     if (!all_aligned16({y, final_state}) || ((uintptr_t)saved & 255u)) return GDN_ERR_INVALID_ARG;
-    if (!good_ws(workspace, workspace_bytes, gdn_scan_fwd_workspace_size(p))) return GDN_ERR_WORKSPACE;
+    if (!good_ws(workspace, workspace_bytes, scan_fwd_bytes(a))) return GDN_ERR_WORKSPACE;
     if (over_input({y, final_state}, {x, dt, A, B, C, D, dt_bias, h0})) return GDN_ERR_INVALID_ARG;
     a.y = y, a.final_state = final_state, a.saved = saved, a.ws = workspace;
     if (!(a.status = status_ptr())) return GDN_ERR_CUDA;
-    if (scan_on_tensor_cores(a)) return finish(scan_fwd_tc(a));
+    if (a.tensor_cores) return finish(scan_fwd_tc(a));
     TimedLaunch t("scan_fwd", a.stream);
     return finish(launch_scan_simt_fwd(a));
 }
@@ -322,12 +326,12 @@ int gdn_scan_bwd(const gdn_scan_problem *p, const void *x, const void *dt, const
     if (rc != GDN_OK) return rc;
     if (!dA || (a.seq.total && (!dy || !dx || !ddt || !dB || !dC))) return GDN_ERR_INVALID_ARG;
     if (!all_aligned16({dy, dht, dx, ddt, dA, dB, dC, dD, ddt_bias, dh0}) || ((uintptr_t)saved & 255u)) return GDN_ERR_INVALID_ARG;
-    if (!good_ws(workspace, workspace_bytes, gdn_scan_bwd_workspace_size(p))) return GDN_ERR_WORKSPACE;
+    if (!good_ws(workspace, workspace_bytes, scan_bwd_bytes(a))) return GDN_ERR_WORKSPACE;
     if (over_input({dx, ddt, dA, dB, dC, dD, ddt_bias, dh0}, {x, dt, A, B, C, D, dt_bias, h0, saved, dy, dht})) return GDN_ERR_INVALID_ARG;
     a.saved = const_cast<void *>(saved), a.dy = dy, a.dht = dht, a.dx = dx, a.ddt = ddt, a.dA = dA, a.dB = dB, a.dC = dC, a.dD = dD;
     a.ddt_bias = ddt_bias, a.dh0 = dh0, a.ws = workspace;
     if (!(a.status = status_ptr())) return GDN_ERR_CUDA;
-    if (scan_on_tensor_cores(a)) return finish(scan_bwd_tc(a));
+    if (a.tensor_cores) return finish(scan_bwd_tc(a));
     TimedLaunch t("scan_bwd", a.stream);
     return finish(launch_scan_simt_bwd(a));
 }

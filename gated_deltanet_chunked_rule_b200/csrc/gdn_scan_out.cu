@@ -386,7 +386,7 @@ cudaError_t run(const ScanArgs &a, const Gates &gates, const __nv_bfloat16 *tile
     // 312 for 32768 packed ones), not behind the chunks' recurrence, whose blocks it would crowd (281 against 278 us
     // for the training step of 2 x 4096 tokens)
     const dim3 grid(slots, a.G * ((hg + q.run - 1) / q.run));
-    return launch(!by_products(a), kernel, grid, dim3(kThreads), kSmem, a.stream, mb, mc, mx, my, q);
+    return launch(!a.products, kernel, grid, dim3(kThreads), kSmem, a.stream, mb, mc, mx, my, q);
 }
 
 }  // namespace

@@ -30,9 +30,6 @@
 // 128 (67 MB of products): 26 + 22 us against 25 + 10 + 29. A forward that keeps nothing needs no second
 // pass: the tiles of the first one, the segments' starts and one factor per chunk are enough for
 // the outputs (8192 tokens, 64 heads: 40 us less of 162).
-#include <stdlib.h>
-#include <string.h>
-
 #include <algorithm>
 
 #include "gdn_scan_tc.cuh"
@@ -563,23 +560,19 @@ int chunks_per_segment(const ScanArgs &a) {
 // The L2 holds 126 MB; the tiles that are written meanwhile pass through it too.
 constexpr size_t kProductBytes = (size_t)100 << 20;
 
-bool by_products(const ScanArgs &a) {
-    const char *e = getenv("GDN_SCAN_SPLIT");  // "segments": never (the tests reach that path at small sizes by it)
-    if (e && strcmp(e, "segments") == 0) return false;
-    return chunks_per_segment(a) > 0 && 2 * tile_bytes(a) <= kProductBytes;
-}
+bool products_fit(const ScanArgs &a) { return chunks_per_segment(a) > 0 && 2 * tile_bytes(a) <= kProductBytes; }
 
 size_t segment_bytes(const ScanArgs &a) {
     const int c = chunks_per_segment(a);
     if (!c) return 0;
-    if (by_products(a)) return align_up(2 * tile_bytes(a));
+    if (a.products) return align_up(2 * tile_bytes(a));
     const size_t slots = a.seq.slots(c * kC);
     return align_up(slots * a.H * (a.P / kPT) * kPT * a.K * 4) + align_up(slots * a.H * 4);
 }
 
 size_t local_bytes(const ScanArgs &a) {
     const int c = chunks_per_segment(a);
-    if (!c || by_products(a)) return 0;
+    if (!c || a.products) return 0;
     return align_up((size_t)a.seq.slots(c * kC) * a.H * a.P * a.K * 2) + align_up((size_t)a.seq.slots(kC) * a.H * 4);
 }
 

@@ -179,7 +179,7 @@ struct StateArgs {
     bool reverse;
     bool after_gates;    // the launch before is launch_gates'
     int chunks_per_seg;  // 0: whole sequences
-    bool products;       // the segments write their chunks' products (by_products)
+    bool products;       // the segments write their chunks' products (ScanArgs::products)
     float *seg;          // those: [chunk slots, units, 64 K]; otherwise [segment slots, units, K, 64]
     float *seg_gam;      // [segment slots, H]
     __nv_bfloat16 *starts;  // nullable: one pass within the segments only (forward, nothing kept); their
@@ -192,7 +192,7 @@ cudaError_t launch_gates(const ScanArgs &a, const Gates &g);
 cudaError_t launch_states(const StateArgs &s);
 // Segments that a problem's state passes are cut into, and their scratch.
 int chunks_per_segment(const ScanArgs &a);
-bool by_products(const ScanArgs &a);
+bool products_fit(const ScanArgs &a);
 size_t segment_bytes(const ScanArgs &a);
 
 // starts, before: as StateArgs', where the tiles are within segments of seg_tokens only.

@@ -250,6 +250,11 @@ size_t gdn_scan_bwd_workspace_size(const gdn_scan_problem *p);
 /* Bytes of what the forward can keep for the backward (0: nothing to keep). */
 size_t gdn_scan_saved_size(const gdn_scan_problem *p);
 
+/* Two variables of the environment choose among the prompt's paths, for comparing them; every call and size
+ * query reads them once, so they must not change between a size query and the call it is for (a workspace
+ * that has become too small is refused). GDN_IMPL=simt: bf16 prompts on the CUDA cores too.
+ * GDN_SCAN_SPLIT=segments: never by the chunks' products (where those fit the L2 cache), always by segments. */
+
 /* h0 or NULL (zero); final_state or NULL; saved or NULL. */
 int gdn_scan_fwd(const gdn_scan_problem *p, const void *x, const void *dt, const float *A, const void *B,
                  const void *C, const float *D, const float *dt_bias, const float *h0, void *y,

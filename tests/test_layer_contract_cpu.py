@@ -36,3 +36,20 @@ def test_token_updates_refuse_outputs_over_inputs(L):
                 a = [q(k) for k in range(10)]  # x, dt, A, B, C, D, dt_bias, h0, y, final
                 a[out] = q(i)
                 assert L.gdn_scan_step(p, *a, None) == INV, (out, i)
+
+
+def test_switches_of_the_prompts_paths(L, monkeypatch):
+    # sizes are those of the path that the environment chooses; 8192 tokens of 64 heads go by segments anyhow
+    def sizes(T, H, dtype=1):
+        p = ctypes.byref(B.gdn_scan_problem(1, T, 1, H, 128, 64, 0, None, dtype, 0, 1, H * 64, 128, 128, H))
+        return L.gdn_scan_fwd_workspace_size(p), L.gdn_scan_bwd_workspace_size(p), L.gdn_scan_saved_size(p)
+
+    for name in ("GDN_IMPL", "GDN_SCAN_SPLIT"):
+        monkeypatch.delenv(name, raising=False)
+    small, large, fp32 = sizes(1024, 4), sizes(8192, 64), sizes(1024, 4, 0)
+    assert small[2] > 0 and fp32[2] == 0
+    monkeypatch.setenv("GDN_SCAN_SPLIT", "segments")
+    assert sizes(1024, 4) != small and sizes(1024, 4)[2] == small[2]
+    assert sizes(8192, 64) == large and sizes(1024, 4, 0) == fp32
+    monkeypatch.setenv("GDN_IMPL", "simt")
+    assert sizes(1024, 4) == fp32
