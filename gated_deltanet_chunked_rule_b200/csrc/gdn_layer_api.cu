@@ -160,7 +160,8 @@ cudaError_t scan_fwd_tc(const ScanArgs &a) {
 }
 
 // Backward workspace: segment scratch | exit-state gradients (hi, lo) | the gradient kernel's
-// parts | gates and entry states (hi, lo), as the forward keeps them, for a call without `saved`.
+// parts | gates and entry states (hi, lo), as the forward keeps them: last, since only a call without
+// `saved` needs them.
 struct ScanBwdLayout {
     size_t seg, g, grad, saved, total;
 };
@@ -326,7 +327,8 @@ int gdn_scan_bwd(const gdn_scan_problem *p, const void *x, const void *dt, const
     if (rc != GDN_OK) return rc;
     if (!dA || (a.seq.total && (!dy || !dx || !ddt || !dB || !dC))) return GDN_ERR_INVALID_ARG;
     if (!all_aligned16({dy, dht, dx, ddt, dA, dB, dC, dD, ddt_bias, dh0}) || ((uintptr_t)saved & 255u)) return GDN_ERR_INVALID_ARG;
-    if (!good_ws(workspace, workspace_bytes, scan_bwd_bytes(a))) return GDN_ERR_WORKSPACE;
+    const size_t kept = a.tensor_cores && saved ? scan_saved_bytes(a) : 0;
+    if (!good_ws(workspace, workspace_bytes, scan_bwd_bytes(a) - kept)) return GDN_ERR_WORKSPACE;
     if (over_input({dx, ddt, dA, dB, dC, dD, ddt_bias, dh0}, {x, dt, A, B, C, D, dt_bias, h0, saved, dy, dht})) return GDN_ERR_INVALID_ARG;
     a.saved = const_cast<void *>(saved), a.dy = dy, a.dht = dht, a.dx = dx, a.ddt = ddt, a.dA = dA, a.dB = dB, a.dC = dC, a.dD = dD;
     a.ddt_bias = ddt_bias, a.dh0 = dh0, a.ws = workspace;

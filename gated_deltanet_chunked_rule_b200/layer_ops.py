@@ -283,6 +283,7 @@ def chunk_selective_scan_bwd(x, dt, A, B, C, D, dt_bias, dt_softplus, saved, dy,
     dD = _empty(D) if D is not None else None
     db = _empty(dt_bias) if dt_bias is not None else None
     dh0 = s.states()
+    need = 0
     if saved is not None:
         _check(s.dev, ("saved", saved, saved.shape, torch.uint8))
         need = _size(s.dev, "gdn_scan_saved_size", s.P)
@@ -290,7 +291,7 @@ def chunk_selective_scan_bwd(x, dt, A, B, C, D, dt_bias, dt_softplus, saved, dy,
             raise ValueError(f"saved holds {saved.numel()} bytes, the problem needs {need}")
         if not need:
             saved = None
-    n = _size(s.dev, "gdn_scan_bwd_workspace_size", s.P)
+    n = _size(s.dev, "gdn_scan_bwd_workspace_size", s.P) - need  # no room to form again what is kept
     ws = s.bytes(n)
     _call(s.dev, "gdn_scan_bwd", *s.inputs(), _p(_dense(saved)), dy.data_ptr(), _p(dht), dx.data_ptr(), ddt.data_ptr(),
           dA.data_ptr(), dB.data_ptr(), dC.data_ptr(), _p(dD), _p(db), dh0.data_ptr(), ws.data_ptr(), n)

@@ -246,6 +246,7 @@ typedef struct {
 } gdn_scan_problem;
 
 size_t gdn_scan_fwd_workspace_size(const gdn_scan_problem *p);
+/* Of a backward without `saved`; with it gdn_scan_saved_size bytes less are enough. */
 size_t gdn_scan_bwd_workspace_size(const gdn_scan_problem *p);
 /* Bytes of what the forward can keep for the backward (0: nothing to keep). */
 size_t gdn_scan_saved_size(const gdn_scan_problem *p);

@@ -53,3 +53,16 @@ def test_switches_of_the_prompts_paths(L, monkeypatch):
     assert sizes(8192, 64) == large and sizes(1024, 4, 0) == fp32
     monkeypatch.setenv("GDN_IMPL", "simt")
     assert sizes(1024, 4) == fp32
+
+
+def test_backward_workspace_with_kept_states(L, monkeypatch):
+    # refused below what is needed; that this is enough is test_scan_paths_gpu.py's
+    for name in ("GDN_IMPL", "GDN_SCAN_SPLIT"):
+        monkeypatch.delenv(name, raising=False)
+    for dtype in (0, 1):
+        p = ctypes.byref(B.gdn_scan_problem(1, 700, 1, 2, 128, 64, 0, None, dtype, 0, 1, 128, 128, 128, 2))
+        full, kept = L.gdn_scan_bwd_workspace_size(p), L.gdn_scan_saved_size(p)
+        a = [q(k) for k in range(8)]
+        out = [q(20 + k) for k in range(8)]
+        for saved, need in ((q(10), full - kept), (None, full)):
+            assert L.gdn_scan_bwd(p, *a, saved, q(11), q(12), *out, q(40), need - 1, None) == B.GDN_ERR_WORKSPACE

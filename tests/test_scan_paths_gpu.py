@@ -76,6 +76,28 @@ def test_kept_states_are_those_of_the_path(gdn, monkeypatch):
         gdn.chunk_selective_scan_bwd(*a, simt, *rest)
 
 
+@pytest.mark.parametrize("T", [0, 150, 1400])
+def test_workspace_with_kept_states(gdn, T):
+    # with what the forward kept, the backward's workspace has no room for it; the bytes behind stay as they were
+    from gated_deltanet_chunked_rule_b200 import _binding as B
+    from gated_deltanet_chunked_rule_b200 import layer_ops as ops
+    v = S.make([T], 2, 1, 128, 64, torch.bfloat16, seed=T)
+    want = S.train(gdn, v)
+    _, _, saved = gdn.chunk_selective_scan_fwd(*S.args(v), True, v["h0"], True, v["cu"], save_for_backward=True)
+    s = ops._Scan(*S.args(v), True, v["h0"], v["cu"])
+    P = ops.byref(s.P)
+    n = B.lib().gdn_scan_bwd_workspace_size(P) - B.lib().gdn_scan_saved_size(P)
+    ws = torch.full((n + 4096,), 77, dtype=torch.uint8, device="cuda")
+    names = ("dx", "ddt", "dA", "dB", "dC", "dD", "ddt_bias", "dh0")
+    out = [torch.empty_like(want[k]) for k in names]
+    ops._call(s.dev, "gdn_scan_bwd", *s.inputs(), saved.data_ptr(), v["dy"].data_ptr(), v["dht"].data_ptr(),
+              *(t.data_ptr() for t in out), ws.data_ptr(), n)
+    torch.cuda.synchronize()
+    assert gdn.device_status() == 0 and (ws[n:] == 77).all()
+    for k, t in zip(names, out):
+        assert torch.equal(t, want[k]), k
+
+
 def chunked(v, lens):
     """The scan in 64 bits on the GPU in chunks of 64 tokens, the state carried from chunk to chunk."""
     x, dt, A, B, C, D, bias = (t.double() if t is not None else None for t in S.args(v))
