@@ -24,6 +24,7 @@ import ctypes
 from typing import Optional
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _binding as _b
 
@@ -206,6 +207,15 @@ def recurrent_gated_delta_rule(q, k, v, g, beta, scale=None, initial_state=None,
     return o, final_state
 
 
+def _recorded(*tensors):
+    """Whether a high-level call goes through its autograd function: where a gradient is wanted, and
+    under forward-mode differentiation, which the functions have no formulas for: there they
+    refuse an input with a tangent, which a plain call would drop."""
+    if forward_ad._current_level >= 0:
+        return True
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
 class _ChunkGDN(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, g, beta, scale, h0, output_final_state, cu_seqlens, cu_host):
@@ -231,8 +241,7 @@ def chunk_gated_delta_rule(q, k, v, g, beta, scale=None, initial_state=None,
         scale = q.shape[-1] ** -0.5
     if cu_seqlens is not None and cu_seqlens_host is None:
         cu_seqlens_host = cu_seqlens.detach().to("cpu")
-    if torch.is_grad_enabled() and any(
-            t is not None and t.requires_grad for t in (q, k, v, g, beta, initial_state)):
+    if _recorded(q, k, v, g, beta, initial_state):
         return _ChunkGDN.apply(q, k, v, g, beta, scale, initial_state, output_final_state,
                                cu_seqlens, cu_seqlens_host)
     o, fin, _ = chunk_gated_delta_rule_fwd(q, k, v, g, beta, scale, initial_state,

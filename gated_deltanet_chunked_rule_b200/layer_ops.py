@@ -24,7 +24,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _binding as _b
-from .api import _DTYPES
+from .api import _DTYPES, _recorded
 
 _F32 = torch.float32
 _Tensor = torch.Tensor
@@ -215,7 +215,7 @@ def causal_conv1d(x, weight, bias=None, activation=None, initial_state=None, out
                   cu_seqlens=None):
     """High-level call: (y, final_state or None), differentiable w.r.t. x, weight, bias and
     initial_state."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias, initial_state)):
+    if _recorded(x, weight, bias, initial_state):
         return _Conv.apply(x, weight, bias, initial_state, activation, output_final_state, cu_seqlens)
     return causal_conv1d_fwd(x, weight, bias, activation, initial_state, output_final_state, cu_seqlens)
 
@@ -337,8 +337,7 @@ def chunk_selective_scan(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus=False
                          output_final_state=False, cu_seqlens=None):
     """High-level call: (y, final_state or None), differentiable w.r.t. every tensor but
     cu_seqlens."""
-    if torch.is_grad_enabled() and any(
-            t is not None and t.requires_grad for t in (x, dt, A, B, C, D, dt_bias, initial_state)):
+    if _recorded(x, dt, A, B, C, D, dt_bias, initial_state):
         return _ChunkScan.apply(x, dt, A, B, C, D, dt_bias, dt_softplus, initial_state, output_final_state, cu_seqlens)
     y, fin, _ = chunk_selective_scan_fwd(x, dt, A, B, C, D, dt_bias, dt_softplus, initial_state, output_final_state,
                                          cu_seqlens)
@@ -404,6 +403,6 @@ class _Norm(torch.autograd.Function):
 
 def layer_norm(x, weight, bias=None, gate=None, eps=1e-5, center=True, gate_first=False):
     """High-level call: y, differentiable w.r.t. x, weight, bias and gate."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias, gate)):
+    if _recorded(x, weight, bias, gate):
         return _Norm.apply(x, weight, bias, gate, eps, center, gate_first)
     return layer_norm_fwd(x, weight, bias, gate, eps, center, gate_first)[0]
