@@ -152,6 +152,7 @@ def chunk_gated_delta_rule_fwd(q, k, v, g, beta, scale, initial_state=None,
                                     _ptr(o), _ptr(fin), _ptr(saved), _ptr(workspace),
                                     workspace.numel(), _stream(dev))
     _b.check("gdn_chunk_fwd", rc)
+    _written(out)
     return o, fin, saved
 
 
@@ -189,7 +190,8 @@ def recurrent_gated_delta_rule(q, k, v, g, beta, scale=None, initial_state=None,
                                cu_seqlens_host=None, out=None, final_state=None):
     """Token-by-token (decode) step: the same recurrence as the chunked forward, one
     token after another, for a few tokens per sequence (gdn_recurrent_fwd). Returns
-    (o, final_state); `final_state` may be `initial_state` itself (updated in place)."""
+    (o, final_state); `final_state` may be `initial_state` itself (updated in place). Not recorded
+    by autograd."""
     if scale is None:
         scale = q.shape[-1] ** -0.5
     q, k, v, g, beta, h0 = map(_c, (q, k, v, g, beta, initial_state))
@@ -198,13 +200,21 @@ def recurrent_gated_delta_rule(q, k, v, g, beta, scale=None, initial_state=None,
     dev = q.device
     _check(P, dev, q=q, k=k, v=v, g=g, beta=beta, h0=h0, out=out, final=final_state)
     o = out if out is not None else torch.empty((B, T, Hv, V), dtype=q.dtype, device=dev)
+    given = final_state
     if final_state is None:
         final_state = torch.empty((P.N, Hv, K, V), dtype=torch.float32, device=dev)
     with torch.cuda.device(dev):
         rc = _b.lib().gdn_recurrent_fwd(P.ref(), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0),
                                         _ptr(o), _ptr(final_state), _stream(dev))
     _b.check("gdn_recurrent_fwd", rc)
+    _written(out, given)
     return o, final_state
+
+
+def _written(*tensors):
+    """Tells autograd that the library wrote into the caller's tensors, so that a graph which
+    saved one of them refuses its backward instead of reading the new values."""
+    torch.autograd.graph.increment_version([t for t in tensors if t is not None])
 
 
 def _recorded(*tensors):

@@ -24,7 +24,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _binding as _b
-from .api import _DTYPES, _recorded
+from .api import _DTYPES, _recorded, _written
 
 _F32 = torch.float32
 _Tensor = torch.Tensor
@@ -183,7 +183,7 @@ def causal_conv1d_bwd(x, weight, bias, dy, dfinal=None, activation=None, initial
 
 def causal_conv1d_update(x, conv_state, weight, bias=None, activation=None):
     """The next few tokens of every sequence: x [B, T, C]; conv_state [B, W-1, C] is updated
-    in place. Returns y [B, T, C]."""
+    in place. Returns y [B, T, C]. Not recorded by autograd."""
     dev, x, weight, bias, P, _, state = _conv(x, weight, bias, activation, None)
     _check(dev, ("conv_state", conv_state, state, x.dtype))
     if conv_state is None:
@@ -191,6 +191,7 @@ def causal_conv1d_update(x, conv_state, weight, bias=None, activation=None):
     _in_place("conv_state", conv_state)
     y = _empty(x)
     _call(dev, "gdn_conv_update", byref(P), x.data_ptr(), _p(weight), _p(bias), conv_state.data_ptr(), y.data_ptr())
+    _written(conv_state)
     return y
 
 
@@ -301,15 +302,17 @@ def chunk_selective_scan_bwd(x, dt, A, B, C, D, dt_bias, dt_softplus, saved, dy,
 def recurrent_selective_scan(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus=False, initial_state=None,
                              final_state=None, cu_seqlens=None):
     """Token by token, for a few tokens per sequence (decoding). Returns (y, final_state);
-    `final_state` may be `initial_state` itself (updated in place)."""
+    `final_state` may be `initial_state` itself (updated in place). Not recorded by autograd."""
     s = _Scan(x, dt, A, B, C, D, dt_bias, dt_softplus, initial_state, cu_seqlens)
     _check(s.dev, ("final_state", final_state, s.state, _F32))
+    given = final_state
     if final_state is None:
         final_state = s.states()
     else:
         _in_place("final_state", final_state)
     y = _empty(x)
     _call(s.dev, "gdn_scan_step", *s.inputs(), y.data_ptr(), final_state.data_ptr())
+    _written(given)
     return y, final_state
 
 

@@ -44,3 +44,43 @@ def test_tangents_are_refused(gdn, name):
             with torch.set_grad_enabled(grad), pytest.raises(NotImplementedError, match="jvp"):
                 f(fwad.make_dual(t, torch.ones_like(t)))
     assert torch.equal(f(t), want)
+
+
+def graph_and_step(gdn, name):
+    """(a graph that saved a state, a step that writes that state)."""
+    p = M.on_gpu(M.params("delta", 9, torch.float32), torch.float32, False)
+    v = S.make([9], 2, 1, 64, 64, torch.float32, seed=2, packed=False)
+    if name == "conv":
+        state = torch.zeros(1, M.W - 1, p["u"].shape[2], device="cuda")
+        u = p["u"].clone().requires_grad_()
+        out = gdn.causal_conv1d(u, p["cw"], p["cb"], "silu", state)[0]
+        return out, u, lambda: gdn.causal_conv1d_update(p["u"][:, :1].contiguous(), state, p["cw"], p["cb"], "silu")
+    if name == "scan":
+        state, x = v["h0"].clone(), v["x"].clone().requires_grad_()
+        a = S.args(v)
+        out = gdn.chunk_selective_scan(x, *a[1:], True, state)[0]
+        one = [t[:, :1] if t is not None and t.dim() > 1 else t for t in a]
+        return out, x, lambda: gdn.recurrent_selective_scan(*one, True, state, state)
+    q, k, w = (t.contiguous() for t in M.split(p["u"]))
+    g, beta = torch.nn.functional.softplus(p["a"]) * p["A"], torch.sigmoid(p["b"])
+    state, x = torch.zeros(1, M.H, M.K, M.V, device="cuda"), w.clone().requires_grad_()
+    out = gdn.chunk_gated_delta_rule(q, k, x, g, beta, initial_state=state)[0]
+    one = [t[:, :1].contiguous() for t in (q, k, w, g, beta)]
+    if name == "delta":
+        return out, x, lambda: gdn.recurrent_gated_delta_rule(*one, initial_state=state, final_state=state)
+    # an output of the caller's own: the memory of v, which the graph saved, given back to another call
+    other = torch.randn_like(w)
+    if name == "step's out":
+        return out, x, lambda: gdn.recurrent_gated_delta_rule(q, k, other, g, beta, out=x.detach())
+    return out, x, lambda: gdn.chunk_gated_delta_rule_fwd(q, k, other, g, beta, 1.0, out=x.detach())
+
+
+@pytest.mark.parametrize("name", ["conv", "scan", "delta", "step's out", "prompt's out"])
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode])
+def test_states_written_in_place_are_noticed(gdn, name, mode):
+    out, x, step = graph_and_step(gdn, name)
+    torch.autograd.grad(out.sum(), x, retain_graph=True)
+    with mode():
+        step()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        torch.autograd.grad(out.sum(), x)
