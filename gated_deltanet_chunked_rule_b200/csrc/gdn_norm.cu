@@ -20,6 +20,8 @@
 // blocks on an SM instead of three; two rows ahead instead of one gain nothing). 4096 centred rows
 // of 4096, L2-resident: forward 13 us, backward 31 us with the second kernel, bound by the
 // barriers of a row's sums.
+#include <algorithm>
+
 #include "gdn_layer.cuh"
 #include "gdn_host.cuh"
 
@@ -572,7 +574,7 @@ cudaError_t by_width(const NormArgs &a, bool bwd) {
 
 int any_dw_blocks(const NormArgs &a) {
     const long long groups = (a.R + 63) / 64;  // at least 64 rows per block
-    return (int)(groups < 148 ? groups : 148);
+    return (int)std::min<long long>(groups, sm_count());
 }
 
 template <typename T>
