@@ -17,7 +17,9 @@
 // Everything that ends in an fp32 result (dA, ddt, its bias) is formed in fp32 from exact
 // products and the two-part states; sums of the crossing pairs run forward or backward
 // without cancellation, except inside one 32 x 32 diagonal block. bf16 results take one
-// rounded operand per term: L o S, the scaled rows, the summed L o Q o delta.
+// rounded operand per term: L o S and the scaled rows; the summed L o Q o delta is cut in two
+// bf16 parts, its products being taken only once (0.6 us of 117; dB and dC came out at 2.3e-3 and
+// up to 2.6e-3 of their norm, half as much again as their own rounding).
 //
 // A CTA (one per SM) takes one chunk and a run of units (a head's 64 columns; linear in them)
 // of one group. The products with B and C of the masked Q are taken once, after the masked
@@ -54,9 +56,11 @@ constexpr int kRowThreads = 256;
 constexpr int kThreads = kRowThreads + 128;
 constexpr int kRowRegs = 208, kAuxRegs = 88;  // 384 threads are launched with 168 each
 static_assert(kRowThreads * kRowRegs + 128 * kAuxRegs <= kThreads * 168, "register split");
-// B | C | P (L o S, at the end the summed masked Q) | x, then scaled x | dY, then dx | h hi, lo | g' hi, lo | scaled dY |
-// dY, then dx, of every second unit
+// B | C | P (L o S, at the end the summed masked Q's high part) | x, then scaled x | dY, then dx | h hi, lo (at the end
+// the summed masked Q's low part) | g' hi, lo | scaled dY | dY, then dx, of every second unit
 constexpr int kB = 0, kCt = 32768, kPm = 65536, kX = 98304, kY = 114688, kH = 131072, kG = 163840, kSy = 196608, kY1 = 212992;
+constexpr int kMl = kH;
+static_assert(kG - kMl >= kC * kC * 2 && kMl % 1024 == 0, "the low part takes h's place");
 constexpr int kVec = 229376;
 struct Vec {
     float v[3][kC];     // [w - 1]: e^{(start of row block w) - gam_s} for s left of block w
@@ -238,11 +242,15 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                 ok = ok && wait_bar(m_ready, 0, abort_flag);
                 if (ok) {
                     tc_fence_after();
-                    const uint32_t mc = cols(sb + kPm), mr = rows(sb + kPm), b = rows(sb + kB), c = rows(sb + kCt);
+                    const uint32_t b = rows(sb + kB), c = rows(sb + kCt);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        mma<kTokenHi, kTokenHi>(tmem + kColC, mc + cstep(k), b + rstep(k), idC, true);
-                        mma<kTokenHi, kTokenHi>(tmem + kColB, mr + rstep(k), c + rstep(k), idB, true);
+                    for (int part = 0; part < 2; ++part) {
+                        const uint32_t mc = cols(sb + (part ? kMl : kPm)), mr = rows(sb + (part ? kMl : kPm));
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            mma<kTokenHi, kTokenHi>(tmem + kColC, mc + cstep(k), b + rstep(k), idC, true);
+                            mma<kTokenHi, kTokenHi>(tmem + kColB, mr + rstep(k), c + rstep(k), idB, true);
+                        }
                     }
                     mma_commit(end_full);
                 }
@@ -578,15 +586,26 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
             tc_fence_before();
             mbar_arrive(&dx_done[i & 1]);
         }
-        // ---- the summed masked Q, in P's place (its last product has completed: dx_full)
+        // ---- the summed masked Q in two parts, in P's place (its last product has completed: dx_full) and in
+        // h's (its products have: cd_full, and so have its reads: hg_read)
+        wait(hg_read, (units - 1) & 1);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (k > wr) continue;  // zeros stand there
+        for (int k = 0; k < 4; ++k)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                st_shared_v4(sb + kPm + (k >> 1) * 16384 + piece(row, 4 * (k & 1) + 2 * half + j), pack_bf16(msum[k][4 * j]),
-                             pack_bf16(msum[k][4 * j + 1]), pack_bf16(msum[k][4 * j + 2]), pack_bf16(msum[k][4 * j + 3]));
-        }
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t at = (k >> 1) * 16384 + piece(row, 4 * (k & 1) + 2 * half + j);
+                uint32_t hi[4] = {}, lo[4] = {};
+                if (k <= wr) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 m = get(msum[k][4 * j + e]);
+                        hi[e] = pack_bf16(m.x, m.y);
+                        lo[e] = pack_bf16(m.x - bf_lo(hi[e]), m.y - bf_hi(hi[e]));
+                    }
+                    st_shared_v4(sb + kPm + at, hi[0], hi[1], hi[2], hi[3]);  // (right of the diagonal zeros stand)
+                }
+                st_shared_v4(sb + kMl + at, lo[0], lo[1], lo[2], lo[3]);
+            }
         fence_proxy_async();
         tc_fence_before();
         mbar_arrive(m_ready);

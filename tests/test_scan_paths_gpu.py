@@ -98,6 +98,23 @@ def test_workspace_with_kept_states(gdn, T):
         assert torch.equal(t, want[k]), k
 
 
+@pytest.mark.parametrize("H,G,K,P,lens", [(4, 1, 128, 64, [128]), (8, 2, 64, 64, [128, 100]), (6, 2, 128, 128, [128]), (1, 1, 128, 64, [127, 1])])
+def test_shared_gradients_round_once(gdn, H, G, K, P, lens):
+    """dB and dC of sequences within a chunk, without states before or gradients behind: one product with the summed
+    masked scores, which it takes in two bf16 parts (2^-16), in fp32 otherwise: 2^-16 and sqrt(T + 512 + 17 * 128) 2^-24,
+    independent roundings, against 2^-8 / sqrt(3) of the result's own. So the error's norm is that of rounding the
+    64-bit result, up to a hundredth, and 5 / sqrt(n) for its scatter over n values."""
+    v = S.make(lens, H, G, K, P, torch.bfloat16, torch.float32, seed=H + K, h0=False, slow=True)
+    v["dht"].zero_()
+    got = S.train(gdn, v)
+    ref, _ = S.reference(v, lens, True)
+    for k in ("dB", "dC"):
+        want = ref[k].reshape(got[k].shape)
+        mine, best = ((t.cpu().double() - want).norm() / want.norm() for t in (got[k], want.to(torch.bfloat16)))
+        print(k, f"{mine:.2e} of {best:.2e}")
+        assert mine <= best * (1.01 + 5 / want.numel() ** 0.5), k
+
+
 def chunked(v, lens):
     """The scan in 64 bits on the GPU in chunks of 64 tokens, the state carried from chunk to chunk."""
     x, dt, A, B, C, D, bias = (t.double() if t is not None else None for t in S.args(v))
