@@ -58,8 +58,12 @@ __global__ void __launch_bounds__(256) scan_gates_tc_kernel(Params p) {
     for (int b = 0; b < 4; ++b) {
         // log1p(exp(v)), or v itself above 20 (where they agree to fp32 precision)
         float d = p.softplus ? (raw[b] > 20.f ? raw[b] : log1pf(expf(raw[b]))) : raw[b];
-        if (b * 32 + lane >= len) d = 0.f;
-        const float g = d * A2;
+        const bool live = b * 32 + lane < len;
+        if (!live) d = 0.f;
+        // 2^-256 and below are 0 with or without the up to 2^116 that other tokens may grow by, but a larger
+        // sum would round the tokens behind it in its block by 2^-24 of itself (a NaN stays one)
+        float g = live ? d * A2 : 0.f;
+        g = g < -256.f ? -256.f : g;
         float f = g, r = g;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {

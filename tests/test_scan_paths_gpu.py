@@ -115,6 +115,38 @@ def test_shared_gradients_round_once(gdn, H, G, K, P, lens):
         assert mine <= best * (1.01 + 5 / want.numel() ** 0.5), k
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("A,small", [(-1e6, 1e-6), (-3e4, 1e-5), (float("-inf"), 0.02)])
+def test_tokens_that_clear_the_state(gdn, dtype, A, small):
+    # one step in nine decays by e^A (to 0), the others slowly: what comes behind it in its block is as exact as
+    # elsewhere. The clearing steps alone where A is infinite (0 times it is no number)
+    v = S.make([200, 40], 2, 1, 128, 64, DT[dtype], torch.float32, seed=13, bias=False)
+    g = torch.Generator().manual_seed(14)
+    v["dt"] = (small * (0.5 + torch.rand(v["dt"].shape, generator=g))).cuda()
+    v["dt"][:, 4::9] = 1.0
+    v["A"].fill_(A)
+    if A == float("-inf"):
+        y, fin, _ = gdn.chunk_selective_scan_fwd(*S.args(v), False, v["h0"], True, v["cu"])
+        S.verify(v, [200, 40], False, {"y": y, "final": fin})
+    else:
+        S.verify(v, [200, 40], False, S.train(gdn, v, False))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("low", [float("-inf"), torch.finfo(torch.float32).min])
+def test_tokens_masked_by_their_step(gdn, dtype, low):
+    # a step of the lowest value is one of 0: the token leaves the state as it is and gets no gradient of its step
+    v = S.make([150, 70], 2, 1, 128, 64, DT[dtype], torch.float32, seed=15)
+    off = torch.zeros(220, dtype=torch.bool)
+    off[[0, 3, 31, 32, 127, 128, 149, 150, 219]] = True
+    w = dict(v, dt=v["dt"].clone())
+    w["dt"][:, off] = low
+    got = S.train(gdn, w)
+    assert not got["ddt"][:, off].any()
+    w["dt"] = w["dt"].clamp(min=-200)  # the reference's 64 bits know no lowest value of 32: softplus is 0 here too
+    S.verify(w, [150, 70], True, got)
+
+
 def chunked(v, lens):
     """The scan in 64 bits on the GPU in chunks of 64 tokens, the state carried from chunk to chunk."""
     x, dt, A, B, C, D, bias = (t.double() if t is not None else None for t in S.args(v))
