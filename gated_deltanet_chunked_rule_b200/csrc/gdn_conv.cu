@@ -16,11 +16,14 @@
 // runs in shared memory, over blocks by a second kernel in a fixed order. The runs are as long as
 // lets every block be resident at once.
 //
-// The bytes: forward reads x and writes y, backward reads x and dy and writes dx. What bounds it
-// is the work on them, 17 and 30 instructions per element, with 16 warps on an SM: 8192 tokens of
-// 8192 channels forward 60 us (42 by the copy rate), of 4352 channels backward 68 us (33). One
-// channel per instruction and runs of 32 tokens: backward 89 us. Tried and slower: the next batch
-// loaded ahead (81 us), two channels per thread and twice the warps (88 us).
+// The bytes: forward reads x and writes y, backward reads x and dy and writes dx. What bounds it are
+// the rows in flight: they stand in registers, 128 a thread and so 16 warps on an SM, which issue in
+// 36 (forward) and 46 % of the cycles and mostly wait for their rows in the others; the work is 17
+// and 30 instructions per element. 8192 tokens of 8192 channels forward 60 us (42 by the copy rate), of
+// 4352 channels backward 68 us (33). One channel per instruction and runs of 32 tokens: backward 89 us.
+// Tried and slower: the next batch loaded ahead into registers (81 us), two channels per thread and
+// twice the warps (88 us). Widths or strides off 16 bytes take one channel per thread: 8191 channels
+// forward 148 us, 4351 backward 190.
 #include <algorithm>
 
 #include "gdn_host.cuh"

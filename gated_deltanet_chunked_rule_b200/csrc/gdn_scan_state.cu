@@ -555,13 +555,14 @@ int chunks_per_segment(const ScanArgs &a) {
     const long long chunks = a.seq.cu ? (a.seq.total + kC - 1) / kC : (a.seq.T + kC - 1) / kC;
     const int fit = sm_count() / std::max(1, pairs * rows);
     if (fit < 2 || chunks < 4) return 0;
-    // a packed batch's sequences end inside segments: twice as many even the SMs' shares out (16 sequences of
-    // 64 .. 8192 tokens, 16 pairs: 124 + 21 us of state and start kernels with 15 or 16 chunks, 143 + 20 with 29)
+    // a packed batch's sequences end inside segments: twice as many even the SMs' shares out (measured on one
+    // batch, 16 sequences of 64 .. 8192 tokens, 16 pairs: 124 + 21 us of state and start kernels with 15 or 16
+    // chunks, 143 + 20 with 29)
     const int segments = a.seq.cu ? 2 * fit : fit;
     return (int)std::max<long long>(2, (chunks + segments - 1) / segments);
 }
 
-// The L2 holds 126 MB; the tiles that are written meanwhile pass through it too.
+// Of sm_100's 126 MB of L2; the tiles that are written meanwhile pass through it too.
 constexpr size_t kProductBytes = (size_t)100 << 20;
 
 bool products_fit(const ScanArgs &a) { return chunks_per_segment(a) > 0 && 2 * tile_bytes(a) <= kProductBytes; }

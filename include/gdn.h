@@ -192,9 +192,12 @@ int gdn_recurrent_fwd(const gdn_problem *p, const void *q, const void *k, const 
  * other tensor is contiguous. cu_seqlens is read on the device only: an
  * inconsistent one never leads out of the tensors and is recorded as
  * GDN_ERR_DEVICE_ARG in the status word; the results are then unspecified.
- * Packed sequences are independent, also for non-finite values. Results do not
- * change from run to run. An output must not be one of the call's inputs (or
- * overlap one), except for the states that are said to be updated in place. The FlashQLA pages have no counterpart to these.
+ * Packed sequences are independent, also for non-finite values; within one, a
+ * non-finite value may reach every token of its 128-token chunk in the bf16 scan
+ * (products with zero weights), and only what the formula says elsewhere. Results do
+ * not change from run to run. An output must not be one of the call's inputs, which
+ * is refused (or overlap one, which is not noticed), except for the states that are
+ * said to be updated in place. The FlashQLA pages have no counterpart to these.
  * ------------------------------------------------------------------------- */
 
 /* Short causal convolution, depthwise: per channel and sequence
@@ -233,7 +236,9 @@ int gdn_conv_update(const gdn_conv_problem *p, const void *x, const void *weight
  *   h_t = exp(delta_t A) h_{t-1} + delta_t B_t x_t^T,   y_t = h_t^T C_t + D x_t
  * with a state h of [K, V] as above. x, y [B*T, Hv, V]; B, C [B*T, Hq, K]; dt [B*T, Hv];
  * A, D, dt_bias [Hv] fp32 (D, dt_bias may be NULL: zero); states [N, Hv, K, V] fp32.
- * delta_t A is <= 0 in practice; its running sums must stay below 80. */
+ * delta_t A is <= 0 in practice; its running sums must stay below 80. A step of the dtype's lowest value
+ * or -inf with dt_softplus is delta = 0 (a masked token), an A of -inf clears the state at every delta > 0
+ * (the gradient of such a step is no number). */
 typedef struct {
     int B, T, Hq, Hv, K, V;     /* K, V in {64, 128}; Hv a multiple of Hq, at most 1024      */
     int num_seqs;               /* 0: N = B; else B == 1 and cu_seqlens given                */
