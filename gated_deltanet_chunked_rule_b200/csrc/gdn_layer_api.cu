@@ -37,7 +37,7 @@ bool over_input(std::initializer_list<const void *> outs, std::initializer_list<
 int make_seq(int B, int T, int num_seqs, const int32_t *cu, SeqMap *m) {
     if (B < 1 || T < 0 || num_seqs < 0) return GDN_ERR_INVALID_ARG;
     const long long total = (long long)B * T;
-    if (total > (1ll << 30)) return GDN_ERR_INVALID_ARG;  // token indices stay in int
+    if (total > (1ll << 30) || num_seqs > (1 << 30)) return GDN_ERR_INVALID_ARG;  // tokens and slots are counted in int
     if (num_seqs > 0 && (B != 1 || !cu)) return GDN_ERR_INVALID_ARG;
     m->cu = num_seqs > 0 ? cu : nullptr;
     m->N = num_seqs > 0 ? num_seqs : B;

@@ -187,9 +187,9 @@ int gdn_recurrent_fwd(const gdn_problem *p, const void *q, const void *k, const 
  * the same state, without the delta correction) and the gated layer norm behind
  * it. Conventions as above: caller-owned device pointers on the current device,
  * 16-byte aligned; nothing allocated or synchronised; a rejected call enqueues
- * nothing; bf16 or fp32. Token strides (in elements) let an input be a slice of
- * a wider tensor: token t of batch row b starts at (b*T + t) * stride. Every
- * other tensor is contiguous. cu_seqlens is read on the device only: an
+ * nothing; bf16 or fp32; at most 2^30 tokens, and as many packed sequences. Token
+ * strides (in elements) let an input be a slice of a wider tensor: token t of batch
+ * row b starts at (b*T + t) * stride. Every other tensor is contiguous. cu_seqlens is read on the device only: an
  * inconsistent one never leads out of the tensors and is recorded as
  * GDN_ERR_DEVICE_ARG in the status word; the results are then unspecified.
  * Packed sequences are independent, also for non-finite values; within one, a

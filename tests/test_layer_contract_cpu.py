@@ -66,3 +66,13 @@ def test_backward_workspace_with_kept_states(L, monkeypatch):
         out = [q(20 + k) for k in range(8)]
         for saved, need in ((q(10), full - kept), (None, full)):
             assert L.gdn_scan_bwd(p, *a, saved, q(11), q(12), *out, q(40), need - 1, None) == B.GDN_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("seqs", [(1 << 30) + 1, (1 << 31) - 1])
+def test_more_sequences_than_counts_hold(L, seqs):
+    # slots (tokens / length + sequences) stay in 32 bits; refused before anything is read
+    a = [q(k) for k in range(30)]
+    p = ctypes.byref(B.gdn_conv_problem(1, 1 << 30, 64, 4, seqs, 1 << 20, 1, 1, 64))
+    assert L.gdn_conv_bwd_workspace_size(p) == 0 and L.gdn_conv_fwd(p, *a[:6], None) == INV
+    p = ctypes.byref(B.gdn_scan_problem(1, 1 << 30, 1, 2, 128, 64, seqs, 1 << 20, 1, 0, 1, 128, 128, 128, 2))
+    assert L.gdn_scan_fwd_workspace_size(p) == 0 and L.gdn_scan_step(p, *a[:10], None) == INV
