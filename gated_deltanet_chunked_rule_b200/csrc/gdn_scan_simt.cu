@@ -12,12 +12,18 @@
 //
 //   dC_t = h_t dy_t,   i_t = a_{t+1} g_{t+1},   g_t = C_t dy_t^T + i_t,   u_t = B_t^T g_t
 //   dx_t = delta u_t + D dy_t,   dB_t = g_t (delta x_t),   w_t = u_t.x_t
-//   d(delta A)_t = a_t <h_{t-1}, g_t> = r_t - delta_t v_t + <h_t, i_t>,   <h_t, i_t> = d(delta A)_{t+1}
-//   with r_t = C_t^T (a_t h_{t-1}) dy_t and v_t = B_t^T i_t x_t;   ddelta_t = A d(delta A)_t + w_t
+//   d(delta A)_t = a_t <h_{t-1}, g_t>,   ddelta_t = A d(delta A)_t + w_t
 //
-// The sum over r - delta v runs to the end of the token's 16-token tile only, where <h, i> is
-// taken anew from a kept state, and neither holds the token's own product (which would cancel):
-// with it and 64 tokens the sums' rounding reached 1e-4 of dA where the decay is fast.
+// <h_{t-1}, g_t> is what crosses token t; within its tile of 16 tokens s < t <= r, with h the state on
+// entry to the tile, i what comes in at its end and L, E, F, W the decays from s to r, from the tile's start
+// through r, from s to the tile's end and over the tile:
+//
+//   d(delta A)_t = sum L_rs (C_r.B_s)(dy_r.x_s) delta_s + sum E_r r_r + sum F_s delta_s v_s + W <h, i>
+//   with r_r = C_r^T h dy_r and v_s = B_s^T i x_s
+//
+// Every term is there once and none is taken off again. (The recurrence d(delta A)_t = r'_t - delta_t v'_t +
+// d(delta A)_{t+1}, run to the tile's end, sums what does not cross t too and then subtracts it; its roundings
+// are shared by the tile's tokens, and dA was off by 2e-6 of its norm where this is off by 3e-7.)
 //
 // One CTA per (sequence or segment of one, head, 32 columns of P): warp w holds state rows
 // 32w .. 32w+31, lane l column l, in registers across its tokens. Where sequences, heads and
@@ -71,6 +77,19 @@ __device__ __forceinline__ float lane_sums(float (&v)[32], int lane) {
     return v[0];
 }
 
+// Product of 32 values in shared memory (16-byte aligned) with a column's 32 in registers, two at a time.
+__device__ __forceinline__ float row_dot(const float *row, const float (&col)[32]) {
+    F2 v[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll
+    for (int k = 0; k < 32; k += 4) {
+        const float4 r = *reinterpret_cast<const float4 *>(row + k);
+        v[0] = fma2(f2(r.x, r.y), f2(col[k], col[k + 1]), v[0]);
+        v[1] = fma2(f2(r.z, r.w), f2(col[k + 2], col[k + 3]), v[1]);
+    }
+    const float2 a = get(add2(v[0], v[1]));
+    return a.x + a.y;
+}
+
 // A tile of tokens in registers on its way to shared memory.
 template <typename Tin, typename Tdt, int K>
 struct Tile {
@@ -100,12 +119,12 @@ struct Tile {
 };
 
 template <int K>
-struct TileSmem {
+struct alignas(16) TileSmem {
     float b[kTile][K], c[kTile][K], x[kTile][kCols], dy[kTile][kCols], a[kTile], d[kTile];
     float red[kTile][K / 32][kCols], red2[kTile][K / 32][kCols];
 };
 
-// Per token, head and slice of P: r, v, w as above and x.dy.
+// Per token, head and slice of P: r, v, w as above (r and v by the tile's h and i) and x.dy.
 enum Dot { kR, kV, kWt, kXd, kDots };
 struct Dots {
     float *at;  // [kDots][total, H, P/32]
@@ -192,6 +211,8 @@ scan_forward_kernel(ScanP p, const Tin *__restrict__ x, const Tdt *__restrict__ 
         put_tile<Tin, Tdt, K, GRAD, ENDS>(s, r, p, A, bias, cnt, tid);
         __syncthreads();
         if (q + kTile < len) r.template load<GRAD, ENDS>(p, x, dt, B, C, dy, h, g, c0, t0 + q + kTile, 1, min(kTile, len - q - kTile), tid);
+        if (GRAD)  // C h, with the state on entry
+            for (int i = 0; i < cnt; ++i) s.red[i][w][lane] = row_dot(&s.c[i][32 * w], hr);
         for (int i = 0; i < cnt; ++i) {
             const float a = s.a[i], dx = s.d[i] * s.x[i][lane];
             float yv = 0.f;
@@ -202,12 +223,10 @@ scan_forward_kernel(ScanP p, const Tin *__restrict__ x, const Tdt *__restrict__ 
             } else {
 #pragma unroll
                 for (int k = 0; k < 32; ++k) {
-                    const float ah = a * hr[k];
-                    if (GRAD) yv = fmaf(s.c[i][32 * w + k], ah, yv);
-                    hr[k] = fmaf(s.b[i][32 * w + k], dx, ah);
+                    hr[k] = fmaf(s.b[i][32 * w + k], dx, a * hr[k]);
                     if (!GRAD) yv = fmaf(s.c[i][32 * w + k], hr[k], yv);
                 }
-                s.red[i][w][lane] = yv;
+                if (!GRAD) s.red[i][w][lane] = yv;
                 if (GRAD) {
                     float v[32];
                     const float d = s.dy[i][lane];
@@ -325,14 +344,14 @@ scan_step_kernel(ScanP p, const Tin *__restrict__ x, const Tdt *__restrict__ dt,
         for (int i = 0; i < 32; ++i) final_state[at + (size_t)(32 * w + i) * p.P] = hr[i];
 }
 
-// The gradient's reverse half: dx, dB parts (without delta), v and w, <h, i> at the end of every
-// tile [slots, H, P/32], dh0.
+// The gradient's reverse half: dx, dB parts (without delta), v and w, <h, i> of every tile (h on entry, i at its
+// end) [slots, H, P/32], dh0.
 // ENDS: only the gradient at the segment's start from zero, and its log decay.
 template <typename Tin, typename Tdt, int K, bool ENDS>
 __global__ void __launch_bounds__(K)
 scan_reverse_kernel(ScanP p, const Tin *__restrict__ x, const Tdt *__restrict__ dt, const Tin *__restrict__ B, const Tin *__restrict__ C,
-                    const Tin *__restrict__ dy, const float *__restrict__ dht, const float *__restrict__ keep, Tin *__restrict__ dx,
-                    float *__restrict__ db_part, float *__restrict__ chunk_q, float *__restrict__ dh0, Dots dots) {
+                    const Tin *__restrict__ dy, const float *__restrict__ h0, const float *__restrict__ dht, const float *__restrict__ keep,
+                    Tin *__restrict__ dx, float *__restrict__ db_part, float *__restrict__ chunk_q, float *__restrict__ dh0, Dots dots) {
     __shared__ TileSmem<K> s;
     __shared__ float qs[K / 32];
     const int h = blockIdx.y, c0 = blockIdx.z * kCols, g = h / (p.H / p.G);
@@ -357,10 +376,15 @@ scan_reverse_kernel(ScanP p, const Tin *__restrict__ x, const Tdt *__restrict__ 
         put_tile<Tin, Tdt, K, true, ENDS, true>(s, r, p, A, bias, cnt, tid);
         if (!ENDS) {
             const size_t slot = (size_t)tile0 + q / kKeep;
-            const float *src = keep + (slot * p.H + h) * K * p.P + c0 + lane;
+            // the state that the tile before ended in
+            const float *src = t0 - wk.s_begin + q >= kKeep ? keep + ((slot - 1) * p.H + h) * K * p.P + (size_t)32 * w * p.P + c0 + lane
+                               : h0                         ? h0 + wk.at
+                                                            : nullptr;
             float v = 0.f;
+            if (src) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v = fmaf(src[(size_t)(32 * w + k) * p.P], gr[k], v);
+                for (int k = 0; k < 32; ++k) v = fmaf(src[(size_t)k * p.P], gr[k], v);
+            }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
             if (lane == 0) qs[w] = v;
@@ -374,6 +398,8 @@ scan_reverse_kernel(ScanP p, const Tin *__restrict__ x, const Tdt *__restrict__ 
         }
         __syncthreads();
         if (q - cnt >= 0) r.template load<true, ENDS, true>(p, x, dt, B, C, dy, h, g, c0, t0 + q - cnt, -1, kTile, tid);
+        if (!ENDS)  // B i, with what comes in at the end
+            for (int i = 0; i < cnt; ++i) s.red2[i][w][lane] = row_dot(&s.b[i][32 * w], gr);
         for (int i = 0; i < cnt; ++i) {
             const float d = s.dy[i][lane], a = s.a[i];
             if constexpr (ENDS) {
@@ -382,17 +408,15 @@ scan_reverse_kernel(ScanP p, const Tin *__restrict__ x, const Tdt *__restrict__ 
                 for (int k = 0; k < 32; ++k) gr[k] = a * fmaf(s.c[i][32 * w + k], d, gr[k]);
             } else {
                 const float xv = s.x[i][lane];
-                float u = 0.f, ui = 0.f, v[32];
+                float u = 0.f, v[32];
 #pragma unroll
                 for (int k = 0; k < 32; ++k) {
-                    ui = fmaf(s.b[i][32 * w + k], gr[k], ui);
                     gr[k] = fmaf(s.c[i][32 * w + k], d, gr[k]);
                     u = fmaf(s.b[i][32 * w + k], gr[k], u);
                     v[k] = gr[k] * xv;
                     gr[k] *= a;
                 }
                 s.red[i][w][lane] = u;
-                s.red2[i][w][lane] = ui;
                 const float sum = lane_sums(v, lane);
                 db_part[(((size_t)(t0 + q - i) * p.H + h) * gridDim.z + blockIdx.z) * K + 32 * w + lane] = sum;
             }
@@ -441,58 +465,128 @@ scan_gather_kernel(ScanP p, const Tdt *__restrict__ dt, const float *__restrict_
     }
 }
 
-// Per tile of 16 tokens and head (16 lanes, one per token): the gradients of the log decay and
-// dt, and this tile's parts [slots, 3, H] of dA, ddt_bias and dD.
-constexpr int kGateHeads = 8;  // per block
-template <typename Tdt>
-__global__ void __launch_bounds__(kGateHeads * kKeep)
-scan_gates_kernel(ScanP p, const Tdt *__restrict__ dt, Dots dots, const float *__restrict__ chunk_q, int S,
-                  Tdt *__restrict__ ddt, float *__restrict__ part) {
-    static_assert(kKeep == 16, "half a warp per tile");
-    const int i = threadIdx.x % kKeep, h = blockIdx.y * kGateHeads + threadIdx.x / kKeep, slot = blockIdx.x;
+// Four elements of a row, by one access.
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                       __uint_as_float(v.y & 0xffff0000u));
+}
+
+// Per tile of 16 tokens and head: the gradients of the log decay and dt, and this tile's parts [slots, 3, H]
+// of dA, ddt_bias and dD. A thread per pair of tokens for the products, then a lane per token.
+template <typename Tin, typename Tdt, int K>
+__global__ void __launch_bounds__(128)
+scan_gates_kernel(ScanP p, const Tin *__restrict__ x, const Tdt *__restrict__ dt, const Tin *__restrict__ B, const Tin *__restrict__ C,
+                  const Tin *__restrict__ dy, Dots dots, const float *__restrict__ chunk_q, Tdt *__restrict__ ddt, float *__restrict__ part) {
+    constexpr int T = kKeep, kPad = 4, kMaxP = 128;  // rows of 16 bytes more: a quarter warp's rows meet all banks
+    static_assert(T == 16 && T * (T - 1) / 2 <= 128, "a thread per pair, half a warp per tile");
+    __shared__ __align__(16) float bs[T][K + kPad], cs[T][K + kPad], xs[T][kMaxP + kPad], ys[T][kMaxP + kPad];
+    __shared__ float ds[T], gs[T], pairs[T][T + 1];
+    const int tid = threadIdx.x, slot = blockIdx.x, h = blockIdx.y, S = p.P / kCols;
+    float *out = part + (size_t)slot * 3 * p.H + h;
     int n, local;
-    float dA = 0.f, dbias = 0.f, dD = 0.f;
-    if (p.m.slot(slot, kKeep, &n, &local) && h < p.H) {
-        const int t0 = p.m.begin(n) + local * kKeep, t = t0 + i;
-        const bool live = t < p.m.end(n);
-        const float A = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.f;
-        const size_t at = (size_t)t * p.H + h;
-        float raw = 0.f, d = 0.f, rv = 0.f, vv = 0.f, wv = 0.f, q = 0.f;
+    if (!p.m.slot(slot, T, &n, &local)) {  // an unused slot adds nothing
+        if (tid < 3) out[tid * p.H] = 0.f;
+        return;
+    }
+    const int t0 = p.m.begin(n) + local * T, cnt = min(T, p.m.end(n) - t0), g = h / (p.H / p.G);
+    // a thread per token and eighth of its row, four elements at a time (the inputs' rows are 16-byte aligned)
+    const int i = tid >> 3, c4 = (tid & 7) * 4;
+    const bool in = i < cnt;
+    const size_t ti = (size_t)(t0 + i);
+#pragma unroll
+    for (int k = c4; k < K; k += 32) {
+        *reinterpret_cast<float4 *>(&bs[i][k]) = in ? load4(B + ti * p.bs + (size_t)g * K + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4 *>(&cs[i][k]) = in ? load4(C + ti * p.cs + (size_t)g * K + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int k = c4; k < kMaxP; k += 32) {
+        if (k >= p.P) break;
+        *reinterpret_cast<float4 *>(&xs[i][k]) = in ? load4(x + ti * p.xs + (size_t)h * p.P + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4 *>(&ys[i][k]) = in ? load4(dy + (ti * p.H + h) * p.P + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    const float A = p.A[h];
+    const int t = t0 + tid;
+    const size_t at = (size_t)t * p.H + h;
+    float raw = 0.f, d = 0.f, rv = 0.f, vv = 0.f, wv = 0.f, q = 0.f, dD = 0.f;
+    if (tid < T) {
         for (int k = 0; k < S; ++k) q += chunk_q[((size_t)slot * p.H + h) * S + k];
-        if (live) {
-            raw = to_f32(dt[t * p.dts + h]) + bias, d = delta_of(raw, p.softplus);
+        if (tid < cnt) {
+            raw = to_f32(dt[(size_t)t * p.dts + h]) + (p.dt_bias ? p.dt_bias[h] : 0.f), d = delta_of(raw, p.softplus);
             for (int k = 0; k < S; ++k) {
                 rv += *dots(kR, at * S + k), vv += *dots(kV, at * S + k), wv += *dots(kWt, at * S + k);
                 dD += *dots(kXd, at * S + k);
             }
         }
-        // a token's log decay: what later tokens of the tile leave, and the tile's end
-        float carry = rv - d * vv;
-        const unsigned half = 0xffffu << (threadIdx.x & 16);
-#pragma unroll
-        for (int o = 1; o < kKeep; o <<= 1) {
-            const float v = __shfl_down_sync(half, carry, o, kKeep);
-            if (i + o < kKeep) carry += v;
-        }
-        carry += q;
-        if (live) {
-            dA = d * carry;
-            float g = fmaf(A, carry, wv);
-            if (p.softplus) g /= 1.f + expf(-raw);
-            ddt[at] = from_f32<Tdt>(g);
-            dbias = g;
-        }
-#pragma unroll
-        for (int o = kKeep / 2; o > 0; o >>= 1) {
-            dA += __shfl_xor_sync(half, dA, o, kKeep);
-            dbias += __shfl_xor_sync(half, dbias, o, kKeep);
-            dD += __shfl_xor_sync(half, dD, o, kKeep);
-        }
+        ds[tid] = d, gs[tid] = tid < cnt ? d * A : 0.f;
     }
-    if (i || h >= p.H) return;
-    part[((size_t)slot * 3 + 0) * p.H + h] = dA;
-    part[((size_t)slot * 3 + 1) * p.H + h] = dbias;
-    part[((size_t)slot * 3 + 2) * p.H + h] = dD;
+    __syncthreads();
+    int r = 1, s = tid;  // pair (r, s), s < r
+    while (s >= r) s -= r++;
+    if (r < cnt) {
+        auto dot = [&](const float *a, const float *b, int len) {
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int k = 0; k < len; k += 4) {
+                const float4 a4 = *reinterpret_cast<const float4 *>(a + k), b4 = *reinterpret_cast<const float4 *>(b + k);
+                v[0] = fmaf(a4.x, b4.x, v[0]), v[1] = fmaf(a4.y, b4.y, v[1]), v[2] = fmaf(a4.z, b4.z, v[2]), v[3] = fmaf(a4.w, b4.w, v[3]);
+            }
+            return (v[0] + v[1]) + (v[2] + v[3]);
+        };
+        float between = 0.f;
+        for (int j = s + 1; j <= r; ++j) between += gs[j];
+        pairs[r][s] = expf(between) * dot(cs[r], bs[s], K) * dot(ys[r], xs[s], p.P) * ds[s];
+    }
+    __syncthreads();
+    if (tid >= T) return;
+    constexpr unsigned kLanes = (1u << T) - 1;
+    // row tid: the sum of the columns before each; then a column's rows from its own on
+    float v[T], before = 0.f;
+#pragma unroll
+    for (int j = 0; j < T - 1; ++j) v[j] = j < tid && tid < cnt ? pairs[tid][j] : 0.f;
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+        pairs[tid][j] = before;
+        if (j < T - 1) before += v[j];
+    }
+    __syncwarp(kLanes);
+    float carry = 0.f;
+#pragma unroll
+    for (int j = 0; j < T; ++j) v[j] = j >= tid && j < cnt ? pairs[j][tid] : 0.f;
+#pragma unroll
+    for (int j = 0; j < T; ++j) carry += v[j];
+    // log decays through the token and after it, then the sums from the token on and before it
+    float upto = gs[tid], from = gs[tid];
+#pragma unroll
+    for (int o = 1; o < T; o <<= 1) {
+        const float a = __shfl_up_sync(kLanes, upto, o, T), b = __shfl_down_sync(kLanes, from, o, T);
+        if (tid >= o) upto += a;
+        if (tid + o < T) from += b;
+    }
+    const float whole = __shfl_sync(kLanes, from, 0, T), next = __shfl_down_sync(kLanes, from, 1, T);
+    float on = expf(upto) * rv, past = tid < T - 1 ? expf(next) * d * vv : d * vv;
+#pragma unroll
+    for (int o = 1; o < T; o <<= 1) {
+        const float a = __shfl_down_sync(kLanes, on, o, T), b = __shfl_up_sync(kLanes, past, o, T);
+        if (tid + o < T) on += a;
+        if (tid >= o) past += b;
+    }
+    past = __shfl_up_sync(kLanes, past, 1, T);
+    carry += on + (tid ? past : 0.f) + expf(whole) * q;
+    float dA = 0.f, dbias = 0.f;
+    if (tid < cnt) {
+        dA = d * carry;
+        dbias = fmaf(A, carry, wv);
+        if (p.softplus) dbias /= 1.f + expf(-raw);
+        ddt[at] = from_f32<Tdt>(dbias);
+    }
+#pragma unroll
+    for (int o = T / 2; o > 0; o >>= 1) {
+        dA += __shfl_xor_sync(kLanes, dA, o, T);
+        dbias += __shfl_xor_sync(kLanes, dbias, o, T);
+        dD += __shfl_xor_sync(kLanes, dD, o, T);
+    }
+    if (tid == 0) out[0] = dA, out[p.H] = dbias, out[2 * p.H] = dD;
 }
 
 // dA, ddt_bias, dD [H] from the slots' parts, in a fixed order.
@@ -516,7 +610,8 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 // Tokens of a segment; 0: whole sequences. Four CTAs of these kernels run on an SM; where there are
 // fewer than two per SM a sequence is cut into about as many segments as would fill them, of at
 // least two tiles (a packed batch, of unknown lengths, by its total). 1000 tokens of 4 heads, K = P =
-// 64: forward and backward 30 + 90 us with two tiles, 34 + 108 with three, 40 + 125 with four.
+// 64: forward and backward 30 + 90 us with two tiles, 34 + 108 with three, 40 + 125 with four (the
+// backward as it was then; 100 with the gates' gradients by pairs).
 int segment_tokens(const ScanArgs &a) {
     const long long ctas = (long long)(a.seq.cu ? 1 : a.seq.N) * a.H * (a.P / kCols);
     const int tokens = a.seq.cu ? a.seq.total : a.seq.T;
@@ -574,7 +669,7 @@ void compose(const ScanArgs &a, const ScanP &p) {
     const dim3 grid(walks(a, p.seg), a.H, a.P / kCols);
     if (REV)
         scan_reverse_kernel<Tin, Tdt, K, true><<<grid, K, 0, a.stream>>>(p, x, (const Tdt *)a.dt, B, C, dy, nullptr, nullptr, nullptr, nullptr,
-                                                                        nullptr, nullptr, Dots{});
+                                                                        nullptr, nullptr, nullptr, Dots{});
     else
         scan_forward_kernel<Tin, Tdt, K, false, true><<<grid, K, 0, a.stream>>>(p, x, (const Tdt *)a.dt, B, C, nullptr, nullptr, nullptr,
                                                                                nullptr, nullptr, nullptr, Dots{}, a.status);
@@ -615,11 +710,12 @@ cudaError_t backward(const ScanArgs &a) {
     compose<Tin, Tdt, K, false>(a, p);
     scan_forward_kernel<Tin, Tdt, K, true, false><<<grid, K, 0, a.stream>>>(p, x, dt, B, C, dy, a.h0, nullptr, nullptr, dc, keep, dots, a.status);
     compose<Tin, Tdt, K, true>(a, p);
-    scan_reverse_kernel<Tin, Tdt, K, false><<<grid, K, 0, a.stream>>>(p, x, dt, B, C, dy, a.dht, keep, (Tin *)a.dx, db, q, a.dh0, dots);
+    scan_reverse_kernel<Tin, Tdt, K, false><<<grid, K, 0, a.stream>>>(p, x, dt, B, C, dy, a.h0, a.dht, keep, (Tin *)a.dx, db, q, a.dh0,
+                                                                      dots);
     if (a.seq.total)
         scan_gather_kernel<Tin, Tdt, K><<<a.seq.total, K, 0, a.stream>>>(p, dt, dc, db, (Tin *)a.dB, (Tin *)a.dC);
     if (slots)
-        scan_gates_kernel<Tdt><<<dim3(slots, (a.H + kGateHeads - 1) / kGateHeads), kGateHeads * kKeep, 0, a.stream>>>(p, dt, dots, q, a.P / kCols, (Tdt *)a.ddt, part);
+        scan_gates_kernel<Tin, Tdt, K><<<dim3(slots, a.H), 128, 0, a.stream>>>(p, x, dt, B, C, dy, dots, q, (Tdt *)a.ddt, part);
     return launch_scan_sum(part, slots, a);
 }
 

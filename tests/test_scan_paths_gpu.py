@@ -147,6 +147,28 @@ def test_tokens_masked_by_their_step(gdn, dtype, low):
     S.verify(w, [150, 70], True, got)
 
 
+@pytest.mark.parametrize("dtype,impl", [("fp32", ""), ("bf16", "simt")])
+@pytest.mark.parametrize("lens", [[300], [7] * 20, [16, 17, 1, 120]])
+def test_gate_gradients_on_cuda_cores_add_up(gdn, monkeypatch, dtype, impl, lens):
+    """Norms over 32 heads of dA and ddt_bias, sums over the tokens of terms of either sign, as large as the root of
+    the sum of their squares. A term is off by at most about 6 2^-24: the products over K and P in up to 32 roundings in
+    sequence, independent ones (sqrt(32 / 3)), as many again for the states' own over the tokens that they remember, the
+    decays' exponentials; the 16 tokens of a tile may share them (sqrt(16)). 24 2^-24; bf16 results' inputs are exact."""
+    if impl:
+        monkeypatch.setenv("GDN_IMPL", impl)
+    v = S.make(lens, 32, 4, 64, 64, DT[dtype], torch.float32, seed=len(lens))
+    g = torch.Generator().manual_seed(5)
+    v["A"] = -(1 + 15 * torch.rand(32, generator=g)).cuda()
+    v["dt_bias"] = (-7 + 5 * torch.rand(32, generator=g)).cuda()
+    v["h0"], v["dht"] = 0.1 * v["h0"], 0.1 * v["dht"]
+    got = S.train(gdn, v)
+    ref, _ = S.reference(v, lens, True)
+    for k in ("dA", "ddt_bias"):
+        off = ((got[k].cpu().double() - ref[k]).norm() / ref[k].norm()).item()
+        print(k, f"{off:.2e}")
+        assert off <= 24 * 2.0 ** -24, k
+
+
 def chunked(v, lens):
     """The scan in 64 bits on the GPU in chunks of 64 tokens, the state carried from chunk to chunk."""
     x, dt, A, B, C, D, bias = (t.double() if t is not None else None for t in S.args(v))
