@@ -100,8 +100,8 @@ int norm_args(const gdn_norm_problem *p, NormArgs *a) {
     return GDN_OK;
 }
 
-// What the forward keeps: the gates, and every chunk's entry state, hi then lo.
-size_t scan_saved_bytes(const ScanArgs &a) { return scan_tc::gates_bytes(a) + 2 * align_up(scan_tc::tile_bytes(a)); }
+// What the forward keeps: the gates, and every chunk's entry state in three parts.
+size_t scan_saved_bytes(const ScanArgs &a) { return scan_tc::gates_bytes(a) + 3 * align_up(scan_tc::tile_bytes(a)); }
 
 // Forward workspace: segment scratch | for a call that keeps nothing: gates | entry states (hi) |
 // segments' starts.
@@ -136,8 +136,9 @@ scan_tc::StateArgs state_pass(const ScanArgs &a, const scan_tc::Gates &gates, bo
     return s;
 }
 
-scan_tc::Tiles tile_pair(char *at, const ScanArgs &a) {
-    return scan_tc::Tiles{(__nv_bfloat16 *)at, (__nv_bfloat16 *)(at + align_up(scan_tc::tile_bytes(a)))};
+scan_tc::Tiles tile_parts(char *at, const ScanArgs &a) {
+    const size_t part = align_up(scan_tc::tile_bytes(a));
+    return scan_tc::Tiles{(__nv_bfloat16 *)at, (__nv_bfloat16 *)(at + part), (__nv_bfloat16 *)(at + 2 * part)};
 }
 
 cudaError_t scan_fwd_tc(const ScanArgs &a) {
@@ -147,7 +148,7 @@ cudaError_t scan_fwd_tc(const ScanArgs &a) {
     cudaError_t e = scan_tc::launch_gates(a, gates);
     if (e != cudaSuccess) return e;
     scan_tc::StateArgs s = state_pass(a, gates, false, ws + L.seg);
-    s.tiles = saved ? tile_pair(saved + scan_tc::gates_bytes(a), a) : scan_tc::Tiles{(__nv_bfloat16 *)(ws + L.tiles), nullptr};
+    s.tiles = saved ? tile_parts(saved + scan_tc::gates_bytes(a), a) : scan_tc::Tiles{(__nv_bfloat16 *)(ws + L.tiles), nullptr, nullptr};
     scan_tc::Locals locals{};
     if (!saved && scan_tc::local_bytes(a)) {
         locals.seg_tokens = s.chunks_per_seg * scan_tc::kC;
@@ -159,8 +160,8 @@ cudaError_t scan_fwd_tc(const ScanArgs &a) {
     return scan_tc::launch_out(a, gates, s.tiles.hi, locals);
 }
 
-// Backward workspace: segment scratch | exit-state gradients (hi, lo) | the gradient kernel's
-// parts | gates and entry states (hi, lo), as the forward keeps them: last, since only a call without
+// Backward workspace: segment scratch | exit-state gradients (three parts) | the gradient kernel's
+// parts | gates and entry states, as the forward keeps them: last, since only a call without
 // `saved` needs them.
 struct ScanBwdLayout {
     size_t seg, g, grad, saved, total;
@@ -169,7 +170,7 @@ ScanBwdLayout scan_bwd_layout(const ScanArgs &a) {
     ScanBwdLayout L;
     L.seg = 0;
     L.g = L.seg + scan_tc::segment_bytes(a);
-    L.grad = L.g + 2 * align_up(scan_tc::tile_bytes(a));
+    L.grad = L.g + 3 * align_up(scan_tc::tile_bytes(a));
     L.saved = L.grad + scan_tc::grad_bytes(a);
     L.total = L.saved + scan_saved_bytes(a);
     return L;
@@ -179,7 +180,7 @@ cudaError_t scan_bwd_tc(const ScanArgs &a) {
     const ScanBwdLayout L = scan_bwd_layout(a);
     char *ws = (char *)a.ws, *saved = a.saved ? (char *)a.saved : ws + L.saved;
     const scan_tc::Gates gates = scan_tc::gates_at(saved, a);
-    const scan_tc::Tiles g = tile_pair(ws + L.g, a), h = tile_pair(saved + scan_tc::gates_bytes(a), a);
+    const scan_tc::Tiles g = tile_parts(ws + L.g, a), h = tile_parts(saved + scan_tc::gates_bytes(a), a);
     cudaError_t e;
     if (!a.saved) {
         if ((e = scan_tc::launch_gates(a, gates)) != cudaSuccess) return e;

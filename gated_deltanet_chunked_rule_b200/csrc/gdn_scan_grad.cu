@@ -1,6 +1,6 @@
 // gdn_scan_grad.cu -- per-chunk gradients of the tensor-core selective scan. Chunks do not
 // depend on each other: the entry states h and the exit-state gradients g' of all chunks are
-// there (bf16 pairs hi + lo from the state passes).
+// there (three bf16 parts each from the state passes).
 //
 // Per chunk and head (rows r, s; L_rs = e^{gam_r - gam_s} for s <= r; delta = the step sizes):
 //
@@ -15,18 +15,22 @@
 //   ddelta_t = A dgam_t + w_t
 //
 // Everything that ends in an fp32 result (dA, ddt, its bias) is formed in fp32 from exact
-// products and the two-part states (2.8e-6 of an element, rms, where C h, B g' and <h, g'> take them; a
-// third part would be half as much traffic again); sums of the crossing pairs run forward or backward
-// without cancellation, except inside one 32 x 32 diagonal block. bf16 results take one
-// rounded operand per term: L o S and the scaled rows; the summed L o Q o delta is cut in two
-// bf16 parts, its products being taken only once (0.6 us of 117; dB and dC came out at 2.3e-3 and
-// up to 2.6e-3 of their norm, half as much again as their own rounding).
+// products and states in three bf16 parts, 24 bits; sums of the crossing pairs run forward or
+// backward and nothing is taken off again (inside a 32 x 32 diagonal block: a prefix over the columns, summed
+// over the rows from each column on). Two parts, and row minus column sums inside the blocks, left dA and the
+// bias off by 1e-6 to 4e-6 of their norm; 2e-7 to 1e-6 now, for 15 us of this kernel's and 14 of the state
+// kernels' (2 x 4096 tokens, 16 heads of 128). bf16 results take one rounded operand per
+// term: L o S and the scaled rows; the summed L o Q o delta is cut in two bf16 parts, its products being taken only
+// once (0.6 us; with one, dB and dC came out at 2.3e-3 and up to 2.6e-3 of their norm, half as much again as
+// their own rounding).
 //
 // A CTA (one per SM) takes one chunk and a run of units (a head's 64 columns; linear in them)
 // of one group. The products with B and C of the masked Q are taken once, after the masked
 // Qs are summed over the units in registers; dC and dB stay in tensor memory meanwhile (S |
 // one 128-column work region | dC | dB = 512 columns). The work region holds C h, then Q, then
-// (L o S)^T dY and B g'; e^{gam} dY h^T and X g'^T run while the mask is applied. Warps 0-7: a
+// (L o S)^T dY and B g'; e^{gam} dY h^T and X g'^T run while the mask is applied. The states' third parts
+// have no shared memory of their own: h's stands in P's place until the mask, g's in the scaled dY's once that
+// is multiplied, so that <h, g'> is summed in two places. Warps 0-7: a
 // thread per row and column half; warp 8 issues the products on the work region, warp 9 those of
 // dC and dB, warp 10 loads (TMA, bulk copies) and stores: a tile's next load is issued as soon as
 // its last reader is done; dY has two tiles, and dx leaves through its dY's. The row warps need the
@@ -35,13 +39,13 @@
 // (row and column sums) goes to memory, and a small kernel scans it: in the row warps the scans and
 // the barriers they need cost 2500 cycles per head.
 //
-// Bound by the chain of one unit's stages, about 10000 cycles: the mask takes 3400 (row block 3,
+// Bound by the chain of one unit's stages, about 11500 cycles: the mask takes 3400 (row block 3,
 // whose two warps share a scheduler, has four column blocks to row block 0's one), the products
-// after it 1500, reading dx 1000. 2 x 4096 tokens, 16 heads of 128, K = 128: 117 us, and 13 us the
-// gates' gradients (150 with one fp32 operation per instruction, 135 with the scans in the row
-// warps and one dY tile); its tiles and rows alone are 250 MB, 39 us. Tried and not better: Q in two
-// halves with B g' under the mask (the products' operand reads then slow the row warps), 16 row
-// warps (spills).
+// after it 1800, reading dx 1000. 2 x 4096 tokens, 16 heads of 128, K = 128: 135 us, and 13 us the
+// gates' gradients; its tiles and rows alone are 320 MB, 50 us. With states in two parts 117 us (and then 150
+// with one fp32 operation per instruction, 135 with the scans in the row warps and one dY tile). Tried and
+// not better: Q in two halves with B g' under the mask (the products' operand reads then slow the row
+// warps), 16 row warps (spills), <h, g'> in the idle warp 11 (8 us more).
 #include <algorithm>
 
 #include "gdn_scan_tc.cuh"
@@ -57,10 +61,10 @@ constexpr int kRowThreads = 256;
 constexpr int kThreads = kRowThreads + 128;
 constexpr int kRowRegs = 208, kAuxRegs = 88;  // 384 threads are launched with 168 each
 static_assert(kRowThreads * kRowRegs + 128 * kAuxRegs <= kThreads * 168, "register split");
-// B | C | P (L o S, at the end the summed masked Q's high part) | x, then scaled x | dY, then dx | h hi, lo (at the end
-// the summed masked Q's low part) | g' hi, lo | scaled dY | dY, then dx, of every second unit
+// B | C | P (before it h's third part; at the end the summed masked Q's high part) | x, then scaled x | dY, then dx | h hi,
+// lo (at the end the summed masked Q's low part) | g' hi, lo | scaled dY, then g's third part | dY, then dx, of every second unit
 constexpr int kB = 0, kCt = 32768, kPm = 65536, kX = 98304, kY = 114688, kH = 131072, kG = 163840, kSy = 196608, kY1 = 212992;
-constexpr int kMl = kH;
+constexpr int kMl = kH, kH2 = kPm, kG2 = kSy;
 static_assert(kG - kMl >= kC * kC * 2 && kMl % 1024 == 0, "the low part takes h's place");
 constexpr int kVec = 229376;
 struct Vec {
@@ -82,13 +86,14 @@ struct Sums {
     float rsum[4][2][kC];  // [block][h]: row sums of W delta, strictly below the diagonal
     float csum[4][kC];     // [w]: column sums of W, strictly below the diagonal
     float wdiag[kC];       // W_tt
+    float cross[kC];       // sum_{r >= t, s < t} W_rs delta_s inside t's diagonal block, s in t's half of its columns
     float hg[32];          // [warp]: <h, g'>
 };
 
 struct GradP {
     Params p;
     int run, runs;
-    const __nv_bfloat16 *h_hi, *h_lo, *g_hi, *g_lo;
+    Tiles h, g;
     __nv_bfloat16 *dx, *dB, *dC;
     Sums *sums;      // [slots, H, slices of a head]
     float *part_bc;  // [2][runs][total, G, K] where runs > 1
@@ -112,6 +117,36 @@ __device__ __forceinline__ float lane_sums(float (&a)[16], const float (&b)[16],
         }
     }
     return a[0];
+}
+
+// Product of two blocked state tiles: this thread's elements of the row threads'.
+template <int K>
+__device__ __forceinline__ float dot_elements(uint32_t a, uint32_t b, int tid) {
+    F2 v = f2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < K * kPT / 8 / kRowThreads; ++j) {
+        const uint32_t at = (j * kRowThreads + tid) * 16;
+        const uint4 x = ld_shared_v4(a + at), y = ld_shared_v4(b + at);
+        const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v = fma2(f2(bf_lo(xw[k]), bf_hi(xw[k])), f2(bf_lo(yw[k]), bf_hi(yw[k])), v);
+    }
+    const float2 s = get(v);
+    return s.x + s.y;
+}
+
+// Sum over the warp's lanes of a[i], delivered to lanes 2 i and 2 i + 1.
+__device__ __forceinline__ float lane_sums(float (&a)[16], int lane) {
+#pragma unroll
+    for (int o = 16; o > 1; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < o / 2; ++i) {
+            const float send = up ? a[i] : a[i + o / 2], keep = up ? a[i + o / 2] : a[i];
+            a[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+    }
+    return a[0] + __shfl_xor_sync(0xffffffffu, a[0], 1);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -147,11 +182,13 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
     uint64_t *ch_full = bars + 6, *q_full = bars + 7, *cd_full = bars + 8, *dx_full = bars + 9, *end_full = bars + 10;  // products
     uint64_t *cb_ready = bars + 11, *r_free = bars + 12, *s_ready = bars + 13, *p_ready = bars + 14, *hg_read = bars + 15,
              *dx_done = bars + 16, *m_ready = bars + 18;  // the row threads; dx_done: two
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 19);
+    uint64_t *h2_full = bars + 19, *g2_full = bars + 20;  // loads of the states' third parts
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 21);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     if (tid == 0) {
         for (int i = 0; i < 11; ++i) mbar_init(bars + i, 1);
         for (int i = 11; i < 19; ++i) mbar_init(bars + i, kRowThreads);
+        mbar_init(h2_full, 1), mbar_init(g2_full, 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -178,6 +215,7 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                 uint32_t b = cols(sb + kB), c = cols(sb + kCt), y = cols(sb + kY), x = cols(sb + kX), yr = rows(sb + kY),
                          pm = rows(sb + kPm), h0 = state_rows(sb + kH), h1 = state_rows(sb + kH + kTile),
                                g0 = state_rows(sb + kG), g1 = state_rows(sb + kG + kTile);
+                uint32_t h2 = state_rows(sb + kH2), g2 = state_rows(sb + kG2);
                 bool ok = wait_bar(cb_full, 0, abort_flag) && wait_bar(cb_ready, 0, abort_flag);
                 tc_fence_after();
                 if (ok) {
@@ -186,7 +224,7 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                 }
                 for (int i = 0; i < units && ok; ++i) {
                     // or the sums below are all formed ahead, in more registers than there are
-                    asm volatile("" : "+r"(b), "+r"(c), "+r"(y), "+r"(x), "+r"(yr), "+r"(pm), "+r"(h0), "+r"(h1), "+r"(g0), "+r"(g1));
+                    asm volatile("" : "+r"(b), "+r"(c), "+r"(y), "+r"(x), "+r"(yr), "+r"(pm), "+r"(h0), "+r"(h1), "+r"(g0), "+r"(g1), "+r"(h2), "+r"(g2));
                     const uint32_t y2 = (i & 1) * ((kY1 - kY) >> 4);
                     // C h
                     if (i > 0) ok = wait_bar(&dx_done[(i - 1) & 1], ((i - 1) >> 1) & 1, abort_flag);  // the work region is read
@@ -198,6 +236,11 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                         mma<kTokenHi, kStateRowsHi<K>>(tmem + kColR, c + cstep(k), h0 + srstep(k), idH, k > 0);
                         mma<kTokenHi, kStateRowsHi<K>>(tmem + kColR, c + cstep(k), h1 + srstep(k), idH, true);
                     }
+                    ok = wait_bar(h2_full, i & 1, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < K / 16; ++k) mma<kTokenHi, kStateRowsHi<K>>(tmem + kColR, c + cstep(k), h2 + srstep(k), idH, true);
                     mma_commit(ch_full);
                     // Q = dY X^T
                     ok = wait_bar(x_full, i & 1, abort_flag) && wait_bar(&y_full[i & 1], (i >> 1) & 1, abort_flag) && wait_bar(r_free, i & 1, abort_flag);
@@ -217,6 +260,11 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                         mma<kTokenHi, kStateRowsHi<K>>(tmem + kColR + 64, b + cstep(k), g0 + srstep(k), idH, k > 0);
                         mma<kTokenHi, kStateRowsHi<K>>(tmem + kColR + 64, b + cstep(k), g1 + srstep(k), idH, true);
                     }
+                    ok = wait_bar(g2_full, i & 1, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < K / 16; ++k) mma<kTokenHi, kStateRowsHi<K>>(tmem + kColR + 64, b + cstep(k), g2 + srstep(k), idH, true);
                     mma_commit(dx_full);
                 }
                 if (!ok) fail();
@@ -260,10 +308,14 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
         } else if (warp == 10) {  // copies
             if (lane == 0) {
                 auto tile_at = [&](int i) { return (((size_t)blockIdx.x * p.G + g) * p.U + u_first + i) * (K * kPT); };
-                auto load_pair = [&](int at, uint64_t *bar, const __nv_bfloat16 *hi, const __nv_bfloat16 *lo, int i) {
+                auto load_pair = [&](int at, uint64_t *bar, const Tiles &t, int i) {
                     mbar_arrive_expect_tx(bar, 2 * kTile);
-                    bulk_load(smem + at, hi + tile_at(i), kTile, bar);
-                    bulk_load(smem + at + kTile, lo + tile_at(i), kTile, bar);
+                    bulk_load(smem + at, t.hi + tile_at(i), kTile, bar);
+                    bulk_load(smem + at + kTile, t.lo + tile_at(i), kTile, bar);
+                };
+                auto load_third = [&](int at, uint64_t *bar, const Tiles &t, int i) {
+                    mbar_arrive_expect_tx(bar, kTile);
+                    bulk_load(smem + at, t.lo2 + tile_at(i), kTile, bar);
                 };
                 auto load_rows = [&](int at, uint64_t *bar, const CUtensorMap *map, int i) {
                     const int u = u_first + i;
@@ -275,21 +327,24 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                     tma_load_3d(smem + kCt + j * 16384, &tm_c, cb_full, 64 * j, g, t0);
                     tma_load_3d(smem + kB + j * 16384, &tm_b, cb_full, 64 * j, g, t0);
                 }
-                int hs = 1, gs = 1, xs = 1, ys = 1;  // loads issued
-                load_pair(kH, h_full, q.h_hi, q.h_lo, 0);
+                int hs = 1, gs = 1, xs = 1, ys = 1, h2s = 1, g2s = 0;  // loads issued
+                load_pair(kH, h_full, q.h, 0);
+                load_third(kH2, h2_full, q.h, 0);
                 load_rows(kX, x_full, &tm_x, 0);
                 load_rows(kY, &y_full[0], &tm_dy, 0);
                 if (units > 1) load_rows(kY1, &y_full[1], &tm_dy, 1), ++ys;
-                load_pair(kG, g_full, q.g_hi, q.g_lo, 0);
+                load_pair(kG, g_full, q.g, 0);
                 bool ok = true;
                 for (int i = 0; i < units && ok; ++i) {
                     const bool more = i + 1 < units;
                     ok = wait_bar(cd_full, i & 1, abort_flag);
+                    if (ok) load_third(kG2, g2_full, q.g, i), ++g2s;  // the scaled dY is read
                     if (ok && more) load_rows(kX, x_full, &tm_x, i + 1), ++xs;
                     ok = ok && wait_bar(hg_read, i & 1, abort_flag);
-                    if (ok && more) load_pair(kH, h_full, q.h_hi, q.h_lo, i + 1), ++hs;
+                    if (ok && more) load_pair(kH, h_full, q.h, i + 1), ++hs;
                     ok = ok && wait_bar(dx_full, i & 1, abort_flag);
-                    if (ok && more) load_pair(kG, g_full, q.g_hi, q.g_lo, i + 1), ++gs;
+                    if (ok && more) load_third(kH2, h2_full, q.h, i + 1), ++h2s;  // P is read
+                    if (ok && more) load_pair(kG, g_full, q.g, i + 1), ++gs;
                     ok = ok && wait_bar(&dx_done[i & 1], (i >> 1) & 1, abort_flag);
                     if (!ok) break;
                     const int y = i & 1 ? kY1 : kY;
@@ -306,6 +361,8 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                 bool done = drain(cb_full, 0);
                 done = drain(h_full, (hs - 1) & 1) && done;
                 done = drain(g_full, (gs - 1) & 1) && done;
+                done = drain(h2_full, (h2s - 1) & 1) && done;
+                if (g2s) done = drain(g2_full, (g2s - 1) & 1) && done;
                 done = drain(x_full, (xs - 1) & 1) && done;
                 done = drain(&y_full[0], ((ys + 1) / 2 - 1) & 1) && done;
                 if (ys > 1) done = drain(&y_full[1], (ys / 2 - 1) & 1) && done;
@@ -372,9 +429,10 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
             // ---- rows of x and dY; e^gam dY for dC, dY.(C h)
             wait(x_full, i & 1);
             wait(&y_full[i & 1], (i >> 1) & 1);
+            if (i > 0) wait(hg_read, (i - 1) & 1);  // every row thread has read g's third part: the scaled dY takes its place
             const uint32_t yb = sb + (i & 1 ? kY1 : kY);
             uint4 xr[4];  // x, this half's 32 columns
-            float ri = 0.f;
+            float ri = 0.f, hg = 0.f;
             if (ok) {
                 uint4 yr[4];
                 F2 dd2 = f2(0.f, 0.f);
@@ -403,6 +461,10 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                     }
                 }
                 sums.dD[half][row] = get(dd2).x + get(dd2).y;
+                // <h, g'> (this thread's 32 elements): h's third part, while P is not in its place yet
+                wait(h2_full, i & 1);
+                wait(g_full, i & 1);
+                if (ok) hg = dot_elements<K>(sb + kH2, sb + kG, tid);
                 wait(ch_full, i & 1);
                 tc_fence_after();
                 float v[32];
@@ -452,10 +514,8 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                     if (k > wr || !ok) {  // right of the diagonal
 #pragma unroll
                         for (int j = 0; j < 16; ++j) w[b][j] = 0.f;
-                        if (i == 0) {
-                            st_shared_v4(at[0], 0u, 0u, 0u, 0u);
-                            st_shared_v4(at[1], 0u, 0u, 0u, 0u);
-                        }
+                        st_shared_v4(at[0], 0u, 0u, 0u, 0u);
+                        st_shared_v4(at[1], 0u, 0u, 0u, 0u);
                         continue;
                     }
                     uint32_t sr[16], vr[16];
@@ -518,6 +578,23 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
                     const float2 rs = get(rs2);
                     sums.rsum[k][half][row] = rs.x + rs.y;
                 }
+                if (ok && kp == wr >> 1) {  // the diagonal block: this row's part of what crosses each column, over the rows from it on
+                    const float4 *dl = reinterpret_cast<const float4 *>(vec.delta + 32 * wr + 16 * half);
+                    float cross[16], before = 0.f;
+#pragma unroll
+                    for (int j4 = 0; j4 < 4; ++j4) {
+                        const float4 d4 = dl[j4];
+                        const float d[4] = {d4.x, d4.y, d4.z, d4.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int j = 4 * j4 + e;
+                            cross[j] = 16 * half + j <= lane ? before : 0.f;
+                            before = fmaf(wr & 1 ? w[1][j] : w[0][j], d[e], before);
+                        }
+                    }
+                    const float x = lane_sums(cross, lane);
+                    if (!(lane & 1)) sums.cross[32 * wr + 16 * half + (lane >> 1)] = x;
+                }
                 if (2 * kp <= wr) {
                     const float cs = lane_sums(w[0], w[1], lane);
                     sums.csum[wr][64 * kp + 32 * (lane >> 4) + 16 * half + (lane & 15)] = cs;
@@ -527,10 +604,10 @@ scan_grad_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant
             tc_fence_before();
             mbar_arrive(p_ready);
             fetch(i + 1);
-            // ---- <h, g'> (this thread's 32 elements)
-            float hg = 0.f;
-            wait(g_full, i & 1);
+            // ---- <h, g'>: g's third part (behind the scaled dY), then the first two of both
+            wait(g2_full, i & 1);
             if (ok) {
+                hg += dot_elements<K>(sb + kH, sb + kG2, tid);
 #pragma unroll
                 for (int j = 0; j < K * kPT / 8 / kRowThreads; ++j) {
                     const uint32_t at = (j * kRowThreads + tid) * 16;
@@ -667,38 +744,40 @@ __global__ void __launch_bounds__(kC) scan_gate_grad_kernel(const Params p, cons
     const float delta = p.gates.at(blockIdx.x, p.H, h)[row];
     float before, after, all;
     around(p.gates.totals(blockIdx.x, p.H, h), wr, &before, &after, &all);
-    // strictly lower W: sums of this token's row left of its block, of its column below it, and of both
-    // inside it
-    float rs[4] = {}, coff = 0.f, cd = 0.f, rw = 0.f, bt = 0.f, wd = 0.f, dD = 0.f, hg = 0.f;
+    // strictly lower W: sums of this token's row left of its block (rs), of its column below it (coff) and inside
+    // it (cd), of its row's first half inside it (left)
+    float rs[4] = {}, coff = 0.f, cd = 0.f, rw = 0.f, bt = 0.f, wd = 0.f, dD = 0.f, hg = 0.f, cross = 0.f, left = 0.f;
     for (int k = 0; k < p.S; ++k) {
         const Sums &s = sums[((size_t)blockIdx.x * p.H + h) * p.S + k];
         rw += s.rowi[0][row] + s.rowi[1][row];
         bt += s.bt[0][row] + s.bt[1][row];
         dD += s.dD[0][row] + s.dD[1][row];
         wd += s.wdiag[row];
+        cross += s.cross[row], left += s.rsum[wr][0][row];
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            if (w <= wr) rs[w] += s.rsum[w][0][row] + s.rsum[w][1][row];
+            if (w < wr) rs[w] += s.rsum[w][0][row] + s.rsum[w][1][row];
             if (w == wr) cd += s.csum[w][row];
             if (w > wr) coff += s.csum[w][row];
         }
         if (lane < 8) hg += s.hg[lane];
     }
-    float roff = 0.f, rd = 0.f;
+    float roff = 0.f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < 4; ++w)
         if (w < wr) roff += rs[w];
-        if (w == wr) rd = rs[w];
-    }
     hg = warp_sum(hg);
-    float suf = rw + roff + rd - delta * cd, pre = delta * (bt + coff);
+    float suf = rw + roff, pre = delta * (bt + coff);  // rows from t on, columns up to it
     const float pre_own = pre;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const float a = __shfl_down_sync(0xffffffffu, suf, o), b = __shfl_up_sync(0xffffffffu, pre, o);
-        if (lane + o < 32) suf += a;
+        const float c = __shfl_down_sync(0xffffffffu, left, o);
+        if (lane + o < 32) suf += a, left += c;
         if (lane >= o) pre += b;
     }
+    // inside the block: `cross`, and for its second half of columns the rows' first halves
+    suf += lane >= 16 ? cross + left : cross;
     const float t_ri = warp_sum(rw), t_bt = warp_sum(delta * bt), r0 = warp_sum(wr > 0 ? rs[0] : 0.f), r1 = warp_sum(wr > 1 ? rs[1] : 0.f);
     if (lane == 0) tot[wr][0] = t_ri, tot[wr][1] = t_bt, tot[wr][2] = r0, tot[wr][3] = r1;
     __syncthreads();
@@ -764,7 +843,7 @@ cudaError_t run(const ScanArgs &a, const Gates &gates, const Tiles &h, const Til
     GradP q{};
     q.p = params(a, gates);
     q.run = units_per_cta(a), q.runs = runs_of(a);
-    q.h_hi = h.hi, q.h_lo = h.lo, q.g_hi = gr.hi, q.g_lo = gr.lo;
+    q.h = h, q.g = gr;
     q.dx = (__nv_bfloat16 *)a.dx, q.dB = (__nv_bfloat16 *)a.dB, q.dC = (__nv_bfloat16 *)a.dC;
     const int slots = a.seq.total ? a.seq.slots(kC) : 0;
     float *part = (float *)ws;

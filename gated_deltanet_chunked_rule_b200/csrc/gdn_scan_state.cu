@@ -246,18 +246,7 @@ scan_state_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constan
             if (!keeps) return;
             const size_t at = ((slot0 + chunk_at(i)) * units + unit) * (K * kPT) + (size_t)(c0 / 8) * K * 8 + row * 8;
 #pragma unroll
-            for (int b = 0; b < kHalf / 8; ++b) {
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float x0 = st[8 * b + 2 * j], x1 = st[8 * b + 2 * j + 1];
-                    hi[j] = pack_bf16(x0, x1);
-                    if (q.tiles.lo) lo[j] = pack_bf16(x0 - bf_lo(hi[j]), x1 - bf_hi(hi[j]));
-                }
-                *reinterpret_cast<uint4 *>(q.tiles.hi + at + (size_t)b * K * 8) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                if (q.tiles.lo)
-                    *reinterpret_cast<uint4 *>(q.tiles.lo + at + (size_t)b * K * 8) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            }
+            for (int b = 0; b < kHalf / 8; ++b) store_parts(q.tiles, at + (size_t)b * K * 8, st + 8 * b);
         };
         keep(0);
         // this token's gates of chunk i: what Xs is scaled by, and the chunk's whole decay (log2)
@@ -462,15 +451,7 @@ scan_chunks_kernel(Params p, const float *__restrict__ products, const float *__
         for (int j = 0; j < kAhead; ++j) {
             const int i = i0 + j;
             if (i >= chunks) break;
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                hi[k] = pack_bf16(st[2 * k], st[2 * k + 1]);
-                lo[k] = pack_bf16(st[2 * k] - bf_lo(hi[k]), st[2 * k + 1] - bf_hi(hi[k]));
-            }
-            const size_t at = (slot(i) * units + unit) * (K * kPT) + ((size_t)c8 * K + row) * 8;
-            *reinterpret_cast<uint4 *>(tiles.hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            if (tiles.lo) *reinterpret_cast<uint4 *>(tiles.lo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            store_parts(tiles, (slot(i) * units + unit) * (K * kPT) + ((size_t)c8 * K + row) * 8, st);
             const float d = ex2((t[j].x + t[j].y) + (t[j].z + t[j].w));
             const float v[8] = {a[j].x, a[j].y, a[j].z, a[j].w, b[j].x, b[j].y, b[j].z, b[j].w};
 #pragma unroll

@@ -11,7 +11,7 @@
 //
 // A "unit" is a head's slice of 64 state columns; unit u of group g is slice u % S of head
 // g (H/G) + u / S, S = P/64. Per chunk slot and unit the state kernel keeps the entry state
-// (forward) or exit gradient (reverse) as two bf16 tiles hi + lo in a blocked layout: 8-column
+// (forward) or exit gradient (reverse) as three bf16 tiles hi + lo + lo2 in a blocked layout: 8-column
 // blocks of 16-byte rows, element (k, p) at (p/8) * K*16 + k*16 + (p%8)*2, which a lane-per-row
 // store writes contiguously and tcgen05 reads without swizzle along either axis.
 #pragma once
@@ -104,11 +104,11 @@ __device__ __forceinline__ void around(const float4 &t, int w, float *before, fl
     *before = lo, *after = hi, *all = (a[0] + a[1]) + (a[2] + a[3]);
 }
 
-// Per-chunk tiles: hi, then lo, of every (chunk slot, unit).
+// Per-chunk tiles of every (chunk slot, unit): bf16 parts that together hold an fp32 element's 24 bits.
 struct Tiles {
-    __nv_bfloat16 *hi, *lo;  // lo nullable
+    __nv_bfloat16 *hi, *lo, *lo2;  // lo and lo2 both null: hi alone
 };
-inline size_t tile_bytes(const ScanArgs &a) {  // of hi (or lo)
+inline size_t tile_bytes(const ScanArgs &a) {  // of one part
     return (size_t)a.seq.slots(kC) * a.H * (a.P / kPT) * a.K * kPT * 2;
 }
 
@@ -170,6 +170,29 @@ __device__ __forceinline__ bool drain(uint64_t *bar, uint32_t parity) {
 
 __device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+// What is left of two values beside their bf16 part.
+__device__ __forceinline__ uint32_t split(float &x0, float &x1) {
+    const uint32_t part = pack_bf16(x0, x1);
+    x0 -= bf_lo(part), x1 -= bf_hi(part);
+    return part;
+}
+
+// Eight consecutive columns of a state row as tile parts, at element `at`.
+__device__ __forceinline__ void store_parts(const Tiles &t, size_t at, const float *v) {
+    uint32_t hi[4], lo[4], lo2[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float x0 = v[2 * j], x1 = v[2 * j + 1];
+        hi[j] = split(x0, x1);
+        if (t.lo) lo[j] = split(x0, x1), lo2[j] = pack_bf16(x0, x1);
+    }
+    *reinterpret_cast<uint4 *>(t.hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    if (t.lo) {
+        *reinterpret_cast<uint4 *>(t.lo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<uint4 *>(t.lo2 + at) = make_uint4(lo2[0], lo2[1], lo2[2], lo2[3]);
+    }
+}
 
 // Launchers of the kernels (see the .cu files).
 // State pass over the chunks: REVERSE walks them backwards with C and dY in place of B and x.

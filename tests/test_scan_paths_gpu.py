@@ -169,6 +169,25 @@ def test_gate_gradients_on_cuda_cores_add_up(gdn, monkeypatch, dtype, impl, lens
         assert off <= 24 * 2.0 ** -24, k
 
 
+@pytest.mark.parametrize("K,P", [(128, 64), (64, 128), (128, 128)])
+@pytest.mark.parametrize("lens", [[2] * 12, [40, 60], [300, 128], [1500]])
+def test_gate_gradients_on_tensor_cores_add_up(gdn, K, P, lens):
+    """The same of the tensor-core kernels, between states as large as the tokens' own: their products are exact ones of
+    bf16 values and of states in 24 bits, summed in fp32. 24 2^-24 as above, and three decays by exponentials of 2^-22
+    each in a term."""
+    v = S.make(lens, 32, 4, K, P, torch.bfloat16, torch.float32, seed=len(lens) + K)
+    g = torch.Generator().manual_seed(5)
+    v["A"] = -(1 + 15 * torch.rand(32, generator=g)).cuda()
+    v["dt_bias"] = (-7 + 5 * torch.rand(32, generator=g)).cuda()
+    ref, _ = S.reference(v, lens, True)
+    for save in (True, False):
+        got = S.train(gdn, v, save=save)
+        for k in ("dA", "ddt_bias"):
+            off = ((got[k].cpu().double() - ref[k]).norm() / ref[k].norm()).item()
+            print(k, f"{off:.2e}")
+            assert off <= (24 + 12) * 2.0 ** -24, k
+
+
 def chunked(v, lens):
     """The scan in 64 bits on the GPU in chunks of 64 tokens, the state carried from chunk to chunk."""
     x, dt, A, B, C, D, bias = (t.double() if t is not None else None for t in S.args(v))
