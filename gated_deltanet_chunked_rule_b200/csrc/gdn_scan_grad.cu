@@ -18,7 +18,7 @@
 // products and states in three bf16 parts, 24 bits; sums of the crossing pairs run forward or
 // backward and nothing is taken off again (inside a 32 x 32 diagonal block: a prefix over the columns, summed
 // over the rows from each column on). Two parts, and row minus column sums inside the blocks, left dA and the
-// bias off by 1e-6 to 4e-6 of their norm; 2e-7 to 1e-6 now, for 15 us of this kernel's and 14 of the state
+// bias off by 1e-6 to 4e-6 of their norm; 2e-7 to 1e-6 now, for 17 us of this kernel's and 10 of the state
 // kernels' (2 x 4096 tokens, 16 heads of 128). bf16 results take one rounded operand per
 // term: L o S and the scaled rows; the summed L o Q o delta is cut in two bf16 parts, its products being taken only
 // once (0.6 us; with one, dB and dC came out at 2.3e-3 and up to 2.6e-3 of their norm, half as much again as

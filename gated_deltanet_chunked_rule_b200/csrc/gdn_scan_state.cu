@@ -27,7 +27,8 @@
 // from L2. Beyond that size the products would go through memory twice, and instead a first pass
 // takes every segment from a zero state, one small kernel composes the segments' starts (their
 // operator is one scalar decay), and a second pass walks them again. 2 x 4096 tokens, 16 heads of
-// 128 (67 MB of products): 26 + 22 us against 25 + 10 + 29. A forward that keeps nothing needs no second
+// 128 (67 MB of products): 26 + 22 us against 25 + 10 + 29 (with two parts kept of each state; three
+// now: 26 + 27). A forward that keeps nothing needs no second
 // pass: the tiles of the first one, the segments' starts and one factor per chunk are enough for
 // the outputs (8192 tokens, 64 heads: 40 us less of 162).
 #include <algorithm>
