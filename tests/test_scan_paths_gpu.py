@@ -216,8 +216,8 @@ def chunked(v, lens):
 def test_long_sequences(gdn, monkeypatch, dtype, T, H, split):
     """Of norms. bf16 results: half a step, 2^-8, for the rounding of the result and of one operand in each of its
     two terms. fp32 results: the operations in sequence, whose roundings are independent, sqrt(T + 512 + 17 * 128)
-    2^-24, and 2^-16 for two-part operands; the gates' gradients pass through four such results (kept states, exit
-    gradients, their product, the sum)."""
+    2^-24, and 2^-16 for operands cut into bf16 parts (two at least); the gates' gradients pass through four such results
+    (kept states, exit gradients, their product, the sum)."""
     if split:
         monkeypatch.setenv("GDN_SCAN_SPLIT", split)
     v = S.make([T], H, 1, 128, 64, DT[dtype], torch.float32, seed=T + H, slow=True)
